@@ -17,26 +17,28 @@ int *g_status[kMaxDevices] = {nullptr};
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-bool valid_mask_kind(int k) { return k >= FLEX_MASK_CAUSAL && k <= FLEX_MASK_ALL; }
+bool valid_mask_kind(int k) { return k >= FLEX_MASK_CAUSAL && k <= FLEX_MASK_WINDOW_SINKS; }
+
+bool takes_params(int kind) {
+    return kind == FLEX_MASK_SLIDING_WINDOW || kind == FLEX_MASK_CAUSAL_PREFIX || kind == FLEX_MASK_DOCUMENT ||
+           kind == FLEX_MASK_WINDOW_SINKS;
+}
+
+}  // namespace
+
+// Sliding window: W >= 0; window + sinks: W >= 0 and a count of sinks >= 0.
+bool valid_window(int kind, const flex_mask_params &prm) {
+    if (kind == FLEX_MASK_SLIDING_WINDOW) return prm.window >= 0;
+    return kind != FLEX_MASK_WINDOW_SINKS || (prm.window >= 0 && prm.prefix >= 0);
+}
+
+namespace {
 
 int check_sizes(int32_t B, int32_t H, int32_t q_len, int32_t kv_len, int32_t q_block, int32_t kv_block) {
     if (B <= 0 || H <= 0 || q_len <= 0 || kv_len <= 0 || q_block <= 0 || kv_block <= 0) return FLEX_ERR_INVALID_ARG;
     if (!valid_block_size(q_block) || !valid_block_size(kv_block)) return FLEX_ERR_UNSUPPORTED;
     if (ceil_blocks(kv_len) > kMaxKvBlocks) return FLEX_ERR_UNSUPPORTED;
     if (B > 65535 || H > 65535) return FLEX_ERR_UNSUPPORTED;
-    return FLEX_OK;
-}
-
-int check_tensor(const flex_tensor *t, int dtype, int64_t B, int64_t H, int64_t S, int64_t D) {
-    if (!t || !t->data) return FLEX_ERR_INVALID_ARG;
-    if (t->dtype != dtype) return FLEX_ERR_INVALID_ARG;
-    if (t->shape[0] != B || t->shape[1] != H || t->shape[2] != S || t->shape[3] != D) return FLEX_ERR_SHAPE;
-    if (t->stride[3] != 1) return FLEX_ERR_ALIGNMENT;
-    const int64_t elem = dtype == FLEX_DTYPE_BF16 ? 2 : 4;
-    for (int i = 0; i < 3; ++i)
-        if (t->stride[i] <= 0 || (t->stride[i] * elem) % 16 != 0 || t->stride[i] * elem >= (int64_t(1) << 40))
-            return FLEX_ERR_ALIGNMENT;
-    if (!aligned16(t->data)) return FLEX_ERR_ALIGNMENT;
     return FLEX_OK;
 }
 
@@ -76,7 +78,7 @@ int prepare_attention(const flex_tensor *q, const flex_tensor *k, const flex_ten
     if (bm->mask_kind == FLEX_MASK_DOCUMENT && Sq != Skv) return FLEX_ERR_SHAPE;
     // each kv tile's document ids are bulk-copied as whole 16-byte words
     if (bm->mask_kind == FLEX_MASK_DOCUMENT && Sq % 4 != 0) return FLEX_ERR_UNSUPPORTED;
-    if (bm->mask_kind == FLEX_MASK_SLIDING_WINDOW && bm->params.window < 0) return FLEX_ERR_INVALID_ARG;
+    if (!valid_window(bm->mask_kind, bm->params)) return FLEX_ERR_INVALID_ARG;
     if (B * H * ((ceil_blocks(Sq) + 1) / 2) > INT32_MAX) return FLEX_ERR_UNSUPPORTED;
 
     p.B = (int)B;
@@ -122,6 +124,19 @@ cudaError_t launch_attention(const AttnProblem &p, int dtype, cudaStream_t s) {
 }
 
 }  // namespace
+
+int check_tensor(const flex_tensor *t, int dtype, int64_t B, int64_t H, int64_t S, int64_t D) {
+    if (!t || !t->data) return FLEX_ERR_INVALID_ARG;
+    if (t->dtype != dtype) return FLEX_ERR_INVALID_ARG;
+    if (t->shape[0] != B || t->shape[1] != H || t->shape[2] != S || t->shape[3] != D) return FLEX_ERR_SHAPE;
+    if (t->stride[3] != 1) return FLEX_ERR_ALIGNMENT;
+    const int64_t elem = dtype == FLEX_DTYPE_BF16 ? 2 : 4;
+    for (int i = 0; i < 3; ++i)
+        if (t->stride[i] <= 0 || (t->stride[i] * elem) % 16 != 0 || t->stride[i] * elem >= (int64_t(1) << 40))
+            return FLEX_ERR_ALIGNMENT;
+    if (!aligned16(t->data)) return FLEX_ERR_ALIGNMENT;
+    return FLEX_OK;
+}
 
 int *device_status_word(int *err) {
     int dev = 0;
@@ -263,8 +278,8 @@ int flex_block_mask_create_qkv(int32_t mask_kind, const flex_mask_params *params
         return FLEX_ERR_INVALID_ARG;
     flex_mask_params prm = {0, 0, nullptr};
     if (params) prm = *params;
-    if (mask_kind == FLEX_MASK_SLIDING_WINDOW && (!params || prm.window < 0)) return FLEX_ERR_INVALID_ARG;
-    if (mask_kind == FLEX_MASK_CAUSAL_PREFIX && !params) return FLEX_ERR_INVALID_ARG;
+    if (takes_params(mask_kind) && !params) return FLEX_ERR_INVALID_ARG;
+    if (!valid_window(mask_kind, prm)) return FLEX_ERR_INVALID_ARG;
     if (mask_kind == FLEX_MASK_DOCUMENT) {
         if (!params || !prm.doc_ids) return FLEX_ERR_INVALID_ARG;
         if (q_len != kv_len) return FLEX_ERR_SHAPE;
@@ -448,9 +463,8 @@ int flex_attention_fwd_host(const flex_tensor *q, const flex_tensor *k, const fl
     if (!is_contiguous(q) || !is_contiguous(k) || !is_contiguous(v)) return FLEX_ERR_INVALID_ARG;
     if (!valid_mask_kind(mask_kind)) return FLEX_ERR_INVALID_ARG;
     const bool doc = mask_kind == FLEX_MASK_DOCUMENT;
-    if ((mask_kind == FLEX_MASK_SLIDING_WINDOW || mask_kind == FLEX_MASK_CAUSAL_PREFIX || doc) && !params)
-        return FLEX_ERR_INVALID_ARG;
-    if (mask_kind == FLEX_MASK_SLIDING_WINDOW && params->window < 0) return FLEX_ERR_INVALID_ARG;
+    if (takes_params(mask_kind) && !params) return FLEX_ERR_INVALID_ARG;
+    if (params && !valid_window(mask_kind, *params)) return FLEX_ERR_INVALID_ARG;
     if (doc && (!params->doc_ids || !dev->doc_ids)) return FLEX_ERR_INVALID_ARG;
     if (doc && !aligned16(dev->doc_ids)) return FLEX_ERR_ALIGNMENT;
     const int64_t B64 = q->shape[0], H64 = q->shape[1], Sq64 = q->shape[2], Skv64 = k->shape[2];

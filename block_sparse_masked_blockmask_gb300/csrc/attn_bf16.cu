@@ -79,6 +79,9 @@ cudaError_t launch_attn_bf16(const AttnProblem &p, cudaStream_t stream) {
     kp.lse = p.lse;
     kp.row_max = p.row_max;
     kp.status = p.status;
+    if (mask_class(p.mask.kind) == kMaskSinks)
+        return p.D == 64 ? launch_bf16_sinks_d64(tq, tk, tv, kp, p.score_kind, stream)
+                         : launch_bf16_sinks_d128(tq, tk, tv, kp, p.score_kind, stream);
     return p.D == 64 ? launch_bf16_d64(tq, tk, tv, kp, p.score_kind, stream)
                      : launch_bf16_d128(tq, tk, tv, kp, p.score_kind, stream);
 }

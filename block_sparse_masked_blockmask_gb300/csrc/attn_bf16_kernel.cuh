@@ -330,6 +330,18 @@ __device__ __forceinline__ void apply_interval_mask(const MaskDesc &m, int q, in
         x2[j] = keep_pair(x2[j], 2 * j >= clo && 2 * j <= chi, 2 * j + 1 >= clo && 2 * j + 1 <= chi);
 }
 
+// Window + sinks: columns up to sink_hi or in [lo, q] (mask_row_sinks), and
+// nothing at or past KV_LEN.
+__device__ __forceinline__ void apply_sinks_mask(const MaskDesc &m, int q, int kv0, uint64_t (&x2)[64]) {
+    int sink_hi, lo;
+    mask_row_sinks(m, q, sink_hi, lo);
+    const int csink = min(sink_hi, m.kv_len - 1) - kv0, clo = lo - kv0, chi = min(q, m.kv_len - 1) - kv0;
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+        x2[j] = keep_pair(x2[j], 2 * j <= csink || (2 * j >= clo && 2 * j <= chi),
+                          2 * j + 1 <= csink || (2 * j + 1 >= clo && 2 * j + 1 <= chi));
+}
+
 // Document mask_mod: same document id (the tile's ids staged in shared
 // memory) and kv <= q.
 __device__ __forceinline__ void apply_document_mask(int q, int kv0, int doc_q, const int32_t *tile_doc,
@@ -473,8 +485,10 @@ __device__ __forceinline__ void build_item(const Bf16Params &p, AttnMisc &ms, It
     __syncwarp();
 }
 
-// DOC: the BlockMask's mask_mod is the document mask (its partial tiles read
-// per-tile document ids staged next to V); other kinds are interval masks.
+// MASKC: the BlockMask's mask class (mask_class).  Document masks read per-tile
+// document ids staged next to V on their partial tiles; window + sinks masks
+// test two column intervals there and, unlike the older kinds, sum the row's
+// weights before their rounding to bf16 (see the softmax loop).
 // BLOCKS128: the BlockMask's blocks are 128 x 128 (else any Q_BLOCK, KV_BLOCK,
 // read as 128-tiles when the scheduler builds an item).
 //
@@ -484,12 +498,13 @@ __device__ __forceinline__ void build_item(const Bf16Params &p, AttnMisc &ms, It
 // union list, Q tiles and first K/V tiles load while the current item
 // computes.  Every role walks the same sequence of published items; all
 // barrier phases (K/V ring, S/P hand-off, Q, O) continue across items.
-template <int D, int SCORE, bool DOC, bool BLOCKS128>
+template <int D, int SCORE, int MASKC, bool BLOCKS128>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_bf16_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const Bf16Params p) {
     using C = Bf16Cfg<D>;
     constexpr int NS = C::kStages;
+    constexpr bool DOC = MASKC == kMaskDocument, SINKS = MASKC == kMaskSinks;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     AttnMisc &ms = *reinterpret_cast<AttnMisc *>(smem + C::kMiscOff);
@@ -1034,6 +1049,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             break;
                         }
                         apply_document_mask(q, kv0, doc_q, ms.stage_doc[stage], x2);
+                    } else if constexpr (SINKS) {
+                        apply_sinks_mask(p.mask, q, kv0, x2);
                     } else {
                         apply_interval_mask(p.mask, q, kv0, x2);
                     }
@@ -1091,21 +1108,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 };
                 // the row sum takes the bf16 weights the PV MMA reads, so
-                // each row's weights sum to l exactly
+                // each row's weights sum to l exactly; window + sinks rows,
+                // which may be short however long the sequence, sum the
+                // unrounded weights, so that lse keeps float32 accuracy (the
+                // rounded ones leave it 3e-5 off at a window of 256)
                 float rsum4[4] = {0.f, 0.f, 0.f, 0.f};
+                uint64_t rsum2[2] = {0, 0};
+                auto weights = [&](int j) {
+                    float d0, d1;
+                    f2_unpack(x2[j], d0, d1);
+                    d0 = ex2_approx(d0);
+                    d1 = ex2_approx(d1);
+                    if constexpr (SINKS) rsum2[j & 1] = f2_add(rsum2[j & 1], f2_pack(d0, d1));
+                    return pack_bf16x2(d0, d1);
+                };
                 if constexpr (C::kSepP) {
                     // all of P in registers first; P_i and O_i are written
                     // once the previous PV MMA of this tile has read P_i and
                     // accumulated into O_i
                     uint32_t pk[64];
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
-                        float d0, d1;
-                        f2_unpack(x2[j], d0, d1);
-                        pk[j] = pack_bf16x2(ex2_approx(d0), ex2_approx(d1));
-                    }
+                    for (int j = 0; j < 64; ++j) pk[j] = weights(j);
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) add_bf16x2_to_f32(rsum4[2 * (j & 1)], rsum4[2 * (j & 1) + 1], pk[j]);
+                    for (int j = 0; j < (SINKS ? 0 : 64); ++j) add_bf16x2_to_f32(rsum4[2 * (j & 1)], rsum4[2 * (j & 1) + 1], pk[j]);
                     if (cnt_total > 0 && !warp_wait(&ms.pv_done[i], (cnt_total - 1) & 1u, abort_flag)) {
                         ok = false;
                         break;
@@ -1121,21 +1146,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int gq = 0; gq < 4; ++gq) {
                         uint32_t pk[16];
 #pragma unroll
-                        for (int t2 = 0; t2 < 16; ++t2) {
-                            const int j = 16 * gq + t2;
-                            float d0, d1;
-                            f2_unpack(x2[j], d0, d1);
-                            pk[t2] = pack_bf16x2(ex2_approx(d0), ex2_approx(d1));
-                        }
+                        for (int t2 = 0; t2 < 16; ++t2) pk[t2] = weights(16 * gq + t2);
                         tmem_st16(p_addr + 16 * gq, pk);
 #pragma unroll
-                        for (int t2 = 0; t2 < 16; ++t2)
+                        for (int t2 = 0; t2 < (SINKS ? 0 : 16); ++t2)
                             add_bf16x2_to_f32(rsum4[2 * (t2 & 1)], rsum4[2 * (t2 & 1) + 1], pk[t2]);
                     }
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
                 mbar_arrive(&ms.p_full[i]);
+                if constexpr (SINKS) {
+                    f2_unpack(rsum2[0], rsum4[0], rsum4[1]);
+                    f2_unpack(rsum2[1], rsum4[2], rsum4[3]);
+                }
                 const float rsum = (rsum4[0] + rsum4[1]) + (rsum4[2] + rsum4[3]);
                 l_run = fmaf(l_run, alpha, rsum);
                 ++cnt;

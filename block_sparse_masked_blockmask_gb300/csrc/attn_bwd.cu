@@ -40,6 +40,11 @@
 #include "tilelist.cuh"
 
 namespace flex {
+
+// compiled in attn_bwd_fp32_sinks.cu
+extern template cudaError_t launch_bwd_fp32_tc_dkdv<true>(const AttnProblem &, const BwdF32TcArgs &, cudaStream_t);
+extern template cudaError_t launch_bwd_fp32_tc_dq<true>(const AttnProblem &, const BwdF32TcArgs &, cudaStream_t);
+
 namespace {
 
 constexpr int kTRows = 64;       // owned rows per CTA, walked rows per step
@@ -206,7 +211,7 @@ __device__ __forceinline__ void store_rows(float *dst, int row0, int len, int ta
 
 // dK, dV (fp32): CTA = 64 kv rows of one kv block; the q blocks come from the
 // transposed lists, each walked in two steps of 64 q rows.
-template <int D, int SCORE>
+template <int D, int SCORE, bool SINKS>
 __global__ void __launch_bounds__(kTThreads, D == 64 ? 2 : 1) attn_bwd_dkdv_kernel(AttnProblem p, BwdArgs a) {
     using C = TiledCfg<D>;
     extern __shared__ float4 smem4[];
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kTThreads, D == 64 ? 2 : 1) attn_bwd_dkdv_kern
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int kv = kv0 + 4 * ta + i;
-                    const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_mod(p.mask, b, q, kv)));
+                    const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_keep<SINKS>(p.mask, b, q, kv)));
                     float pr = 0.f, dts = 0.f;
                     if (keep) {
                         float grad;
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(kTThreads, D == 64 ? 2 : 1) attn_bwd_dkdv_kern
 
 // dQ (fp32): CTA = 64 q rows of one q block; the kv tiles come from the kv
 // side of the BlockMask, as in the forward pass, each walked in two steps.
-template <int D, int SCORE>
+template <int D, int SCORE, bool SINKS>
 __global__ void __launch_bounds__(kTThreads, D == 64 ? 2 : 1) attn_bwd_dq_kernel(AttnProblem p, BwdArgs a) {
     using C = TiledCfg<D>;
     extern __shared__ float4 smem4[];
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(kTThreads, D == 64 ? 2 : 1) attn_bwd_dq_kernel
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int kv = kv0 + tw + 16 * j;
-                    const bool keep = lse[i] != -INFINITY && (full || (kv < p.kv_len && mask_mod(p.mask, b, q, kv)));
+                    const bool keep = lse[i] != -INFINITY && (full || (kv < p.kv_len && mask_keep<SINKS>(p.mask, b, q, kv)));
                     float dts = 0.f;
                     if (keep) {
                         float grad;
@@ -426,13 +431,13 @@ __global__ void __launch_bounds__(128) block_mask_transpose_kernel(const int32_t
     }
 }
 
-template <int D, int SCORE>
+template <int D, int SCORE, bool SINKS>
 cudaError_t launch_bwd_fp32_score(const AttnProblem &p, const BwdArgs &a, bool dkdv, bool dq, cudaStream_t stream) {
     using C = TiledCfg<D>;
     cudaError_t e =
-        cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, SCORE, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attn_bwd_dq_kernel<D, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attn_bwd_dq_kernel<D, SCORE, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)C::kSmem);
     if (e != cudaSuccess) return e;
     // grid.y holds at most 65535 (b, h) pairs per launch
@@ -441,11 +446,11 @@ cudaError_t launch_bwd_fp32_score(const AttnProblem &p, const BwdArgs &a, bool d
         part.bh_begin = begin;
         const int count = p.B * p.H - begin < 65535 ? p.B * p.H - begin : 65535;
         if (dkdv) {
-            attn_bwd_dkdv_kernel<D, SCORE><<<dim3(2 * p.nkvt, count), kTThreads, C::kSmem, stream>>>(part, a);
+            attn_bwd_dkdv_kernel<D, SCORE, SINKS><<<dim3(2 * p.nkvt, count), kTThreads, C::kSmem, stream>>>(part, a);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
         if (dq) {
-            attn_bwd_dq_kernel<D, SCORE><<<dim3(2 * p.nqt, count), kTThreads, C::kSmem, stream>>>(part, a);
+            attn_bwd_dq_kernel<D, SCORE, SINKS><<<dim3(2 * p.nqt, count), kTThreads, C::kSmem, stream>>>(part, a);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
     }
@@ -513,7 +518,7 @@ cudaError_t launch_dkdv_dq(cudaStream_t stream, DkDv &&dkdv, Dq &&dq) {
 // fp32: delta, then dK/dV and dQ on the tensor cores (three-way bf16 split);
 // dK/dV of a q side longer than kBwdF32TcMaxQTiles tiles falls to the
 // register-tiled CUDA-core kernel.
-template <int D>
+template <int D, bool SINKS>
 cudaError_t launch_bwd_fp32(const AttnProblem &p, const BwdArgs &a, cudaStream_t stream) {
     const int64_t rows = (int64_t)p.B * p.H * p.q_len;
     attn_bwd_delta_kernel<D, float><<<(unsigned)((rows * 32 + 255) / 256), 256, 0, stream>>>(p, a, rows);
@@ -521,20 +526,20 @@ cudaError_t launch_bwd_fp32(const AttnProblem &p, const BwdArgs &a, cudaStream_t
     if (e != cudaSuccess) return e;
     const BwdF32TcArgs ta{static_cast<const float *>(a.dout), a.delta, a.q_num, a.q_idx, a.fq_num, a.fq_idx,
                           static_cast<float *>(a.dk), static_cast<float *>(a.dv), static_cast<float *>(a.dq)};
-    auto dq = [&](cudaStream_t s) { return launch_bwd_fp32_tc_dq(p, ta, s); };
+    auto dq = [&](cudaStream_t s) { return launch_bwd_fp32_tc_dq<SINKS>(p, ta, s); };
     if (p.nqt <= kBwdF32TcMaxQTiles)
-        return launch_dkdv_dq(stream, [&](cudaStream_t s) { return launch_bwd_fp32_tc_dkdv(p, ta, s); }, dq);
+        return launch_dkdv_dq(stream, [&](cudaStream_t s) { return launch_bwd_fp32_tc_dkdv<SINKS>(p, ta, s); }, dq);
     // dK/dV of a longer q side on the CUDA cores
     return launch_dkdv_dq(
         stream,
         [&](cudaStream_t s) {
             switch (p.score_kind) {
                 case FLEX_SCORE_SOFTCAP:
-                    return launch_bwd_fp32_score<D, FLEX_SCORE_SOFTCAP>(p, a, true, false, s);
+                    return launch_bwd_fp32_score<D, FLEX_SCORE_SOFTCAP, SINKS>(p, a, true, false, s);
                 case FLEX_SCORE_ALIBI:
-                    return launch_bwd_fp32_score<D, FLEX_SCORE_ALIBI>(p, a, true, false, s);
+                    return launch_bwd_fp32_score<D, FLEX_SCORE_ALIBI, SINKS>(p, a, true, false, s);
                 default:
-                    return launch_bwd_fp32_score<D, FLEX_SCORE_IDENTITY>(p, a, true, false, s);
+                    return launch_bwd_fp32_score<D, FLEX_SCORE_IDENTITY, SINKS>(p, a, true, false, s);
             }
         },
         dq);
@@ -609,7 +614,9 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, int dtype, const void *dout, c
                             void *dv, float *delta, cudaStream_t stream) {
     const BwdArgs a{dout, q_num, q_idx, fq_num, fq_idx, dq, dk, dv, delta};
     if (dtype == FLEX_DTYPE_BF16) return launch_bwd_bf16_tc(p, a, stream);
-    return p.D == 64 ? launch_bwd_fp32<64>(p, a, stream) : launch_bwd_fp32<128>(p, a, stream);
+    if (mask_class(p.mask.kind) == kMaskSinks)
+        return p.D == 64 ? launch_bwd_fp32<64, true>(p, a, stream) : launch_bwd_fp32<128, true>(p, a, stream);
+    return p.D == 64 ? launch_bwd_fp32<64, false>(p, a, stream) : launch_bwd_fp32<128, false>(p, a, stream);
 }
 
 }  // namespace flex

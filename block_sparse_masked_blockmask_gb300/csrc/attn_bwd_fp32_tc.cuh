@@ -175,7 +175,7 @@ __device__ __forceinline__ float score_t(float cap, float t, float slope, int q,
     return t;
 }
 
-template <int SCORE>
+template <int SCORE, bool SINKS>
 __global__ void __launch_bounds__(16 * 32, 1) dkdv_kernel(AttnProblem p, BwdF32TcArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(16 * 32, 1) dkdv_kernel(AttnProblem p, BwdF32T
                 for (int c = 0; c < 32; ++c) {
                     const int q = q0 + 32 * half + c;
                     const float lse = lse_s[32 * half + c];
-                    const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_mod(p.mask, b, q, kv)));
+                    const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_keep<SINKS>(p.mask, b, q, kv)));
                     float grad;
                     const float x = score_t<SCORE>(p.score_param, __uint_as_float(sr[c]) * scale, slope, q, kv, grad);
                     const float pr = keep ? ex2_approx(fmaf(x, kLog2e, -lse * kLog2e)) : 0.f;
@@ -470,7 +470,7 @@ constexpr uint32_t kDqMiscOff = kStage0 + 2 * kDqStageBytes;
 constexpr size_t kDqSmemBytes = kDqMiscOff + sizeof(Misc) + 1024;
 static_assert(kDqSmemBytes <= 232448, "shared memory per CTA");
 
-template <int SCORE>
+template <int SCORE, bool SINKS>
 __global__ void __launch_bounds__(16 * 32, 1) dq_kernel(AttnProblem p, BwdF32TcArgs a, int bh_x) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(16 * 32, 1) dq_kernel(AttnProblem p, BwdF32TcA
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const int kv = kv0 + 32 * half + c;
-                    const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_mod(p.mask, b, q, kv)));
+                    const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_keep<SINKS>(p.mask, b, q, kv)));
                     float grad;
                     const float x = score_t<SCORE>(p.score_param, __uint_as_float(sr[c]) * scale, slope, q, kv, grad);
                     const float pr = ex2_approx(fmaf(x, kLog2e, -lb));
@@ -776,7 +776,7 @@ __device__ __forceinline__ void store64(uint8_t *dst, uint32_t part_bytes, uint3
 }
 }  // namespace d128
 
-template <int SCORE>
+template <int SCORE, bool SINKS>
 __global__ void __launch_bounds__(16 * 32, 1) dq128_kernel(AttnProblem p, BwdF32TcArgs a, int bh_x) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(16 * 32, 1) dq128_kernel(AttnProblem p, BwdF32
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const int kv = kv0 + 32 * half + c;
-                    const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_mod(p.mask, b, q, kv)));
+                    const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_keep<SINKS>(p.mask, b, q, kv)));
                     float grad;
                     const float x = score_t<SCORE>(p.score_param, __uint_as_float(sr[c]) * scale, slope, q, kv, grad);
                     const float pr = ex2_approx(fmaf(x, kLog2e, -lb));
@@ -1097,7 +1097,7 @@ static_assert(dp_slot(1) + 64 == kTmemCols && s_buf(1) + 96 == kTmemCols, "tenso
 static_assert(Role<0>::kSt0 % 1024 == 0 && kStBytes % 1024 == 0, "ring alignment");
 }  // namespace d128kv
 
-template <int SCORE, int ROLE>
+template <int SCORE, int ROLE, bool SINKS>
 __device__ __forceinline__ void dkdv128_role(const AttnProblem &p, const BwdF32TcArgs &a, uint8_t *smem, Misc &ms,
                                              int kvb, int bh, int warp, int lane) {
     namespace c = d128kv;
@@ -1329,7 +1329,7 @@ __device__ __forceinline__ void dkdv128_role(const AttnProblem &p, const BwdF32T
                     for (int cc = 0; cc < 32; ++cc) {
                         const int q = q0 + 32 * half + cc;
                         const float lse = rows_s[32 * half + cc];
-                        const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_mod(p.mask, b, q, kv)));
+                        const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_keep<SINKS>(p.mask, b, q, kv)));
                         float grad;
                         const float x =
                             score_t<SCORE>(p.score_param, __uint_as_float(sr[cc]) * scale, slope, q, kv, grad);
@@ -1350,7 +1350,7 @@ __device__ __forceinline__ void dkdv128_role(const AttnProblem &p, const BwdF32T
                     for (int cc = 0; cc < 32; ++cc) {
                         const int q = q0 + 32 * half + cc;
                         const float lse = rows_s[32 * half + cc];
-                        const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_mod(p.mask, b, q, kv)));
+                        const bool keep = lse != -INFINITY && (full || (kv < p.kv_len && mask_keep<SINKS>(p.mask, b, q, kv)));
                         float grad;
                         const float x =
                             score_t<SCORE>(p.score_param, __uint_as_float(sr[cc]) * scale, slope, q, kv, grad);
@@ -1399,7 +1399,7 @@ __device__ __forceinline__ void dkdv128_role(const AttnProblem &p, const BwdF32T
     }
 }
 
-template <int SCORE>
+template <int SCORE, bool SINKS>
 __global__ void __launch_bounds__(16 * 32, 1) dkdv128_kernel(AttnProblem p, BwdF32TcArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1452,9 +1452,9 @@ __global__ void __launch_bounds__(16 * 32, 1) dkdv128_kernel(AttnProblem p, BwdF
     tc_fence_after_sync();
 
     if (role == 0)
-        dkdv128_role<SCORE, 0>(p, a, smem, ms, kvb, bh, warp, lane);
+        dkdv128_role<SCORE, 0, SINKS>(p, a, smem, ms, kvb, bh, warp, lane);
     else
-        dkdv128_role<SCORE, 1>(p, a, smem, ms, kvb, bh, warp, lane);
+        dkdv128_role<SCORE, 1, SINKS>(p, a, smem, ms, kvb, bh, warp, lane);
 
     // ------------------------------------------------------------ teardown
     tc_fence_before_sync();
@@ -1469,7 +1469,8 @@ __global__ void __launch_bounds__(16 * 32, 1) dkdv128_kernel(AttnProblem p, BwdF
 
 // dK and dV of fp32 inputs on the tensor cores (p.D == 64 or 128; p.nqt <=
 // kBwdF32TcMaxQTiles).
-inline cudaError_t launch_bwd_fp32_tc_dkdv(const AttnProblem &p, const BwdF32TcArgs &a, cudaStream_t stream) {
+template <bool SINKS>
+cudaError_t launch_bwd_fp32_tc_dkdv(const AttnProblem &p, const BwdF32TcArgs &a, cudaStream_t stream) {
     using namespace bwdf32;
     const bool d64 = p.D == 64;
     const size_t smem = d64 ? kSmemBytes : d128kv::kSmemBytes;
@@ -1490,16 +1491,17 @@ inline cudaError_t launch_bwd_fp32_tc_dkdv(const AttnProblem &p, const BwdF32TcA
     };
     switch (p.score_kind) {
         case FLEX_SCORE_SOFTCAP:
-            return d64 ? pick(dkdv_kernel<FLEX_SCORE_SOFTCAP>) : pick(dkdv128_kernel<FLEX_SCORE_SOFTCAP>);
+            return d64 ? pick(dkdv_kernel<FLEX_SCORE_SOFTCAP, SINKS>) : pick(dkdv128_kernel<FLEX_SCORE_SOFTCAP, SINKS>);
         case FLEX_SCORE_ALIBI:
-            return d64 ? pick(dkdv_kernel<FLEX_SCORE_ALIBI>) : pick(dkdv128_kernel<FLEX_SCORE_ALIBI>);
+            return d64 ? pick(dkdv_kernel<FLEX_SCORE_ALIBI, SINKS>) : pick(dkdv128_kernel<FLEX_SCORE_ALIBI, SINKS>);
         default:
-            return d64 ? pick(dkdv_kernel<FLEX_SCORE_IDENTITY>) : pick(dkdv128_kernel<FLEX_SCORE_IDENTITY>);
+            return d64 ? pick(dkdv_kernel<FLEX_SCORE_IDENTITY, SINKS>) : pick(dkdv128_kernel<FLEX_SCORE_IDENTITY, SINKS>);
     }
 }
 
 // dQ of fp32 inputs on the tensor cores (p.D == 64 or 128).
-inline cudaError_t launch_bwd_fp32_tc_dq(const AttnProblem &p, const BwdF32TcArgs &a, cudaStream_t stream) {
+template <bool SINKS>
+cudaError_t launch_bwd_fp32_tc_dq(const AttnProblem &p, const BwdF32TcArgs &a, cudaStream_t stream) {
     using namespace bwdf32;
     const size_t smem = p.D == 64 ? kDqSmemBytes : d128::kSmemBytes;
     const bool bh_x = p.nqt <= 65535;
@@ -1521,11 +1523,11 @@ inline cudaError_t launch_bwd_fp32_tc_dq(const AttnProblem &p, const BwdF32TcArg
     const bool d64 = p.D == 64;
     switch (p.score_kind) {
         case FLEX_SCORE_SOFTCAP:
-            return d64 ? pick(dq_kernel<FLEX_SCORE_SOFTCAP>) : pick(dq128_kernel<FLEX_SCORE_SOFTCAP>);
+            return d64 ? pick(dq_kernel<FLEX_SCORE_SOFTCAP, SINKS>) : pick(dq128_kernel<FLEX_SCORE_SOFTCAP, SINKS>);
         case FLEX_SCORE_ALIBI:
-            return d64 ? pick(dq_kernel<FLEX_SCORE_ALIBI>) : pick(dq128_kernel<FLEX_SCORE_ALIBI>);
+            return d64 ? pick(dq_kernel<FLEX_SCORE_ALIBI, SINKS>) : pick(dq128_kernel<FLEX_SCORE_ALIBI, SINKS>);
         default:
-            return d64 ? pick(dq_kernel<FLEX_SCORE_IDENTITY>) : pick(dq128_kernel<FLEX_SCORE_IDENTITY>);
+            return d64 ? pick(dq_kernel<FLEX_SCORE_IDENTITY, SINKS>) : pick(dq128_kernel<FLEX_SCORE_IDENTITY, SINKS>);
     }
 }
 

@@ -209,6 +209,10 @@ __device__ __forceinline__ void mask_col_interval(const MaskDesc &m, int kv, int
             l = kv;
             h = min(h, (int64_t)kv + (int64_t)m.window - 1);
             break;
+        case FLEX_MASK_WINDOW_SINKS:    // q >= kv and (q - kv < W or kv < sinks): one interval per column
+            l = kv;
+            if (kv >= m.prefix) h = min(h, (int64_t)kv + (int64_t)m.window - 1);
+            break;
         case FLEX_MASK_CAUSAL_PREFIX:   // (q <= P and kv <= P) or q >= kv
             l = kv <= m.prefix ? 0 : kv;
             break;
@@ -278,13 +282,15 @@ __device__ __forceinline__ void bwd_build_list(const BwdTcParams &p, bool kv_maj
 // first streamed tiles load while the current one ends.  Every role walks the
 // same sequence of published items; the ring, S/dP hand-off and column
 // barriers run on across items with the CTA's global step count.
-template <int D, int SCORE, bool DOC, bool KV_MAJOR>
+template <int D, int SCORE, int MASKC, bool KV_MAJOR>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap map_r0, const __grid_constant__ CUtensorMap map_r1,
                        const __grid_constant__ CUtensorMap map_s0, const __grid_constant__ CUtensorMap map_s1,
                        const BwdTcParams p) {
     using C = BwdTcCfg<D, KV_MAJOR>;
     constexpr int NA = C::kNA, NB = C::kNB;
+    constexpr bool DOC = MASKC == kMaskDocument, SINKS = MASKC == kMaskSinks;
+    static_assert(!(SINKS && KV_MAJOR), "a column of a window + sinks mask is one interval");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     BwdMisc &ms = *reinterpret_cast<BwdMisc *>(smem + C::kMiscOff);
@@ -637,6 +643,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               const int w0 = blk * 128;  // first walked row of the step
               // keep-interval of walked columns for this row (partial steps)
               int clo = 0, chi = -1;
+              int sink_hi = -1;  // window + sinks: columns up to here are kept too
               if (!full) {
                   int lo, hi;
                   if constexpr (KV_MAJOR) {
@@ -651,7 +658,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                           lo = 0;
                           hi = row < p.q_len ? row : -1;
                       } else {
-                          if (!mask_row_interval(p.mask, row, lo, hi)) hi = lo - 1;
+                          if constexpr (SINKS) {
+                              mask_row_sinks(p.mask, row, sink_hi, lo);
+                              sink_hi = row < p.q_len ? min(sink_hi, p.kv_len - 1) - w0 : -1;
+                              hi = row;
+                          } else if (!mask_row_interval(p.mask, row, lo, hi)) {
+                              hi = lo - 1;
+                          }
                           hi = min(hi, p.kv_len - 1);
                           if (row >= p.q_len) hi = lo - 1;
                       }
@@ -739,6 +752,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                           else p_chunk(std::false_type{}, c0, 0u);
                       } else {
                           uint32_t keep = interval_bits(clo, chi, cbase + 32 * c0);
+                          if constexpr (SINKS && !KV_MAJOR) keep |= interval_bits(0, sink_hi, cbase + 32 * c0);
                           if constexpr (DOC) {
                               uint32_t same = 0u;
   #pragma unroll

@@ -7,10 +7,10 @@
 
 namespace flex {
 
-template <int D, int SCORE, bool DOC, bool KV_MAJOR>
+template <int D, int SCORE, int MASKC, bool KV_MAJOR>
 cudaError_t launch_bwd_tc_kernel(const CUtensorMap (&maps)[4], const BwdTcParams &kp, cudaStream_t stream) {
     using C = BwdTcCfg<D, KV_MAJOR>;
-    auto kernel = attn_bwd_tc_kernel<D, SCORE, DOC, KV_MAJOR>;
+    auto kernel = attn_bwd_tc_kernel<D, SCORE, MASKC, KV_MAJOR>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
     if (e != cudaSuccess) return e;
     // one CTA per (batch, head, owned block); the grid is split so it stays
@@ -27,28 +27,28 @@ cudaError_t launch_bwd_tc_kernel(const CUtensorMap (&maps)[4], const BwdTcParams
     return cudaSuccess;
 }
 
-template <int D, bool DOC, bool KV_MAJOR>
+template <int D, int MASKC, bool KV_MAJOR>
 cudaError_t launch_bwd_tc_score(const CUtensorMap (&maps)[4], const BwdTcParams &kp, int score_kind,
                                 cudaStream_t stream) {
     switch (score_kind) {
         case FLEX_SCORE_SOFTCAP:
-            return launch_bwd_tc_kernel<D, FLEX_SCORE_SOFTCAP, DOC, KV_MAJOR>(maps, kp, stream);
+            return launch_bwd_tc_kernel<D, FLEX_SCORE_SOFTCAP, MASKC, KV_MAJOR>(maps, kp, stream);
         case FLEX_SCORE_ALIBI:
-            return launch_bwd_tc_kernel<D, FLEX_SCORE_ALIBI, DOC, KV_MAJOR>(maps, kp, stream);
+            return launch_bwd_tc_kernel<D, FLEX_SCORE_ALIBI, MASKC, KV_MAJOR>(maps, kp, stream);
         default:
-            return launch_bwd_tc_kernel<D, FLEX_SCORE_IDENTITY, DOC, KV_MAJOR>(maps, kp, stream);
+            return launch_bwd_tc_kernel<D, FLEX_SCORE_IDENTITY, MASKC, KV_MAJOR>(maps, kp, stream);
     }
 }
 
 template <bool KV_MAJOR>
 cudaError_t launch_bwd_tc_dir(const CUtensorMap (&maps)[4], const BwdTcParams &kp, int D, int score_kind,
                               cudaStream_t stream) {
-    const bool doc = kp.mask.kind == FLEX_MASK_DOCUMENT;
+    const int mc = mask_class(kp.mask.kind);
     if (D == 64)
-        return doc ? launch_bwd_tc_score<64, true, KV_MAJOR>(maps, kp, score_kind, stream)
-                   : launch_bwd_tc_score<64, false, KV_MAJOR>(maps, kp, score_kind, stream);
-    return doc ? launch_bwd_tc_score<128, true, KV_MAJOR>(maps, kp, score_kind, stream)
-               : launch_bwd_tc_score<128, false, KV_MAJOR>(maps, kp, score_kind, stream);
+        return mc == kMaskDocument ? launch_bwd_tc_score<64, kMaskDocument, KV_MAJOR>(maps, kp, score_kind, stream)
+                                   : launch_bwd_tc_score<64, kMaskInterval, KV_MAJOR>(maps, kp, score_kind, stream);
+    return mc == kMaskDocument ? launch_bwd_tc_score<128, kMaskDocument, KV_MAJOR>(maps, kp, score_kind, stream)
+                               : launch_bwd_tc_score<128, kMaskInterval, KV_MAJOR>(maps, kp, score_kind, stream);
 }
 
 }  // namespace flex

@@ -196,10 +196,11 @@ __device__ __noinline__ bool f32_produce(F32Misc &ms, uint8_t *ring, uint64_t *f
     return true;
 }
 
-template <int D, int SCORE, bool DOC>
+template <int D, int SCORE, int MASKC>
 __global__ void __launch_bounds__(kF32MaxThreads, 1) attn_fp32_kernel(AttnProblem p, int bh_major) {
     using C = F32Cfg<D>;
     constexpr int KS = C::KS;
+    constexpr bool DOC = MASKC == kMaskDocument, SINKS = MASKC == kMaskSinks;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     F32Misc &ms = *reinterpret_cast<F32Misc *>(smem + C::kMiscOff);
@@ -369,8 +370,15 @@ __global__ void __launch_bounds__(kF32MaxThreads, 1) attn_fp32_kernel(AttnProble
         int doc_q = 0;
         if (DOC && row_in) doc_q = p.mask.doc_ids[(int64_t)b * p.mask.doc_len + q];
         int lo = 0, hi = -1;  // the kept kv interval of an interval mask_mod
+        int sink_hi = -1;     // window + sinks: kv up to here are kept too
         if (!DOC && row_in) {
-            mask_row_interval(p.mask, q, lo, hi);
+            if constexpr (SINKS) {
+                mask_row_sinks(p.mask, q, sink_hi, lo);
+                sink_hi = min(sink_hi, p.kv_len - 1);
+                hi = q;
+            } else {
+                mask_row_interval(p.mask, q, lo, hi);
+            }
             hi = min(hi, p.kv_len - 1);
         }
         bool ok = true;
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(kF32MaxThreads, 1) attn_fp32_kernel(AttnProble
                             keep = row_in && kv <= q && kv < p.kv_len &&
                                    p.mask.doc_ids[(int64_t)b * p.mask.doc_len + kv] == doc_q;
                         else
-                            keep = kv >= lo && kv <= hi;
+                            keep = (kv >= lo && kv <= hi) || (SINKS && kv <= sink_hi);
                         if (!keep) s = -INFINITY;
                     }
                     x[c0 + j] = s;
@@ -542,11 +550,11 @@ __global__ void __launch_bounds__(kF32MaxThreads, 1) attn_fp32_kernel(AttnProble
     }
 }
 
-template <int D, int SCORE, bool DOC>
+template <int D, int SCORE, int MASKC>
 cudaError_t launch_fp32_kernel(const AttnProblem &p, cudaStream_t stream) {
     using C = F32Cfg<D>;
     const size_t smem = f32_smem_bytes<D>();
-    auto kern = attn_fp32_kernel<D, SCORE, DOC>;
+    auto kern = attn_fp32_kernel<D, SCORE, MASKC>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (p.nqt <= 65535) {
@@ -566,22 +574,28 @@ cudaError_t launch_fp32_kernel(const AttnProblem &p, cudaStream_t stream) {
     return cudaSuccess;
 }
 
-template <int D, bool DOC>
+template <int D, int MASKC>
 cudaError_t launch_fp32_score(const AttnProblem &p, cudaStream_t stream) {
     switch (p.score_kind) {
         case FLEX_SCORE_SOFTCAP:
-            return launch_fp32_kernel<D, FLEX_SCORE_SOFTCAP, DOC>(p, stream);
+            return launch_fp32_kernel<D, FLEX_SCORE_SOFTCAP, MASKC>(p, stream);
         case FLEX_SCORE_ALIBI:
-            return launch_fp32_kernel<D, FLEX_SCORE_ALIBI, DOC>(p, stream);
+            return launch_fp32_kernel<D, FLEX_SCORE_ALIBI, MASKC>(p, stream);
         default:
-            return launch_fp32_kernel<D, FLEX_SCORE_IDENTITY, DOC>(p, stream);
+            return launch_fp32_kernel<D, FLEX_SCORE_IDENTITY, MASKC>(p, stream);
     }
 }
 
 template <int D>
 cudaError_t launch_fp32_d(const AttnProblem &p, cudaStream_t stream) {
-    return p.mask.kind == FLEX_MASK_DOCUMENT ? launch_fp32_score<D, true>(p, stream)
-                                             : launch_fp32_score<D, false>(p, stream);
+    switch (mask_class(p.mask.kind)) {
+        case kMaskDocument:
+            return launch_fp32_score<D, kMaskDocument>(p, stream);
+        case kMaskSinks:
+            return launch_fp32_score<D, kMaskSinks>(p, stream);
+        default:
+            return launch_fp32_score<D, kMaskInterval>(p, stream);
+    }
 }
 
 }  // namespace

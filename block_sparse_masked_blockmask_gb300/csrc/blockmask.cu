@@ -11,6 +11,9 @@
 //    tile is full when every row's interval covers the tile's columns and
 //    empty when no row's interval meets them: Q_BLOCK row tests instead of
 //    Q_BLOCK x KV_BLOCK predicate evaluations.
+//  * window + sinks: the kept kv of a row are two intervals
+//    (mask_row_sinks); the same row tests, a row covering the tile when one of
+//    them does.
 //  * document: exact quick decisions first (a tile above the diagonal is
 //    empty; a tile on or below it whose row and column ids are one id is
 //    full; disjoint id ranges are empty), otherwise mask_mod is evaluated on
@@ -48,6 +51,26 @@ __device__ __forceinline__ uint8_t classify_interval_tile(const MaskDesc &m, int
         const int a = max(lo, kv0), e = min(hi, kv0 + kvbs - 1);
         any |= row && a <= e;
         all &= row && lo <= kv0 && hi >= kv0 + kvbs - 1;
+    }
+    any = __any_sync(0xffffffffu, any);
+    all = __all_sync(0xffffffffu, all);
+    return all ? kFull : (any ? kPartial : kEmpty);
+}
+
+// Window + sinks: the same row tests on the row's two intervals.
+__device__ __forceinline__ uint8_t classify_sinks_tile(const MaskDesc &m, int q0, int kv0, int qbs, int kvbs,
+                                                       int lane) {
+    bool any = false, all = true;
+    const int last = kv0 + kvbs - 1;
+    for (int r = lane; r < qbs; r += 32) {
+        const int q = q0 + r;
+        int sink_hi, lo;
+        mask_row_sinks(m, q, sink_hi, lo);
+        const int hi = min(q, m.kv_len - 1);
+        sink_hi = min(sink_hi, m.kv_len - 1);
+        const bool row = q < m.q_len;
+        any |= row && (kv0 <= sink_hi || max(lo, kv0) <= min(hi, last));
+        all &= row && (last <= sink_hi || (lo <= kv0 && hi >= last));
     }
     any = __any_sync(0xffffffffu, any);
     all = __all_sync(0xffffffffu, all);
@@ -165,6 +188,8 @@ __global__ void __launch_bounds__(kBmThreads) block_mask_kernel(MaskDesc m, int 
         uint8_t st;
         if constexpr (KIND == FLEX_MASK_DOCUMENT)
             st = classify_document_tile(m, b, q0, kvb * kvbs, qbs, kvbs, lane, row_doc, row_range[0], row_range[1]);
+        else if constexpr (KIND == FLEX_MASK_WINDOW_SINKS)
+            st = classify_sinks_tile(m, q0, kvb * kvbs, qbs, kvbs, lane);
         else
             st = classify_interval_tile(m, q0, kvb * kvbs, qbs, kvbs, lane);
         if (lane == 0) status[kvb] = st;
@@ -224,6 +249,9 @@ cudaError_t launch_block_mask(const MaskDesc &mask, int B, int H, int q_len, int
         case FLEX_MASK_DOCUMENT:
             return launch_kind<FLEX_MASK_DOCUMENT>(mask, B, H, nqb, nkvb, q_block, kv_block, kv_num, kv_idx,
                                                    full_num, full_idx, stream);
+        case FLEX_MASK_WINDOW_SINKS:
+            return launch_kind<FLEX_MASK_WINDOW_SINKS>(mask, B, H, nqb, nkvb, q_block, kv_block, kv_num, kv_idx,
+                                                       full_num, full_idx, stream);
         default:
             return launch_kind<FLEX_MASK_ALL>(mask, B, H, nqb, nkvb, q_block, kv_block, kv_num, kv_idx, full_num,
                                               full_idx, stream);

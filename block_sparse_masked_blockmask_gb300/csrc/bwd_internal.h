@@ -17,6 +17,8 @@ cudaError_t launch_bwd_tc_dkdv(const CUtensorMap (&maps)[4], const BwdTcParams &
                                cudaStream_t stream);
 cudaError_t launch_bwd_tc_dq(const CUtensorMap (&maps)[4], const BwdTcParams &kp, int D, int score_kind,
                              cudaStream_t stream);
+cudaError_t launch_bwd_tc_dq_sinks(const CUtensorMap (&maps)[4], const BwdTcParams &kp, int D, int score_kind,
+                                   cudaStream_t stream);
 // q blocks per kv block the tensor-core backward walks on chip (NQB limit for bf16)
 constexpr int kBwdTcMaxQBlocks = 2048;
 

@@ -25,7 +25,7 @@ __host__ __device__ constexpr int ceil_div(int64_t len, int bs) { return (int)((
 struct MaskDesc {
     int32_t kind;
     int32_t window;
-    int32_t prefix;
+    int32_t prefix;             // causal + prefix: inclusive bound; window + sinks: first tokens that stay visible
     int32_t doc_len;            // row length of doc_ids (== q_len == kv_len)
     const int32_t *doc_ids;     // [B, doc_len]
     int32_t q_len, kv_len;      // positions at or past these are padding: masked
@@ -34,7 +34,8 @@ struct MaskDesc {
 // Tiles along a length: the last one may reach past it (padding, masked).
 __host__ __device__ constexpr int ceil_blocks(int64_t len) { return (int)((len + kBlock - 1) / kBlock); }
 
-// mask_mod(b, h, q, kv) for the enumerated kinds.  No kind depends on h.
+// mask_mod(b, h, q, kv) for the enumerated kinds but window + sinks (mask_keep
+// below).  No kind depends on h.
 __host__ __device__ __forceinline__ bool mask_mod(const MaskDesc &m, int b, int q, int kv) {
     switch (m.kind) {
         case FLEX_MASK_CAUSAL:
@@ -51,7 +52,8 @@ __host__ __device__ __forceinline__ bool mask_mod(const MaskDesc &m, int b, int 
 }
 
 // The interval kinds keep, for a fixed row q, exactly the kv in [lo, hi].
-// Returns false for kinds whose kept set is not an interval (document).
+// Returns false for kinds whose kept set is not an interval (document, window
+// + sinks).
 __host__ __device__ __forceinline__ bool mask_row_interval(const MaskDesc &m, int q, int &lo, int &hi) {
     switch (m.kind) {
         case FLEX_MASK_CAUSAL:
@@ -73,6 +75,33 @@ __host__ __device__ __forceinline__ bool mask_row_interval(const MaskDesc &m, in
         default:
             return false;
     }
+}
+
+// The window + sinks kind keeps two intervals per row, [0, sink_hi] and
+// [lo, q].  Once the window reaches down to the sinks they are one,
+// [0, q] (sink_hi is then q, and lo 0).
+__host__ __device__ __forceinline__ void mask_row_sinks(const MaskDesc &m, int q, int &sink_hi, int &lo) {
+    lo = q - m.window + 1 > 0 ? q - m.window + 1 : 0;
+    sink_hi = m.prefix - 1 < q ? m.prefix - 1 : q;
+    if (lo <= sink_hi + 1) {
+        lo = 0;
+        sink_hi = q;
+    }
+}
+
+// mask_mod in kernels compiled apart for window + sinks masks: one more case
+// in the switch above made the fp32 backward 6% slower for every kind.
+template <bool SINKS>
+__host__ __device__ __forceinline__ bool mask_keep(const MaskDesc &m, int b, int q, int kv) {
+    if constexpr (SINKS) return q >= kv && (q - kv < m.window || kv < m.prefix);
+    return mask_mod(m, b, q, kv);
+}
+
+// Mask classes the attention kernels are compiled for: interval kinds, the
+// document kind, and window + sinks.
+enum : int { kMaskInterval = 0, kMaskDocument = 1, kMaskSinks = 2 };
+__host__ __device__ constexpr int mask_class(int kind) {
+    return kind == FLEX_MASK_DOCUMENT ? kMaskDocument : kind == FLEX_MASK_WINDOW_SINKS ? kMaskSinks : kMaskInterval;
 }
 
 // Problem description handed from the C-ABI layer to the attention launchers.
@@ -107,6 +136,12 @@ cudaError_t launch_attn_bf16(const AttnProblem &p, cudaStream_t stream);
 bool make_bf16_tile_map(CUtensorMap *map, const void *base, int B, int H, int S, int D, const int64_t st[4]);
 
 cudaError_t launch_wait_timeout_selftest(int *status, uint64_t limit_ns, cudaStream_t stream);
+
+// Argument checks shared by the C-ABI layer's files: a [B, H, S, D] tensor of
+// the given type and shape with 16-byte aligned base and strides, inner stride
+// 1; and the parameters of the windowed mask kinds.
+int check_tensor(const flex_tensor *t, int dtype, int64_t B, int64_t H, int64_t S, int64_t D);
+bool valid_window(int kind, const flex_mask_params &prm);
 
 // The per-device workspace holding the status word (allocated once per device).
 int *device_status_word(int *err);

@@ -29,6 +29,7 @@ FLEX_MASK_SLIDING_WINDOW = 1
 FLEX_MASK_CAUSAL_PREFIX = 2
 FLEX_MASK_DOCUMENT = 3
 FLEX_MASK_ALL = 4
+FLEX_MASK_WINDOW_SINKS = 5
 
 FLEX_SCORE_IDENTITY = 0
 FLEX_SCORE_SOFTCAP = 1
@@ -174,6 +175,14 @@ def flex_block_mask_sizes(B: int, H: int, q_len: int, kv_len: int, block: int = 
     return n_num.value, n_idx.value
 
 
+def _mask_params(mask_kind: int, window: int, prefix: int, sinks: int, doc_ids=None) -> flex_mask_params:
+    """The C parameters of a mask kind (the count of sinks travels in `prefix`)."""
+    if sinks and mask_kind != FLEX_MASK_WINDOW_SINKS:
+        raise ValueError("sinks belong to FLEX_MASK_WINDOW_SINKS")
+    return flex_mask_params(window, sinks if mask_kind == FLEX_MASK_WINDOW_SINKS else prefix,
+                            doc_ids.data_ptr() if doc_ids is not None else None)
+
+
 class BlockMask:
     """Device BlockMask: the C struct plus the torch tensors that own its buffers."""
 
@@ -227,11 +236,13 @@ def flex_block_mask_transpose(block_mask: BlockMask, stream=None) -> BlockMaskQ:
 
 def flex_block_mask_create(mask_kind: int, B: int, H: int, q_len: int, kv_len: int, block: int = 128,
                            window: int = 0, prefix: int = 0, doc_ids: torch.Tensor | None = None,
-                           device=None, stream=None, kv_block: int | None = None) -> BlockMask:
+                           device=None, stream=None, kv_block: int | None = None, sinks: int = 0) -> BlockMask:
     """Build a BlockMask on the device (asynchronous on `stream`).
 
     Tiles are block (Q_BLOCK) rows by kv_block (KV_BLOCK; default: block)
     columns; flex_block_mask_create_qkv is called when kv_block is given.
+    FLEX_MASK_WINDOW_SINKS takes `window` and `sinks` (first tokens that stay
+    visible).
     """
     device = torch.device(device) if device is not None else (
         doc_ids.device if doc_ids is not None else torch.device("cuda", torch.cuda.current_device()))
@@ -247,7 +258,7 @@ def flex_block_mask_create(mask_kind: int, B: int, H: int, q_len: int, kv_len: i
     assert t["kv_num_blocks"].numel() == n_num and t["kv_indices"].numel() == n_idx
     if doc_ids is not None:
         doc_ids = doc_ids.to(device=device, dtype=torch.int32).contiguous()
-    params = flex_mask_params(window, prefix, doc_ids.data_ptr() if doc_ids is not None else None)
+    params = _mask_params(mask_kind, window, prefix, sinks, doc_ids)
     bm = flex_block_mask()
     bm.kv_num_blocks = t["kv_num_blocks"].data_ptr()
     bm.kv_indices = t["kv_indices"].data_ptr()
@@ -437,7 +448,7 @@ def flex_attention_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, b
                             mask_kind: int, out: torch.Tensor, lse: torch.Tensor, window: int = 0, prefix: int = 0,
                             doc_ids: torch.Tensor | None = None, score_kind: int = FLEX_SCORE_IDENTITY,
                             score_param: float = 0.0, scale: float | None = None, chunks: int = 8,
-                            stream=None) -> None:
+                            stream=None, sinks: int = 0) -> None:
     """BlockMask build + attention from host q, k, v into host out, lse (see include/flexattn.h).
 
     q, k, v, out, lse (and doc_ids) are contiguous CPU tensors, pinned for the
@@ -454,7 +465,7 @@ def flex_attention_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, b
     if doc_ids is not None and doc_ids.dtype != torch.int32:
         raise ValueError("doc_ids must be int32")
     tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
-    params = flex_mask_params(window, prefix, doc_ids.data_ptr() if doc_ids is not None else None)
+    params = _mask_params(mask_kind, window, prefix, sinks, doc_ids)
     dev = buffers.struct()
     with torch.cuda.device(buffers.device):
         rc = load_library().flex_attention_fwd_host(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), mask_kind,

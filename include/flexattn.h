@@ -81,7 +81,9 @@ typedef enum {
     FLEX_MASK_SLIDING_WINDOW = 1,  /* q >= kv and q - kv < window                           */
     FLEX_MASK_CAUSAL_PREFIX = 2,   /* (q <= prefix and kv <= prefix) or q >= kv (inclusive) */
     FLEX_MASK_DOCUMENT = 3,        /* doc_ids[b][q] == doc_ids[b][kv] and q >= kv           */
-    FLEX_MASK_ALL = 4              /* every pair (dense attention; for checks and timing)   */
+    FLEX_MASK_ALL = 4,             /* every pair (dense attention; for checks and timing)   */
+    FLEX_MASK_WINDOW_SINKS = 5     /* q >= kv and (q - kv < window or kv < prefix): a sliding
+                                      window plus the first `prefix` tokens (sinks)         */
 } flex_mask_kind;
 
 /* The enumerated score_mods, applied to the scaled score s = scale * q.k. */
@@ -98,8 +100,11 @@ typedef enum {
 
 /* Parameters of a mask_mod.  Unused fields are ignored for kinds that do not need them. */
 typedef struct {
-    int32_t window;                /* FLEX_MASK_SLIDING_WINDOW: W >= 0 (W = 0 masks everything) */
-    int32_t prefix;                /* FLEX_MASK_CAUSAL_PREFIX: P, inclusive bound                */
+    int32_t window;                /* FLEX_MASK_SLIDING_WINDOW, FLEX_MASK_WINDOW_SINKS: W >= 0
+                                      (W = 0: the window keeps nothing)                          */
+    int32_t prefix;                /* FLEX_MASK_CAUSAL_PREFIX: P, inclusive bound;
+                                      FLEX_MASK_WINDOW_SINKS: how many first tokens stay visible
+                                      (>= 0; 0 is a plain sliding window)                        */
     const int32_t *doc_ids;        /* FLEX_MASK_DOCUMENT: device, [B, Q_LEN] int32, contiguous   */
 } flex_mask_params;
 

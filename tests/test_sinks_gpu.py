@@ -1,0 +1,161 @@
+"""Sliding window + sinks masks: the BlockMask against brute force, and the
+forward and backward against the formulas in float64.
+
+Bounds.  Scores are float32 sums of D exact products: each is off by at most
+(D + 8) 2^-24 scale sum |q k|, and so is lse, plus 2^-20 for the exponentials
+and their sum.  The bf16 path rounds P (half a step: 2^-8 of each weight) and
+its outputs (2^-8 of each); dS is rounded once more, and delta comes from the
+rounded out.  So with A the same sums over absolute values,
+  |d out| <= 2^-8 |out| + (2^-8 + e) A_out,  and likewise for the gradients,
+where e covers the relative error of P that the score errors cause.  The
+float32 path splits every operand into three bf16 parts: what it leaves out of
+each product is at most 2^-22 of it, 2^-18 of A with the sums.
+"""
+import itertools
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_masked_blockmask_gb300 import flexattn as fa
+
+pytestmark = pytest.mark.gpu
+
+
+def dense_mask(q_len, kv_len, window, sinks):
+    q, kv = torch.arange(q_len)[:, None], torch.arange(kv_len)
+    return (q >= kv) & ((q - kv < window) | (kv < sinks))
+
+
+def brute_blocks(keep, qb, kvb):
+    nq, nk = -(-keep.shape[0] // qb), -(-keep.shape[1] // kvb)
+    pad = torch.zeros((nq * qb, nk * kvb), dtype=torch.bool)
+    pad[:keep.shape[0], :keep.shape[1]] = keep
+    t = pad.reshape(nq, qb, nk, kvb)
+    full = t.all(3).all(1)
+    return t.any(3).any(1) & ~full, full
+
+
+def ordered(sel):
+    """Per row: the selected blocks ascending, then the others."""
+    return torch.sort((~sel).to(torch.int8), dim=1, stable=True).indices.to(torch.int32)
+
+
+@pytest.mark.parametrize("q_len,kv_len", [(1, 1), (127, 127), (129, 129), (1000, 1000), (200, 700), (700, 200)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (0, 3), (1, 0), (1, 1), (100, 4), (128, 128), (64, 200), (257, 129),
+                                          (2**31 - 1, 5), (3, 2**31 - 1)])
+def test_block_mask(q_len, kv_len, window, sinks):
+    keep = dense_mask(q_len, kv_len, window, sinks)
+    for qb, kvb in ((128, 128), (16, 64), (256, 32)):
+        bm = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, 1, 2, q_len, kv_len, qb, window=window, sinks=sinks,
+                                       kv_block=kvb)
+        part, full = brute_blocks(keep, qb, kvb)
+        got = bm.as_numpy()
+        for h in range(2):
+            assert np.array_equal(got["kv_num_blocks"][0, h], part.sum(1).int().numpy())
+            assert np.array_equal(got["full_kv_num_blocks"][0, h], full.sum(1).int().numpy())
+            assert np.array_equal(got["kv_indices"][0, h], ordered(part).numpy())
+            assert np.array_equal(got["full_kv_indices"][0, h], ordered(full).numpy())
+
+
+def reference(q, k, v, g, keep, score, cap, scale):
+    """float64 out, lse, gradients, the same sums over absolute values, and the bound of the scores' errors."""
+    q, k, v, g = (x.double() for x in (q, k, v, g))
+    H, D = q.shape[1], q.shape[3]
+    t = scale * (q @ k.transpose(2, 3))
+    size = scale * (q.abs() @ k.abs().transpose(2, 3))
+    s, slope = t, torch.ones_like(t)
+    if score == fa.FLEX_SCORE_SOFTCAP:
+        s = cap * torch.tanh(t / cap)
+        slope = 1 - torch.tanh(t / cap) ** 2
+    elif score == fa.FLEX_SCORE_ALIBI:
+        h = torch.arange(1, H + 1, device=q.device, dtype=torch.float64)
+        far = torch.arange(q.shape[2], device=q.device)[:, None] - torch.arange(k.shape[2], device=q.device)
+        s = t - (2.0 ** (-8.0 * h / H)).reshape(1, H, 1, 1) * far
+        size = size + far.abs()
+    s = s.masked_fill(~keep, -math.inf)
+    lse = torch.logsumexp(s, -1)
+    p = torch.where(keep, (s - lse[..., None]).exp(), 0.0)
+    e_s = ((D + 8) * 2.0**-24 * torch.where(keep, size, 0.0)).amax(-1)
+    out = p @ v
+    dv = p.transpose(2, 3) @ g
+    dp = g @ v.transpose(2, 3)
+    delta = (g * out).sum(-1, keepdim=True)
+    ds = p * (dp - delta) * slope
+    # per pair: |dS| and what the rounding of out does to delta, and P times the size of dP
+    ads = p * slope * ((dp - delta).abs() + (g.abs() * out.abs()).sum(-1, keepdim=True))
+    adp = p * slope * (g.abs() @ v.abs().transpose(2, 3) + (g * out).abs().sum(-1, keepdim=True))
+    absolute = dict(out=p @ v.abs(), dv=p.transpose(2, 3) @ g.abs(), dq=scale * (ads @ k.abs()),
+                    dk=scale * (ads.transpose(2, 3) @ q.abs()))
+    product = dict(out=absolute["out"], dv=absolute["dv"], dq=scale * (adp @ k.abs()),
+                   dk=scale * (adp.transpose(2, 3) @ q.abs()))
+    return dict(out=out, lse=lse, dq=scale * (ds @ k), dk=scale * (ds.transpose(2, 3) @ q), dv=dv), absolute, product, e_s
+
+
+CASES = [(w, s) + x for (w, s), x in zip(
+    [(0, 0), (0, 3), (1, 0), (1, 1), (16, 4), (100, 4), (128, 128), (300, 17), (64, 200), (2**31 - 1, 5), (40, 2**31 - 1),
+     (256, 4), (257, 130)],
+    itertools.cycle([(130, 130), (1, 1), (129, 129), (500, 500), (300, 200), (130, 300), (257, 257)]))]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sinks,q_len,kv_len", CASES + [(100, 4, 1000, 1000), (256, 4, 700, 700)])
+def test_forward_and_backward(window, sinks, q_len, kv_len, D, dtype):
+    B, H = 2, 3
+    scale = 1.0 / math.sqrt(D)
+    gen = torch.Generator().manual_seed(q_len * 7 + D)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, v, g = (torch.randn((B, H, n, D), generator=gen).to(dt).cuda() for n in (q_len, kv_len, kv_len, q_len))
+    keep = dense_mask(q_len, kv_len, window, sinks).cuda()
+    for score in (fa.FLEX_SCORE_IDENTITY, fa.FLEX_SCORE_ALIBI):
+        ref, absolute, product, e_s = reference(q, k, v, g, keep, score, 0.0, scale)
+        for blocks in ((128, None), (64, 256)):
+            bm = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, B, H, q_len, kv_len, blocks[0], window=window,
+                                           sinks=sinks, kv_block=blocks[1])
+            out, lse = fa.flex_attention_fwd(q, k, v, bm, score)
+            got = dict(zip(("dq", "dk", "dv"), fa.flex_attention_bwd(q, k, v, out, lse, g, bm,
+                                                                     fa.flex_block_mask_transpose(bm), score)))
+            assert fa.flex_device_status() == fa.FLEX_OK
+            got["out"] = out
+            empty = ~keep.any(-1)
+            assert torch.isneginf(lse[:, :, empty]).all() and (out[:, :, empty] == 0).all()
+            assert (got["dq"][:, :, empty] == 0).all()
+            live = ~empty
+            e_lse = (lse.double() - ref["lse"]).abs()[:, :, live]
+            assert (e_lse <= e_s[:, :, live] + 2.0**-20 * (1 + ref["lse"][:, :, live].abs())).all(), \
+                (score, blocks, float(e_lse.max()))
+            e_p = 2 * float(e_s.max()) + 2.0**-18 if live.any() else 0.0  # relative error of a recomputed P
+            for name, x in got.items():
+                diff = (x.double() - ref[name]).abs()
+                r = 2.0**-8 if dtype == "bf16" else 2.0**-18
+                bound = r * ref[name].abs() + 2 * r * absolute[name] + (e_p + 2.0**-18) * product[name]
+                assert (diff <= bound + 1e-30).all(), (name, score, blocks, float((diff - bound).max()))
+
+
+def test_no_sinks_is_the_sliding_window():
+    q, k, v = (torch.randn((1, 2, 700, 64), device="cuda").bfloat16() for _ in range(3))
+    a = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, 1, 2, 700, 700, window=100)
+    b = fa.flex_block_mask_create(fa.FLEX_MASK_SLIDING_WINDOW, 1, 2, 700, 700, window=100)
+    for key, x in a.as_numpy().items():
+        assert np.array_equal(x, b.as_numpy()[key])
+    (oa, la), (ob, lb) = fa.flex_attention_fwd(q, k, v, a), fa.flex_attention_fwd(q, k, v, b)
+    # the older kind sums its weights after rounding them: each off by 2^-8 at most
+    assert (oa.float() - ob.float()).abs().max() <= 3 * 2.0**-8 * v.float().abs().max()
+    assert (la - lb).abs().max() <= 2.0**-8 * 1.01
+
+
+def test_host_entry_point_and_options():
+    B, H, S, D = 1, 4, 333, 64
+    q, k, v = (torch.randn((B, H, S, D)).bfloat16().pin_memory() for _ in range(3))
+    out, lse = torch.empty_like(q).pin_memory(), torch.empty((B, H, S)).pin_memory()
+    fa.flex_attention_fwd_host(q, k, v, fa.DeviceBuffers(B, H, S, S, D, torch.bfloat16), fa.FLEX_MASK_WINDOW_SINKS, out,
+                               lse, window=50, sinks=7, chunks=3)
+    torch.cuda.synchronize()
+    bm = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, B, H, S, S, window=50, sinks=7)
+    o, l_, m = fa.flex_attention_fwd_opts(q.cuda(), k.cuda(), v.cuda(), bm, output_max=True)
+    assert torch.equal(o.cpu(), out) and torch.equal(l_.cpu(), lse)
+    x = (q.double() @ k.double().transpose(2, 3)) / math.sqrt(D)
+    x = x.masked_fill(~dense_mask(S, S, 50, 7), -math.inf)
+    assert (m.cpu().double() - x.amax(-1)).abs().max() <= 1e-4
