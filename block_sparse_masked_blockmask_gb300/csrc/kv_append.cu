@@ -1,0 +1,230 @@
+// Appending keys and values to a paged cache: token t of sequence b goes to
+// position cache_lens[b] + t, i.e. page page_table[b][position / page] and
+// slot position % page; keys are rotated by their position on the way.
+//
+// A bf16 cache holds the values rounded once.  An e4m3 cache holds, for each
+// (page, head), codes and one power-of-two scale s: value = code * s, with s
+// the smallest power of two that keeps the page's largest magnitude within
+// 448 s (e4m3's largest value).  While a page fills, its scale only grows: the
+// codes already there are then divided by the growth.  Because both are powers
+// of two, that is exact but for codes that fall below 2^-6 (e4m3's
+// subnormals), which round once more.
+//
+// Bound by memory (read 2 or 4 bytes and write 1 or 2 per value).  One CTA
+// owns one (page, head) of one of the two tensors, so the scale needs no
+// exchange between CTAs and no atomics in global memory: it reads the tokens
+// that fall on its page into registers (two items of 16 values a thread),
+// rotates them in float32, reduces the largest magnitude, and writes codes.
+// The rotated key is quantised from float32, not from a bf16 rounding of it.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "kv_internal.h"
+#include "ptx.cuh"
+
+namespace flex {
+namespace {
+
+constexpr int kItems = 2;   // items (of 16 values) per thread
+constexpr int kMinExp = -126;  // scales are normal float32 powers of two
+
+// Four floats to e4m3 (round to nearest even), the first in the lowest byte.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+// Four e4m3 codes times f, as codes again.
+__device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float f) {
+    float x[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t h2;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w >> (16 * j))));
+        const __half2 h = *reinterpret_cast<const __half2 *>(&h2);
+        x[2 * j] = __low2float(h) * f;
+        x[2 * j + 1] = __high2float(h) * f;
+    }
+    return pack_e4m3x4(x[0], x[1], x[2], x[3]);
+}
+
+// The smallest power of two s with amax <= 448 s = 1.75 * 2^8 s, from the
+// bits of a finite amax >= 0.
+__device__ __forceinline__ float power_scale(uint32_t amax_bits) {
+    int e = (int)(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u);
+    e = max(e, kMinExp);
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ void load8(const uint16_t *src, float (&x)[8]) {
+    const uint4 r = *reinterpret_cast<const uint4 *>(src);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(w[j] << 16);
+        x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void load8(const float *src, float (&x)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// T: source type; E4M3: the cache's codes (else bf16).
+template <typename T, bool E4M3, int D>
+__global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p) {
+    __shared__ uint64_t turns[64];
+    __shared__ uint32_t amax_smem;
+    constexpr int IT = D / 16;  // items per token
+    const int h = blockIdx.y >> 1, is_v = blockIdx.y & 1, b = blockIdx.z;
+    const int page = p.cache.page;
+    const int64_t first = p.cache_lens[b];
+    const int n_new = min(max(p.new_lens ? p.new_lens[b] : p.S, 0), p.S);
+    if (first < 0 || n_new == 0) return;
+    const int64_t slot = first / page + blockIdx.x;          // entry of the page table
+    const int64_t page0 = slot * page;                       // the page's first position
+    const int64_t lo = max(first, page0), hi = min(first + n_new, page0 + page);
+    if (lo >= hi || slot >= p.max_pages) return;
+    const int id = p.page_table[(int64_t)b * p.max_pages + slot];
+    if (id < 0 || id >= p.cache.num_pages) return;           // a bad page: its tokens are dropped
+    const int64_t ph = (int64_t)id * p.cache.H + h;
+    const bool rotate = !is_v && p.inv_freq;
+    float *scale_at = is_v ? p.cache.v_scale : p.cache.k_scale;
+    const int old_n = (int)(lo - page0);                     // tokens the page already holds
+    const float old = E4M3 && old_n > 0 ? scale_at[ph] : 0.f;
+    if (threadIdx.x == 0) amax_smem = 0u;
+    if (rotate)
+        for (int i = threadIdx.x; i < p.rotary / 2; i += blockDim.x) turns[i] = turns_per_position(p.inv_freq[i]);
+    __syncthreads();
+
+    const T *src = static_cast<const T *>(is_v ? p.v : p.k);
+    const int64_t *st = is_v ? p.v_stride : p.k_stride;
+    src += b * st[0] + h * st[1];
+    const int n = (int)(hi - lo), total = n * IT;
+    float x[kItems][2][8];
+    int e0[kItems], e1[kItems];
+    uint32_t top = 0u;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int i = k * (int)blockDim.x + (int)threadIdx.x;
+        if (i >= total) continue;
+        const int tok = i / IT, item = i % IT;
+        const int64_t pos = lo + tok;
+        const bool turned = rotate && item < p.rotary / 16;
+        const bool half = turned && p.layout == FLEX_ROPE_HALF;
+        e0[k] = half ? item * 8 : item * 16;
+        e1[k] = half ? p.rotary / 2 + item * 8 : item * 16 + 8;
+        const T *row = src + (pos - first) * st[2];
+        load8(row + e0[k], x[k][0]);
+        load8(row + e1[k], x[k][1]);
+        if (turned) {
+            // |angle| <= pi: the fast sine and cosine are within 2^-21 there
+            auto turn = [&](float &a, float &z, int j) {
+                float sn, cs;
+                __sincosf(half_turns(turns[item * 8 + j], (int32_t)pos) * 3.14159265358979f, &sn, &cs);
+                sn *= p.attention_scale;
+                cs *= p.attention_scale;
+                const float a0 = a, z0 = z;
+                a = a0 * cs - z0 * sn;
+                z = z0 * cs + a0 * sn;
+            };
+            if (half) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) turn(x[k][0][j], x[k][1][j], j);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) turn(x[k][j / 4][2 * (j % 4)], x[k][j / 4][2 * (j % 4) + 1], j);
+            }
+        }
+        if constexpr (E4M3) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float &y = x[k][j / 8][j % 8];
+                const uint32_t a = __float_as_uint(y) & 0x7FFFFFFFu;
+                if (a >= 0x7F800000u)
+                    y = __uint_as_float(0x7FC00000u);  // infinities and NaN: the code NaN, no part in the scale
+                else
+                    top = max(top, a);
+            }
+        }
+    }
+    uint8_t *dst = (is_v ? p.cache.v : p.cache.k) + ph * page * D * (E4M3 ? 1 : 2);
+    float inv = 1.f;
+    if constexpr (E4M3) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (threadIdx.x % 32 == 0) atomicMax(&amax_smem, top);
+        __syncthreads();
+        const float want = power_scale(amax_smem);
+        const float now = old > want ? old : want;
+        if (threadIdx.x == 0) scale_at[ph] = now;
+        if (old_n > 0 && now != old) {
+            const float f = old / now;
+            uint4 *codes = reinterpret_cast<uint4 *>(dst);
+            for (int i = threadIdx.x; i < old_n * D / 16; i += blockDim.x) {
+                uint4 w = codes[i];
+                w.x = rescale_e4m3x4(w.x, f);
+                w.y = rescale_e4m3x4(w.y, f);
+                w.z = rescale_e4m3x4(w.z, f);
+                w.w = rescale_e4m3x4(w.w, f);
+                codes[i] = w;
+            }
+        }
+        inv = 1.f / now;
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int i = k * (int)blockDim.x + (int)threadIdx.x;
+        if (i >= total) continue;
+        const int64_t at = (int64_t)(old_n + i / IT) * D;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float(&y)[8] = x[k][u];
+            const int64_t e = at + (u ? e1[k] : e0[k]);
+            if constexpr (E4M3)
+                *reinterpret_cast<uint2 *>(dst + e) =
+                    make_uint2(pack_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                               pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+            else
+                *reinterpret_cast<uint4 *>(dst + 2 * e) =
+                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                               pack_bf16x2(y[6], y[7]));
+        }
+    }
+}
+
+template <typename T, bool E4M3, int D>
+cudaError_t launch_append(const AppendProblem &p, cudaStream_t stream) {
+    const int page = p.cache.page;
+    // threads for the tokens that can fall on one page, two items each
+    const int most = (p.S < page ? p.S : page) * (D / 16);
+    int threads = (most + kItems - 1) / kItems;
+    threads = (threads + 31) / 32 * 32;
+    // pages that S tokens can touch, starting anywhere in one
+    const int64_t pages = ((int64_t)p.S + page - 2) / page + 1;
+    const dim3 grid((unsigned)(pages < p.max_pages ? pages : p.max_pages), 2u * p.cache.H, p.B);
+    kv_append_kernel<T, E4M3, D><<<grid, threads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, bool E4M3>
+cudaError_t launch_append_d(const AppendProblem &p, cudaStream_t stream) {
+    return p.cache.D == 64 ? launch_append<T, E4M3, 64>(p, stream) : launch_append<T, E4M3, 128>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendProblem &p, int src_dtype, int cache_dtype, cudaStream_t stream) {
+    const bool e4m3 = cache_dtype == FLEX_DTYPE_E4M3;
+    if (src_dtype == FLEX_DTYPE_BF16)
+        return e4m3 ? launch_append_d<uint16_t, true>(p, stream) : launch_append_d<uint16_t, false>(p, stream);
+    return e4m3 ? launch_append_d<float, true>(p, stream) : launch_append_d<float, false>(p, stream);
+}
+
+}  // namespace flex

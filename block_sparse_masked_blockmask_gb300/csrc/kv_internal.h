@@ -1,0 +1,76 @@
+// Internal declarations of the rotary positions and the paged key/value
+// cache: problem descriptions handed from the C-ABI layer to the launchers,
+// and the arithmetic that both the rotation kernel and the append share.
+#pragma once
+
+#include "flex_internal.h"
+
+namespace flex {
+
+struct RopeProblem {
+    int B, S, D;
+    int heads[2];                    // heads of the two tensors (0: no second tensor)
+    const void *in[2];
+    void *out[2];
+    int64_t in_stride[2][3], out_stride[2][3];  // b, h, s (elements)
+    const double *inv_freq;          // radians per position, rotary / 2 of them
+    const int32_t *positions;        // [B, S], or null: 0 .. S - 1
+    int rotary, layout;
+    float attention_scale;
+    float direction;                 // +1 rotates forward, -1 back
+};
+
+struct KvCache {
+    int num_pages, H, page, D, page_shift;
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;        // e4m3 only
+};
+
+struct AppendProblem {
+    int B, S;
+    KvCache cache;
+    const void *k, *v;
+    int64_t k_stride[3], v_stride[3];  // b, h, s (elements)
+    const int32_t *page_table;       // [B, max_pages]
+    int max_pages;
+    const int32_t *cache_lens, *new_lens;
+    const double *inv_freq;          // null: no rotation
+    int rotary, layout;
+    float attention_scale;
+};
+
+struct CacheAttnProblem {
+    int B, Hq, G, Q;                 // query heads, heads per key head, query tokens
+    KvCache cache;
+    const uint16_t *q;
+    int64_t q_stride[3];             // b, h, token (elements)
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *kv_lens;
+    int window, sinks;               // window INT32_MAX: every earlier token
+    int causal;                      // 0: rows see every cached token
+    int score_kind;
+    float score_param, scale;
+    uint16_t *out;
+    float *lse;
+};
+
+cudaError_t launch_rope(const RopeProblem &p, int dtype, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendProblem &p, int src_dtype, int cache_dtype, cudaStream_t stream);
+cudaError_t launch_cache_attention(const CacheAttnProblem &p, int cache_dtype, cudaStream_t stream);
+
+// Angles are kept as turns in 64-bit fixed point: position * frequency wraps
+// modulo one turn by itself, so the angle of any int32 position is as exact as
+// the frequency (2^-53 of it).  In float32 the angle of position 131072 would
+// be off by 0.004 radians.
+__device__ __forceinline__ uint64_t turns_per_position(double inv_freq) {
+    const double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
+    return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
+}
+// The angle of a position in half turns, in [-1, 1).
+__device__ __forceinline__ float half_turns(uint64_t turns, int32_t position) {
+    const int32_t hi = (int32_t)((turns * (uint64_t)(int64_t)position) >> 32);
+    return (float)hi * 4.656612873077393e-10f;  // 2^-31
+}
+
+}  // namespace flex

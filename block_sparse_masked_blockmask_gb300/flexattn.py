@@ -37,11 +37,21 @@ FLEX_SCORE_ALIBI = 2
 
 FLEX_DTYPE_BF16 = 0
 FLEX_DTYPE_FP32 = 1
+FLEX_DTYPE_E4M3 = 2
+
+FLEX_ROPE_HALF = 0
+FLEX_ROPE_INTERLEAVED = 1
+
+FLEX_ROPE_SCALE_NONE = 0
+FLEX_ROPE_SCALE_LINEAR = 1
+FLEX_ROPE_SCALE_BASE = 2
+FLEX_ROPE_SCALE_PARTS = 3
 
 EXPORTED = ("flex_block_mask_sizes", "flex_block_mask_sizes_qkv", "flex_block_mask_create", "flex_block_mask_create_qkv",
             "flex_block_mask_transpose", "flex_attention_fwd",
             "flex_attention_fwd_opts", "flex_attention_bwd", "flex_attention_fwd_noalloc", "flex_attention_fwd_host", "flex_device_status",
-            "flex_selftest_wait_timeout", "flex_status_string")
+            "flex_selftest_wait_timeout", "flex_status_string", "flex_rope_frequencies", "flex_rope_fwd", "flex_rope_bwd",
+            "flex_kv_cache_append", "flex_kv_cache_attention")
 
 
 class FlexError(RuntimeError):
@@ -79,6 +89,18 @@ class flex_block_mask_q(ctypes.Structure):
 class flex_kernel_options(ctypes.Structure):
     _fields_ = [("prescale_qk", ctypes.c_int32), ("rows_guaranteed_safe", ctypes.c_int32),
                 ("max_scores", ctypes.c_void_p)]
+
+
+class flex_rope_params(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("attention_scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class flex_kv_cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("H", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 class flex_device_buffers(ctypes.Structure):
@@ -144,6 +166,18 @@ def load_library():
             lib.flex_device_status.restype = ctypes.c_int
             lib.flex_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
             lib.flex_selftest_wait_timeout.restype = ctypes.c_int
+            f64 = ctypes.c_double
+            lib.flex_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, ctypes.POINTER(f64)]
+            lib.flex_rope_frequencies.restype = ctypes.c_int
+            for f in (lib.flex_rope_fwd, lib.flex_rope_bwd):
+                f.argtypes = [tp, tp, ctypes.POINTER(flex_rope_params), vp, tp, tp, vp]
+                f.restype = ctypes.c_int
+            cp = ctypes.POINTER(flex_kv_cache)
+            lib.flex_kv_cache_append.argtypes = [cp, tp, tp, vp, i32, vp, vp, ctypes.POINTER(flex_rope_params), vp]
+            lib.flex_kv_cache_append.restype = ctypes.c_int
+            lib.flex_kv_cache_attention.argtypes = [tp, cp, vp, i32, vp, i32, ctypes.POINTER(flex_mask_params), i32,
+                                                    ctypes.c_float, ctypes.c_float, vp, vp, vp]
+            lib.flex_kv_cache_attention.restype = ctypes.c_int
             lib.flex_status_string.argtypes = [ctypes.c_int]
             lib.flex_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -475,6 +509,175 @@ def flex_attention_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, b
                                                     _stream_handle(stream, buffers.device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_attention_fwd_host")
+
+
+def flex_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = FLEX_ROPE_SCALE_NONE,
+                          factor: float = 1.0, original_len: float = 0.0, low_turns: float = 1.0,
+                          high_turns: float = 32.0, device=None) -> torch.Tensor:
+    """Frequencies of the rotation, float64 [rotary_dim / 2], on `device` (a plan a program makes once)."""
+    host = torch.empty(max(rotary_dim // 2, 1), dtype=torch.float64)
+    rc = load_library().flex_rope_frequencies(rotary_dim, base, scaling, factor, original_len, low_turns, high_turns,
+                                              ctypes.cast(host.data_ptr(), ctypes.POINTER(ctypes.c_double)))
+    if rc != FLEX_OK:
+        raise FlexError(rc, "flex_rope_frequencies")
+    return host.to(torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+
+
+def _device_array(x: torch.Tensor | None, name: str, dtype: torch.dtype, device, shape) -> int | None:
+    """The address of a contiguous tensor of this type, shape and device (None stays None)."""
+    if x is None:
+        return None
+    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    return x.data_ptr()
+
+
+def _rope_params(inv_freq: torch.Tensor, layout: int, attention_scale: float, device) -> flex_rope_params:
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a float64 [rotary_dim / 2] tensor")
+    return flex_rope_params(_device_array(inv_freq, "inv_freq", torch.float64, device, inv_freq.shape),
+                            2 * inv_freq.numel(), layout, attention_scale, 0)
+
+
+def _rope(name: str, q, k, inv_freq, positions, layout, attention_scale, q_out, k_out, stream):
+    device = q.device
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
+    for x in (q, k, q_out, k_out):
+        if x is not None and x.device != device:
+            raise ValueError("q, k and their outputs must be on one device")
+    params = _rope_params(inv_freq, layout, attention_scale, device)
+    pos = _device_array(positions, "positions", torch.int32, device, (q.shape[0], q.shape[2]))
+    tq, oq = _tensor(q), _tensor(q_out)
+    tk, ok = (None if k is None else ctypes.byref(_tensor(k))), (None if k is None else ctypes.byref(_tensor(k_out)))
+    with torch.cuda.device(device):
+        rc = getattr(load_library(), name)(ctypes.byref(tq), tk, ctypes.byref(params), pos, ctypes.byref(oq), ok,
+                                           _stream_handle(stream, device))
+    if rc != FLEX_OK:
+        raise FlexError(rc, name)
+    return q_out, k_out
+
+
+def flex_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, inv_freq: torch.Tensor,
+                  positions: torch.Tensor | None = None, layout: int = FLEX_ROPE_HALF, attention_scale: float = 1.0,
+                  q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """q [B, Hq, S, D] and k [B, Hk, S, D] (or None) turned by their positions; returns (q_out, k_out).
+
+    positions: int32 [B, S] (default 0 .. S - 1).  The outputs may be the
+    inputs.  Asynchronous on `stream`.
+    """
+    return _rope("flex_rope_fwd", q, k, inv_freq, positions, layout, attention_scale, q_out, k_out, stream)
+
+
+def flex_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, inv_freq: torch.Tensor,
+                  positions: torch.Tensor | None = None, layout: int = FLEX_ROPE_HALF, attention_scale: float = 1.0,
+                  dq_out: torch.Tensor | None = None, dk_out: torch.Tensor | None = None, stream=None):
+    """Gradients of flex_rope_fwd's inputs from those of its outputs; same arguments."""
+    return _rope("flex_rope_bwd", dq, dk, inv_freq, positions, layout, attention_scale, dq_out, dk_out, stream)
+
+
+_CACHE_DTYPES = {torch.bfloat16: FLEX_DTYPE_BF16, torch.float8_e4m3fn: FLEX_DTYPE_E4M3}
+
+
+class KVCache:
+    """Paged key/value cache: the C struct plus the torch tensors that own its memory.
+
+    k, v: contiguous [num_pages, H, page_size, D], bfloat16 or float8_e4m3fn;
+    the latter with k_scale, v_scale: contiguous float32 [num_pages, H].
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        if k.dim() != 4 or k.dtype not in _CACHE_DTYPES:
+            raise ValueError("k must be a bfloat16 or float8_e4m3fn [num_pages, H, page_size, D] tensor")
+        scaled = k.dtype == torch.float8_e4m3fn
+        if scaled != (k_scale is not None) or scaled != (v_scale is not None):
+            raise ValueError("an e4m3 cache needs k_scale and v_scale, a bf16 cache takes none")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        n, h, page, d = k.shape
+        self.struct = flex_kv_cache(n, h, page, d, _CACHE_DTYPES[k.dtype], 0,
+                                    _device_array(k, "k", k.dtype, k.device, k.shape),
+                                    _device_array(v, "v", k.dtype, k.device, k.shape),
+                                    _device_array(k_scale, "k_scale", torch.float32, k.device, (n, h)),
+                                    _device_array(v_scale, "v_scale", torch.float32, k.device, (n, h)))
+
+
+def flex_kv_cache_create(num_pages: int, H: int, D: int, page_size: int = 64,
+                         dtype: torch.dtype = torch.float8_e4m3fn, device=None) -> KVCache:
+    """A new cache of num_pages pages (uninitialised) on `device`."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    k, v = (torch.empty((num_pages, H, page_size, D), dtype=dtype, device=device) for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return KVCache(k, v)
+    return KVCache(k, v, *(torch.empty((num_pages, H), dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def flex_kv_cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
+                         cache_lens: torch.Tensor, new_lens: torch.Tensor | None = None,
+                         inv_freq: torch.Tensor | None = None, layout: int = FLEX_ROPE_HALF,
+                         attention_scale: float = 1.0, stream=None) -> None:
+    """Write k, v [B, H, S, D] behind each sequence's cache_lens[b] tokens (asynchronous on `stream`).
+
+    page_table int32 [B, max_pages], cache_lens and new_lens int32 [B].  k is
+    rotated by its positions when inv_freq is given.
+    """
+    device = cache.k.device
+    B = k.shape[0]
+    if k.device != device or v.device != device:
+        raise ValueError("k and v must be on the cache's device")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 [B, max_pages] tensor")
+    table = _device_array(page_table, "page_table", torch.int32, device, (B, page_table.shape[1]))
+    lens = _device_array(cache_lens, "cache_lens", torch.int32, device, (B,))
+    new = _device_array(new_lens, "new_lens", torch.int32, device, (B,))
+    params = None if inv_freq is None else ctypes.byref(_rope_params(inv_freq, layout, attention_scale, device))
+    tk, tv = _tensor(k), _tensor(v)
+    with torch.cuda.device(device):
+        rc = load_library().flex_kv_cache_append(ctypes.byref(cache.struct), ctypes.byref(tk), ctypes.byref(tv), table,
+                                                 page_table.shape[1], lens, new, params,
+                                                 _stream_handle(stream, device))
+    if rc != FLEX_OK:
+        raise FlexError(rc, "flex_kv_cache_append")
+
+
+def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                            mask_kind: int = FLEX_MASK_CAUSAL, window: int = 0, sinks: int = 0,
+                            score_kind: int = FLEX_SCORE_IDENTITY, score_param: float = 0.0,
+                            scale: float | None = None, out: torch.Tensor | None = None,
+                            lse: torch.Tensor | None = None, stream=None):
+    """The newest tokens' queries q [B, Hq, Q, D] against the cache; returns (out, lse).
+
+    kv_lens int32 [B] counts the tokens in the cache, the query tokens among
+    them.  Asynchronous on `stream`.
+    """
+    device = cache.k.device
+    if q.dim() != 4 or q.device != device:
+        raise ValueError("q must be a [B, Hq, Q, D] tensor on the cache's device")
+    B, Hq, Q, D = q.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((B, Hq, Q, D), dtype=q.dtype, device=device)
+    if lse is None:
+        lse = torch.empty((B, Hq, Q), dtype=torch.float32, device=device)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 [B, max_pages] tensor")
+    table = _device_array(page_table, "page_table", torch.int32, device, (B, page_table.shape[1]))
+    lens = _device_array(kv_lens, "kv_lens", torch.int32, device, (B,))
+    out_at = _device_array(out, "out", q.dtype, device, q.shape)
+    lse_at = _device_array(lse, "lse", torch.float32, device, (B, Hq, Q))
+    params = _mask_params(mask_kind, window, 0, sinks)
+    tq = _tensor(q)
+    with torch.cuda.device(device):
+        rc = load_library().flex_kv_cache_attention(ctypes.byref(tq), ctypes.byref(cache.struct), table,
+                                                    page_table.shape[1], lens, mask_kind, ctypes.byref(params),
+                                                    score_kind, float(score_param), float(scale), out_at, lse_at,
+                                                    _stream_handle(stream, device))
+    if rc != FLEX_OK:
+        raise FlexError(rc, "flex_kv_cache_attention")
+    return out, lse
 
 
 def flex_selftest_wait_timeout(limit_ms: int = 50, stream=None, device=None) -> None:

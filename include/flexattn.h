@@ -11,6 +11,10 @@
  *   flex_attention_bwd      the gradients dq, dk, dv of the same attention,
  *                           walking the q side of the BlockMask
  *                           (flex_block_mask_transpose) for dk and dv.
+ *   flex_rope_fwd, flex_rope_bwd       rotary positions of q and k, and the gradient
+ *   flex_kv_cache_append               new keys (rotated on the way) and values
+ *                                      into a paged cache (bf16 or e4m3)
+ *   flex_kv_cache_attention            the newest tokens' attention against it
  * Helpers size the BlockMask buffers, name status codes and read the device
  * status word.
  *
@@ -95,7 +99,8 @@ typedef enum {
 
 typedef enum {
     FLEX_DTYPE_BF16 = 0,           /* bfloat16 storage; tensor-core path, fp32 accumulation */
-    FLEX_DTYPE_FP32 = 1            /* float32 storage; float32-accurate tensor-core forward */
+    FLEX_DTYPE_FP32 = 1,           /* float32 storage; float32-accurate tensor-core forward */
+    FLEX_DTYPE_E4M3 = 2            /* 8-bit floating point with scales; key/value caches only */
 } flex_dtype;
 
 /* Parameters of a mask_mod.  Unused fields are ignored for kinds that do not need them. */
@@ -404,6 +409,138 @@ FLEX_API int flex_attention_bwd(const flex_tensor *q, const flex_tensor *k, cons
                                 const float *lse, const void *dout, const flex_block_mask *bm,
                                 const flex_block_mask_q *bq, int32_t score_kind, float score_param, float scale,
                                 void *dq, void *dk, void *dv, float *delta, void *stream);
+
+/*
+ * Rotary positions.  The first rotary_dim values of a head are rotary_dim / 2
+ * pairs; pair i of a token at position p is turned by p * inv_freq[i]:
+ *   (x0, x1) -> a (x0 cos - x1 sin, x1 cos + x0 sin),  a = attention_scale;
+ * the head's other values are copied.
+ */
+typedef enum {
+    FLEX_ROPE_HALF = 0,            /* pair i = values i and i + rotary_dim / 2 */
+    FLEX_ROPE_INTERLEAVED = 1      /* pair i = values 2 i and 2 i + 1          */
+} flex_rope_layout;
+
+typedef struct {
+    const double *inv_freq;        /* device, [rotary_dim / 2] float64, radians per position (finite) */
+    int32_t rotary_dim;            /* a multiple of 16, at most the head dim                          */
+    int32_t layout;                /* flex_rope_layout                                                */
+    float attention_scale;         /* finite; multiplies the rotated values (1: a plain rotation)     */
+    int32_t reserved;
+} flex_rope_params;
+
+/* How the frequencies base^(-2 i / rotary_dim) are stretched for contexts longer than trained on. */
+typedef enum {
+    FLEX_ROPE_SCALE_NONE = 0,
+    FLEX_ROPE_SCALE_LINEAR = 1,    /* all divided by factor                                              */
+    FLEX_ROPE_SCALE_BASE = 2,      /* base multiplied by factor^(rotary_dim / (rotary_dim - 2))          */
+    FLEX_ROPE_SCALE_PARTS = 3      /* by the turns t_i a pair makes within original_len: kept from
+                                      high_turns on, divided by factor up to low_turns, linear in t_i
+                                      between                                                            */
+} flex_rope_scaling;
+
+/*
+ * Frequencies of the rotation into inv_freq (HOST memory, rotary_dim / 2
+ * float64).  factor >= 1 is read by every scaling but NONE; original_len > 0
+ * and 0 <= low_turns < high_turns by PARTS.  Errors: FLEX_ERR_INVALID_ARG.
+ */
+FLEX_API int flex_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                                   double original_len, double low_turns, double high_turns, double *inv_freq);
+
+/*
+ * Rotate q [B, Hq, S, D] and k [B, Hk, S, D] in one launch.
+ *   k, k_out may both be NULL (one tensor).  Types bf16 or fp32 (one type for
+ *   all), D in {64, 128}; strides as in flex_tensor, 16-byte aligned.
+ *   positions : device, contiguous [B, S] int32 (any value, negative ones turn
+ *               backwards), or NULL: 0 .. S - 1 for every batch entry.
+ *   q_out, k_out : tensors of the inputs' shapes with their own strides;
+ *               they may be the inputs themselves (same data and strides) and
+ *               must not overlap them otherwise.
+ * Angles are exact to 2^-33 of a turn for every position; sine, cosine and the
+ * rotation are float32, the result is rounded once.
+ * Errors: FLEX_ERR_INVALID_ARG, FLEX_ERR_SHAPE, FLEX_ERR_ALIGNMENT,
+ * FLEX_ERR_UNSUPPORTED (head dim, rotary_dim not a multiple of 16, B > 65535,
+ * heads > 32767), FLEX_ERR_CUDA.  Asynchronous on `stream`.
+ */
+FLEX_API int flex_rope_fwd(const flex_tensor *q, const flex_tensor *k, const flex_rope_params *rope,
+                           const int32_t *positions, const flex_tensor *q_out, const flex_tensor *k_out, void *stream);
+
+/*
+ * Gradient of flex_rope_fwd: from the gradients of its outputs to those of its
+ * inputs (each pair turned back, times attention_scale).  Same arguments.
+ */
+FLEX_API int flex_rope_bwd(const flex_tensor *dq, const flex_tensor *dk, const flex_rope_params *rope,
+                           const int32_t *positions, const flex_tensor *dq_out, const flex_tensor *dk_out,
+                           void *stream);
+
+/*
+ * A paged key/value cache.  Pages hold page_size consecutive positions of one
+ * sequence for all heads; a page table [B, max_pages] int32 (device,
+ * contiguous) maps position p of sequence b to page page_table[b][p / page_size],
+ * slot p % page_size.  Entries outside 0 .. num_pages - 1 stand for no page.
+ * FLEX_DTYPE_E4M3: value = code * scale[page][head] with power-of-two scales.
+ * The caller owns all of it; nothing need be initialised before the first
+ * append.
+ */
+typedef struct {
+    int32_t num_pages, H;          /* pages; key/value heads                                  */
+    int32_t page_size, D;          /* a power of two from 16 to 256; head dim 64 or 128       */
+    int32_t dtype;                 /* FLEX_DTYPE_BF16 or FLEX_DTYPE_E4M3                      */
+    int32_t reserved;
+    void *k, *v;                   /* device, [num_pages, H, page_size, D], 16-byte aligned   */
+    float *k_scale, *v_scale;      /* device, [num_pages, H] float32 (E4M3; else unused)      */
+} flex_kv_cache;
+
+/*
+ * Append k, v [B, H, S, D] (bf16 or fp32) to the cache: token t < new_lens[b]
+ * of sequence b goes to position cache_lens[b] + t.
+ *   cache_lens : device, [B] int32: tokens sequence b already has.
+ *   new_lens   : device, [B] int32 (clamped to 0 .. S), or NULL: S for all.
+ *                Tokens past it (padding) are not read.
+ *   rope       : NULL, or the rotation applied to k by its position on the way
+ *                (in float32, with the result rounded once to the cache's type).
+ * E4M3: a page's scale is the smallest power of two that keeps the largest
+ * magnitude written to it since its first slot was written within 448 scale;
+ * when an append raises it, the page's earlier codes are rounded to it.  NaN
+ * and infinities are stored as NaN and do not raise the scale.  Tokens whose
+ * position has no page (past max_pages, or a bad entry) are dropped; slots
+ * that get no token keep their contents.  A page must not be appended to by
+ * two sequences of one call, or by two calls that may run at the same time.
+ * Errors: FLEX_ERR_INVALID_ARG, FLEX_ERR_SHAPE, FLEX_ERR_ALIGNMENT,
+ * FLEX_ERR_UNSUPPORTED (page size, head dim, more than 2^30 positions per
+ * sequence, sizes as for flex_rope_fwd), FLEX_ERR_CUDA.  Asynchronous on
+ * `stream`; cache_lens is read, not advanced.
+ */
+FLEX_API int flex_kv_cache_append(const flex_kv_cache *cache, const flex_tensor *k, const flex_tensor *v,
+                                  const int32_t *page_table, int32_t max_pages, const int32_t *cache_lens,
+                                  const int32_t *new_lens, const flex_rope_params *rope, void *stream);
+
+/*
+ * Attention of each sequence's newest tokens against the cache.  q is
+ * [B, Hq, Q, D] bf16 with Hq a multiple of the cache's H (query head h reads
+ * key head h / (Hq / H)); query token t of sequence b has position
+ * kv_lens[b] - Q + t, so the new tokens are appended first and kv_lens counts
+ * them.  With s and the result rows as in flex_attention_fwd:
+ *   kv_lens   : device, [B] int32, tokens in the cache (clamped to 0 ..
+ *               max_pages * page_size).  Rows at negative positions keep nothing.
+ *   mask_kind : FLEX_MASK_CAUSAL (kv <= position), FLEX_MASK_SLIDING_WINDOW,
+ *               FLEX_MASK_WINDOW_SINKS (params), FLEX_MASK_ALL (every cached
+ *               token); positions in place of q.  Tokens no row keeps are not
+ *               read, nor the pages that hold no others.
+ *   score_kind, score_param, scale : as for flex_attention_fwd.
+ *   out, lse  : device, contiguous [B, Hq, Q, D] bf16 and [B, Hq, Q] float32.
+ * Rows that keep nothing get out = 0, lse = -inf; tokens on a bad page count
+ * as masked.  What lies in slots that a row does not keep has no effect on
+ * it, NaN included.  Made for few query tokens (a decoding step, a handful of
+ * tokens to check); any Q is computed, at the rate of a step of 16 rows per
+ * key head.  Errors: as flex_kv_cache_append, and FLEX_ERR_UNSUPPORTED for
+ * fp32 q and for the prefix and document masks.  Asynchronous on `stream`; no
+ * workspace.
+ */
+FLEX_API int flex_kv_cache_attention(const flex_tensor *q, const flex_kv_cache *cache, const int32_t *page_table,
+                                     int32_t max_pages, const int32_t *kv_lens, int32_t mask_kind,
+                                     const flex_mask_params *params, int32_t score_kind, float score_param,
+                                     float scale, void *out, float *lse, void *stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of
