@@ -1,6 +1,7 @@
 // C-ABI layer of the rotary positions and the paged key/value cache
 // (include/flexattn.h): argument checks on the host and dispatch to the
-// kernels.  None of these calls allocates, keeps state or synchronises.
+// kernels.  None of these calls synchronises; only the attention uses a
+// workspace, the per-device status word.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -81,7 +82,7 @@ int check_cache(const flex_kv_cache *c, const int32_t *page_table, int32_t max_p
     if (c->num_pages <= 0 || c->H <= 0 || c->page_size <= 0 || c->D <= 0 || max_pages <= 0) return FLEX_ERR_SHAPE;
     if (c->D != 64 && c->D != 128) return FLEX_ERR_UNSUPPORTED;
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return FLEX_ERR_UNSUPPORTED;
-    if (c->H > 32767 || (int64_t)max_pages * c->page_size > kMaxCacheLen) return FLEX_ERR_UNSUPPORTED;
+    if (c->H > 32767 || (int64_t)c->num_pages * c->H > INT32_MAX || (int64_t)max_pages * c->page_size > kMaxCacheLen) return FLEX_ERR_UNSUPPORTED;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
         !aligned(page_table, 4) || !aligned(lens, 4))
         return FLEX_ERR_ALIGNMENT;
@@ -225,6 +226,8 @@ int flex_kv_cache_attention(const flex_tensor *q, const flex_kv_cache *cache, co
     p.scale = scale;
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
+    p.status = device_status_word(&rc);
+    if (!p.status) return rc;
     return launch_cache_attention(p, cache->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FLEX_OK
                                                                                                      : FLEX_ERR_CUDA;
 }

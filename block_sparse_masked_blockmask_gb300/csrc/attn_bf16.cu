@@ -43,6 +43,16 @@ bool make_bf16_tile_map(CUtensorMap *map, const void *base, int B, int H, int S,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tile_map_3d(CUtensorMap *map, const void *base, CUtensorMapDataType type, const uint64_t (&dims)[3],
+                      const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, st[2] = {strides[0], strides[1]};
+    const cuuint32_t bx[3] = {box[0], box[1], box[2]}, estr[3] = {1, 1, 1};
+    return enc(map, type, 3, const_cast<void *>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_attn_bf16(const AttnProblem &p, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
     if (!make_bf16_tile_map(&tq, p.q, p.B, p.H, p.q_len, p.D, p.q_stride) ||

@@ -135,6 +135,10 @@ cudaError_t launch_attn_bf16(const AttnProblem &p, cudaStream_t stream);
 // (st[3] == 1): 64 x 128 boxes (head dims x rows), 128-byte swizzle.
 bool make_bf16_tile_map(CUtensorMap *map, const void *base, int B, int H, int S, int D, const int64_t st[4]);
 
+// TMA tensor map of a 3-D view (innermost extent first; strides in bytes).
+bool make_tile_map_3d(CUtensorMap *map, const void *base, CUtensorMapDataType type, const uint64_t (&dims)[3],
+                      const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
+
 cudaError_t launch_wait_timeout_selftest(int *status, uint64_t limit_ns, cudaStream_t stream);
 
 // Argument checks shared by the C-ABI layer's files: a [B, H, S, D] tensor of

@@ -98,15 +98,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Cache data is read once: keep it out of L1.
+// 16 or 8 bytes of shared memory.
 template <int BYTES>
-__device__ __forceinline__ void load_stream(uint32_t *w, const uint8_t *src) {
+__device__ __forceinline__ void load_shared(uint32_t *w, uint32_t addr) {
     if constexpr (BYTES == 8)
-        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(src));
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
     else
-        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "l"(src));
+                     : "r"(addr));
 }
 
 // D: head dim; E4M3: cache type (else bf16); NT: tiles of 8 query rows.
@@ -114,48 +114,67 @@ template <int D, bool E4M3, int NT>
 struct Cfg {
     static constexpr int kElem = E4M3 ? 1 : 2;
     static constexpr int kRowBytes = D * kElem;
-    // 16-token groups a warp has in flight: 4 KB of keys and 4 KB of values
-    static constexpr int kSub = 4096 / (16 * kRowBytes);
-    static constexpr int kTokens = 16 * kSub;
+    static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;  // a row of a staged panel (TMA swizzle span)
+    static constexpr int kPanels = kRowBytes / kPanelBytes;
+    static constexpr int kTile = 4096;                  // bytes of keys (of values) per step of a warp
+    static constexpr int kTokens = kTile / kRowBytes;
+    static constexpr int kSub = kTokens / 16;           // groups of 16 tokens per step
+    static constexpr int kStages = NT == 1 ? 2 : 3;     // steps in flight per warp
     static constexpr int kSteps = D / 16;               // k16 steps of S, m16 tiles of O
     static constexpr int kKWords = kRowBytes / 16;      // words of one key a thread holds
     static constexpr int kVBytes = kRowBytes / 8;       // bytes of one value a thread holds
     static constexpr int kVLoad = kVBytes < 16 ? 8 : 16;
     static constexpr int kRows = 8 * NT;
     static constexpr int kAccStride = D + 4;
-    // shared memory: Q operand, then per warp the accumulators and statistics
+    // shared memory: the warps' rings (over them, at the end, the partial
+    // accumulators), then the Q operand
+    static constexpr int kRing = kWarps * kStages * 2 * kTile;
     static constexpr int kQBytes = NT * kSteps * 32 * 8;
-    static constexpr int kAccBytes = kWarps * kRows * kAccStride * 4;
-    static constexpr int kSmem = (kQBytes > kAccBytes ? kQBytes : kAccBytes);
+    static_assert(kWarps * kRows * kAccStride * 4 <= kRing, "partial accumulators fit the rings");
+    static constexpr int kSmem = 1024 + kRing + kQBytes;  // 1024: alignment of the swizzle
 };
 
-struct Stats {
-    float m[kWarps][32], l[kWarps][32], f[kWarps][32];  // per warp and row
-    float cm[32], cl[32];                               // of the CTA
-    float qf[32];                                       // the power of two taken off a query row
+struct Misc {
+    uint64_t k_full[kWarps][3], v_full[kWarps][3];
+    float m[kWarps][16], l[kWarps][16];  // per warp and row
+    float cm[16], cl[16];                // of the CTA
+    float qf[16];                        // the power of two taken off a query row
+    int abort;
 };
 
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_kernel(CacheAttnProblem p, int csize,
-                                                                                    int row_tiles) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+    cache_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                           const CacheAttnProblem p, int csize, int row_tiles, int box_rows) {
     using C = Cfg<D, E4M3, NT>;
-    constexpr int SUB = C::kSub, KS = C::kSteps;
+    constexpr int SUB = C::kSub, KS = C::kSteps, ST = C::kStages;
     namespace cg = cooperative_groups;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Stats st;
-    uint2 *qs = reinterpret_cast<uint2 *>(smem);
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Misc ms;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint2 *qs = reinterpret_cast<uint2 *>(smem + C::kRing);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
     const int rank = (int)(blockIdx.x % csize);
     const int pair = (int)(blockIdx.x / csize);
     const int rt = pair % row_tiles, bh = pair / row_tiles, hk = bh % p.cache.H, b = bh / p.cache.H;
     const int page = p.cache.page;
+    const int kv_len = __ldg(p.kv_lens + b);
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+        for (int i = 0; i < kWarps * 3; ++i) {
+            mbar_init(&ms.k_full[0][0] + i, 1);
+            mbar_init(&ms.v_full[0][0] + i, 1);
+        }
+        ms.abort = 0;
+        fence_barrier_init();
+    }
 
     // rows of this tile: r = query token * G + head within the group
     const int rows = p.Q * p.G, r0 = rt * C::kRows, r1 = min(r0 + C::kRows, rows) - 1;
     const int tmin = r0 / p.G, tmax = r1 / p.G;
-    const int cap = (int)min((int64_t)p.max_pages * page, (int64_t)INT_MAX);
-    const int n = min(max(p.kv_lens[b], 0), cap);
-    // what any row of the tile keeps: [0, send) and [lo, hi)
+    const int n = (int)min((int64_t)max(kv_len, 0), (int64_t)p.max_pages * page);
+    // what any row of the tile keeps: [0, send) and [lo_min, hi)
     const int hi = p.causal ? max(n - p.Q + tmax + 1, 0) : n;
     const int64_t lo_min = p.causal ? max((int64_t)n - p.Q + tmin - p.window + 1, (int64_t)0) : 0;
     int lo = (int)min(lo_min, (int64_t)hi) / C::kTokens * C::kTokens;
@@ -172,64 +191,78 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
     auto tile_base = [&](int i) { return i < nsink ? i * C::kTokens : lo + (i - nsink) * C::kTokens; };
 
     const int *table = p.page_table + (int64_t)b * p.max_pages;
-    const int64_t page_bytes = (int64_t)page * C::kRowBytes;
-    uint32_t kw[SUB][2][C::kKWords], vw[SUB][4][C::kVBytes / 4];
-    int64_t ph[SUB], ph_next[SUB];  // page * heads + head of the groups in flight, -1: nothing there
-    auto lookup = [&](int base, int64_t (&q)[SUB]) {
-#pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-            const int at = base + 16 * j;
-            q[j] = -1;
-            if (at < hi && (at + 16 > lo_min || at < send)) {
-                const int id = __ldg(table + (at >> p.cache.page_shift));
-                if (id >= 0 && id < p.cache.num_pages) q[j] = (int64_t)id * p.cache.H + hk;
-            }
-        }
-    };
-    auto load_k = [&](int base, const int64_t (&q)[SUB]) {
-#pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-            const uint8_t *src = p.cache.k + q[j] * page_bytes +
-                                 (int64_t)((base + 16 * j) & (page - 1)) * C::kRowBytes + g * C::kRowBytes + t * 16;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int c = 0; c < C::kKWords / 4; ++c) {
-                    if (q[j] >= 0)
-                        load_stream<16>(&kw[j][r][4 * c], src + r * 8 * C::kRowBytes + c * 64);
-                    else
-                        kw[j][r][4 * c] = kw[j][r][4 * c + 1] = kw[j][r][4 * c + 2] = kw[j][r][4 * c + 3] = 0u;
-                }
-        }
-    };
-    auto load_v = [&](int base, const int64_t (&q)[SUB]) {
-#pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-            const uint8_t *src = p.cache.v + q[j] * page_bytes +
-                                 (int64_t)((base + 16 * j) & (page - 1)) * C::kRowBytes + 2 * t * C::kRowBytes +
-                                 g * C::kVLoad;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int c = 0; c < C::kVBytes / C::kVLoad; ++c) {
-                    uint32_t *w = &vw[j][r][c * C::kVLoad / 4];
-                    if (q[j] >= 0) {
-                        load_stream<C::kVLoad>(w, src + ((r & 1) + (r >> 1) * 8) * C::kRowBytes + c * 128);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < C::kVLoad / 4; ++e) w[e] = 0u;
-                    }
-                }
-        }
-    };
-
     const int step = csize * kWarps;
     int tile = rank * kWarps + warp;
-    if (tile < ntiles) {
-        lookup(tile_base(tile), ph);
-        load_k(tile_base(tile), ph);
-        load_v(tile_base(tile), ph);
+    // Of the 16-token groups of a step: page * heads + head, or -1 where there
+    // is nothing that a row keeps, and the page's scales.  The groups of one
+    // box share a page.  Lane i holds those of the warp's step 32 k + i, so that
+    // the loads' latencies are met once in 32 steps.
+    int ph_lane[SUB];
+    float ks_lane[SUB], vs_lane[SUB];
+    auto lookup = [&](int first) {
+        const int mine = first + lane * step;
+        const int base = tile_base(mine);
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) {
+            const int at = base + 16 * j, box = at & ~(box_rows - 1);
+            ph_lane[j] = -1;
+            if (mine < ntiles && box < hi && (box + box_rows > lo_min || box < send)) {
+                const int id = __ldg(table + (at >> p.cache.page_shift));
+                if (id >= 0 && id < p.cache.num_pages) ph_lane[j] = id * p.cache.H + hk;
+            }
+            ks_lane[j] = vs_lane[j] = 0.f;
+        }
+        if constexpr (E4M3) {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j)
+                if (ph_lane[j] >= 0) {
+                    ks_lane[j] = __ldg(p.cache.k_scale + ph_lane[j]);
+                    vs_lane[j] = __ldg(p.cache.v_scale + ph_lane[j]);
+                }
+        }
+    };
+    auto take = [&](int i, int (&ph)[SUB], float (&ks)[SUB], float (&vs)[SUB]) {
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) {
+            ph[j] = __shfl_sync(0xffffffffu, ph_lane[j], i);
+            ks[j] = E4M3 ? __shfl_sync(0xffffffffu, ks_lane[j], i) : 1.f;
+            vs[j] = E4M3 ? __shfl_sync(0xffffffffu, vs_lane[j], i) : 1.f;
+        }
+    };
+    uint8_t *ring = smem + warp * ST * 2 * C::kTile;
+    // one step's keys (or values) into ring slot s (lane 0)
+    auto fetch = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int base, const int (&ph)[SUB]) {
+        if (lane == 0) {
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) bytes += ph[j] >= 0 ? 16u * C::kRowBytes : 0u;
+            mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+            for (int j = 0; j < SUB; ++j)
+                if (ph[j] >= 0 && ((16 * j) & (box_rows - 1)) == 0)
+#pragma unroll
+                    for (int c = 0; c < C::kPanels; ++c)
+                        tma_load_3d(dst + c * C::kTokens * C::kPanelBytes + 16 * j * C::kPanelBytes, map, bar,
+                                    c * (C::kPanelBytes / C::kElem), (base + 16 * j) & (page - 1), ph[j]);
+        }
+    };
+    __syncthreads();  // barriers initialised
+
+    // the first steps in flight; ph, ks, vs: of the current step and the ST - 1 behind it
+    int ph[ST][SUB];
+    float ks[ST][SUB], vs[ST][SUB];
+    lookup(tile);
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+        take(s, ph[s], ks[s], vs[s]);
+        if (tile + s * step < ntiles) {
+            const int base = tile_base(tile + s * step);
+            uint8_t *slot = ring + s * 2 * C::kTile;
+            fetch(&map_k, slot, &ms.k_full[warp][s], base, ph[s]);
+            fetch(&map_v, slot + C::kTile, &ms.v_full[warp][s], base, ph[s]);
+        }
     }
+    int ahead = ST;  // of the warp's steps, the next to be asked for
 
     // Q operand: the rows' largest magnitudes first (e4m3), then the fragments
     auto q_row = [&](int r) {
@@ -251,19 +284,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
             // exponent field of the largest value; 1 for a row of zeros and
             // for rows with infinities or NaN, whose scores are not finite
             const uint32_t e = top >> 7;
-            if (lane == 0) st.qf[r] = e == 0u || e == 255u ? 1.f : __uint_as_float(e << 23);
+            if (lane == 0) ms.qf[r] = e == 0u || e == 255u ? 1.f : __uint_as_float(e << 23);
         }
         __syncthreads();
     }
     for (int i = threadIdx.x; i < NT * KS * 32; i += kThreads) {
-        const int l = i % 32, j = (i / 32) % KS, nt = i / (32 * KS), r = nt * 8 + (l >> 2);
+        const int l = i % 32, j = (i / 32) % KS, nt = i / (32 * KS), r = nt * 8 + (l >> 2), lt = l & 3;
         // the four head dims of step j that lane l's key words hold
-        const int d = E4M3 ? (j / 4) * 64 + (l & 3) * 16 + (j % 4) * 4 : (j / 2) * 32 + (l & 3) * 8 + (j % 2) * 4;
+        const int d = C::kPanelBytes == 64 ? lt * 16 + j * 4
+                      : E4M3               ? (2 * lt + j / 4) * 16 + (j % 4) * 4
+                                           : (j / 4) * 64 + (2 * lt + (j % 4) / 2) * 8 + (j % 2) * 4;
         uint2 w = make_uint2(0u, 0u);
         if (r0 + r <= r1) {
             w = *reinterpret_cast<const uint2 *>(q_row(r) + d);
             if constexpr (E4M3) {
-                const float f = 1.f / st.qf[r];
+                const float f = 1.f / ms.qf[r];
                 w.x = pack_f16x2(__uint_as_float(w.x << 16) * f, __uint_as_float(w.x & 0xFFFF0000u) * f);
                 w.y = pack_f16x2(__uint_as_float(w.y << 16) * f, __uint_as_float(w.y & 0xFFFF0000u) * f);
             }
@@ -271,10 +306,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
         qs[i] = w;
     }
     __syncthreads();
+    uint2 qr[NT == 1 ? KS : 1];  // one row tile: the operand stays in registers
+    if constexpr (NT == 1) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qr[s] = qs[s * 32 + lane];
+    }
 
     // this thread's rows: columns 2t and 2t + 1 of every row tile
-    float slope[NT][2], qscale[NT][2];
-    int pos[NT][2], seen[NT][2];  // position, and the last kv it keeps (-1: nothing)
+    float slope[NT][2], qscale[NT][2];  // in base-2 units
+    int pos[NT][2], seen[NT][2];        // position, and the last kv it keeps (-1: nothing)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -284,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
             const int h = hk * p.G + (live ? row % p.G : 0);
             pos[nt][u] = n - p.Q + (live ? row / p.G : 0);
             seen[nt][u] = live && pos[nt][u] >= 0 ? (p.causal ? pos[nt][u] : n - 1) : -1;
-            qscale[nt][u] = p.scale * (E4M3 ? st.qf[r] : 1.f);
-            slope[nt][u] = exp2f(-8.f * (float)(h + 1) / (float)p.Hq);
+            qscale[nt][u] = p.scale * (E4M3 ? ms.qf[r] : 1.f) * (p.score_kind == FLEX_SCORE_SOFTCAP ? 1.f : kLog2e);
+            slope[nt][u] = exp2f(-8.f * (float)(h + 1) / (float)p.Hq) * kLog2e;
         }
 
     float m[NT][2], l[NT][2], acc[NT][KS][4], vref = 0.f;
@@ -296,31 +336,58 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
 #pragma unroll
         for (int i = 0; i < KS; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
     }
+    // byte offsets of this thread's pieces within a staged tile
+    const uint32_t ring_at = smem_u32(ring);
+    uint32_t koff[2], voff[2];
+    if constexpr (C::kPanelBytes == 128) {
+        koff[0] = g * 128 + (((2 * t) ^ g) * 16);
+        koff[1] = g * 128 + (((2 * t + 1) ^ g) * 16);
+        voff[0] = 2 * t * 128 + ((g ^ (2 * t)) * 16);
+        voff[1] = (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) * 16);
+    } else {
+        koff[0] = koff[1] = g * 64 + ((t ^ (g >> 1)) * 16);
+        voff[0] = 2 * t * 64 + (((g >> 1) ^ t) * 16) + (g & 1) * 8;
+        voff[1] = voff[0] + 64;
+    }
 
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true, refetched = false;  // refetched: this slot's next keys were already asked for
     for (; tile < ntiles; tile += step) {
         const int base = tile_base(tile);
-        const bool more = tile + step < ntiles;
-        const int next = more ? tile_base(tile + step) : 0;
-        if (more) lookup(next, ph_next);
-        float ks[SUB], vs[SUB];
+        const bool more = tile + ST * step < ntiles;
+        const int next = more ? tile_base(tile + ST * step) : 0;
+        int ph_next[SUB];
+        float ks_next[SUB], vs_next[SUB];
+        if (more && ahead % 32 == 0) lookup(tile + ST * step);
+        take(ahead % 32, ph_next, ks_next, vs_next);
+        ++ahead;
         bool whole = base + C::kTokens <= all_hi && (base >= all_lo || base + C::kTokens <= p.sinks);
 #pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-            whole = whole && ph[j] >= 0;
-            ks[j] = vs[j] = 1.f;
-            if constexpr (E4M3) {
-                ks[j] = ph[j] >= 0 ? __ldg(p.cache.k_scale + ph[j]) : 0.f;
-                vs[j] = ph[j] >= 0 ? __ldg(p.cache.v_scale + ph[j]) : 0.f;
-            }
-        }
+        for (int j = 0; j < SUB; ++j) whole = whole && ph[0][j] >= 0;
+        const uint32_t k_at = ring_at + slot * 2 * C::kTile, v_at = k_at + C::kTile;
         // ---- S^T = K Q^T
+        if (!__all_sync(0xffffffffu, mbar_wait(&ms.k_full[warp][slot], phase, &ms.abort))) {
+            ok = false;
+            break;
+        }
         float x[NT][SUB][4];
+        uint32_t kw[SUB][2][C::kKWords];
 #pragma unroll
         for (int j = 0; j < SUB; ++j) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) x[nt][j][0] = x[nt][j][1] = x[nt][j][2] = x[nt][j][3] = 0.f;
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int c = 0; c < C::kKWords / 4; ++c)
+                    load_shared<16>(&kw[j][r][4 * c], k_at + koff[c & 1] + (c >> 1) * C::kTokens * C::kPanelBytes +
+                                                          (16 * j + 8 * r) * C::kPanelBytes);
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) {
                 uint32_t a0, a1, a2, a3;
                 if constexpr (E4M3) {
                     a0 = e4m3_lo(kw[j][0][s]);
@@ -335,42 +402,65 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const uint2 q = qs[(nt * KS + s) * 32 + lane];
+                    const uint2 q = NT == 1 ? qr[NT == 1 ? s : 0] : qs[(nt * KS + s) * 32 + lane];
                     mma16816<E4M3>(x[nt][j], a0, a1, a2, a3, q.x, q.y);
                 }
             }
-        }
-        if (more) load_k(next, ph_next);
+        __syncwarp();  // every lane has read the keys
+        if (more) fetch(&map_k, ring + slot * 2 * C::kTile, &ms.k_full[warp][slot], next, ph_next);
 
         // ---- scores in base-2 units, masked
         float top[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            top[nt][0] = top[nt][1] = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < SUB; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int u = e & 1, kv = base + 16 * j + g + (e >> 1) * 8;
-                    float s = x[nt][j][e] * (qscale[nt][u] * ks[j]);
-                    if (p.score_kind == FLEX_SCORE_SOFTCAP)
-                        s = p.score_param * tanhf(s / p.score_param);
-                    else if (p.score_kind == FLEX_SCORE_ALIBI)
-                        s -= slope[nt][u] * (float)(pos[nt][u] - kv);
-                    s *= kLog2e;
-                    if (!whole) {
-                        const bool keep = ph[j] >= 0 && kv <= seen[nt][u] &&
+                for (int e = 0; e < 4; ++e) x[nt][j][e] *= qscale[nt][e & 1] * ks[0][j];
+        if (p.score_kind == FLEX_SCORE_SOFTCAP) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < SUB; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[nt][j][e] = p.score_param * tanhf(x[nt][j][e] / p.score_param) * kLog2e;
+        } else if (p.score_kind == FLEX_SCORE_ALIBI) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < SUB; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[nt][j][e] -= slope[nt][e & 1] * (float)(pos[nt][e & 1] - (base + 16 * j + g + (e >> 1) * 8));
+        }
+        if (!whole) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < SUB; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int u = e & 1, kv = base + 16 * j + g + (e >> 1) * 8;
+                        const bool keep = ph[0][j] >= 0 && kv <= seen[nt][u] &&
                                           (pos[nt][u] - kv < p.window || kv < p.sinks);
-                        if (!keep) s = -INFINITY;
+                        if (!keep) x[nt][j][e] = -INFINITY;
                     }
-                    x[nt][j][e] = s;
-                    top[nt][u] = fmaxf(top[nt][u], s);
-                }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            top[nt][0] = fmaxf(x[nt][0][0], x[nt][0][2]);
+            top[nt][1] = fmaxf(x[nt][0][1], x[nt][0][3]);
+#pragma unroll
+            for (int j = 1; j < SUB; ++j) {
+                top[nt][0] = fmax3(top[nt][0], x[nt][j][0], x[nt][j][2]);
+                top[nt][1] = fmax3(top[nt][1], x[nt][j][1], x[nt][j][3]);
+            }
         }
         // ---- running maximum and V scale
-        float vmax = vs[0];
+        float vmax = vs[0][0];
 #pragma unroll
-        for (int j = 1; j < SUB; ++j) vmax = fmaxf(vmax, vs[j]);
+        for (int j = 1; j < SUB; ++j) vmax = fmaxf(vmax, vs[0][j]);
         bool raise = vmax > vref;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) raise |= top[nt][0] > m[nt][0] + kRaise || top[nt][1] > m[nt][1] + kRaise;
@@ -400,39 +490,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
                 }
             }
         }
-        // ---- values of tokens that no row keeps: zero, whatever lies there
-        bool mixed = false;  // a token that some rows keep and some do not has a value that is not finite
-        if (!whole) {
-#pragma unroll
-            for (int j = 0; j < SUB; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int kv = base + 16 * j + 2 * t + (r & 1) + (r >> 1) * 8;
-                    const bool any = kv < hi && (kv >= lo_min || kv < send);
-                    const bool every = kv < all_hi && (kv >= all_lo || kv < p.sinks);
-                    bool odd = false;
-#pragma unroll
-                    for (int c = 0; c < C::kVBytes / 4; ++c) {
-                        if (!any) vw[j][r][c] = 0u;
-                        const uint32_t w = vw[j][r][c];
-                        if constexpr (E4M3)
-                            odd |= __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
-                        else
-                            odd |= __vcmpgeu2(w & 0x7FFF7FFFu, 0x7F807F80u) != 0u;
-                    }
-                    mixed |= odd && !every;
-                }
-            mixed = __any_sync(0xffffffffu, mixed);
-        }
         // ---- P, its sum, and P^T as operand
         uint32_t pb[NT][SUB][2];
-        float vf[SUB];
 #pragma unroll
-        for (int j = 0; j < SUB; ++j) vf[j] = E4M3 && vref > 0.f ? vs[j] / vref : 0.f;
+        for (int j = 0; j < SUB; ++j) {
+            const float vf = !E4M3 || vs[0][j] == vref ? 1.f : vs[0][j] / vref;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < SUB; ++j) {
+            for (int nt = 0; nt < NT; ++nt) {
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -440,90 +504,152 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
                     l[nt][e & 1] += w[e];
                 }
                 if constexpr (E4M3) {
-                    pb[nt][j][0] = transpose8(pack_f16x2(w[0] * vf[j], w[1] * vf[j]));
-                    pb[nt][j][1] = transpose8(pack_f16x2(w[2] * vf[j], w[3] * vf[j]));
+                    pb[nt][j][0] = transpose8(pack_f16x2(w[0] * vf, w[1] * vf));
+                    pb[nt][j][1] = transpose8(pack_f16x2(w[2] * vf, w[3] * vf));
                 } else {
                     pb[nt][j][0] = transpose8(pack_bf16x2(w[0], w[1]));
                     pb[nt][j][1] = transpose8(pack_bf16x2(w[2], w[3]));
                 }
             }
+        }
         // ---- O^T += V^T P^T
-        auto product = [&](const uint32_t (&v)[SUB][4][C::kVBytes / 4], const uint32_t (&w)[NT][SUB][2]) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ms.v_full[warp][slot], phase, &ms.abort))) {
+            ok = false;
+            refetched = more;
+            break;
+        }
+        auto load_v = [&](int j, uint32_t (&v)[4][C::kVBytes / 4]) {
 #pragma unroll
-            for (int j = 0; j < SUB; ++j)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    uint32_t a0, a1, a2, a3;
-                    if constexpr (E4M3) {
-                        const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
-                        const uint32_t lo2 = prmt(v[j][0][i / 2], v[j][1][i / 2], sel);
-                        const uint32_t hi2 = prmt(v[j][2][i / 2], v[j][3][i / 2], sel);
-                        a0 = e4m3_lo(lo2);
-                        a1 = e4m3_hi(lo2);
-                        a2 = e4m3_lo(hi2);
-                        a3 = e4m3_hi(hi2);
-                    } else {
-                        a0 = prmt(v[j][0][i], v[j][1][i], 0x5410u);
-                        a1 = prmt(v[j][0][i], v[j][1][i], 0x7632u);
-                        a2 = prmt(v[j][2][i], v[j][3][i], 0x5410u);
-                        a3 = prmt(v[j][2][i], v[j][3][i], 0x7632u);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816<E4M3>(acc[nt][i], a0, a1, a2, a3, w[nt][j][0], w[nt][j][1]);
-                }
+                for (int c = 0; c < C::kVBytes / C::kVLoad; ++c)
+                    load_shared<C::kVLoad>(&v[r][c * 4], v_at + voff[r & 1] + c * C::kTokens * C::kPanelBytes +
+                                                             (16 * j + 8 * (r >> 1)) * C::kPanelBytes);
         };
-        if (!mixed) {
-            product(vw, pb);
-        } else {
-            // one query token's rows at a time, with what they do not keep zeroed
-            for (int tok = tmin; tok <= tmax; ++tok) {
-                const int at = n - p.Q + tok;
-                uint32_t v2[SUB][4][C::kVBytes / 4], p2[NT][SUB][2];
+        auto product = [&](const uint32_t (&v)[4][C::kVBytes / 4], int j, auto &&weight) {
 #pragma unroll
-                for (int j = 0; j < SUB; ++j) {
+            for (int i = 0; i < KS; ++i) {
+                uint32_t a0, a1, a2, a3;
+                if constexpr (E4M3) {
+                    const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
+                    const uint32_t lo2 = prmt(v[0][i / 2], v[1][i / 2], sel);
+                    const uint32_t hi2 = prmt(v[2][i / 2], v[3][i / 2], sel);
+                    a0 = e4m3_lo(lo2);
+                    a1 = e4m3_hi(lo2);
+                    a2 = e4m3_lo(hi2);
+                    a3 = e4m3_hi(hi2);
+                } else {
+                    a0 = prmt(v[0][i], v[1][i], 0x5410u);
+                    a1 = prmt(v[0][i], v[1][i], 0x7632u);
+                    a2 = prmt(v[2][i], v[3][i], 0x5410u);
+                    a3 = prmt(v[2][i], v[3][i], 0x7632u);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma16816<E4M3>(acc[nt][i], a0, a1, a2, a3, weight(nt, 0), weight(nt, 1));
+            }
+        };
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) {
+                uint32_t v[4][C::kVBytes / 4];
+                load_v(j, v);
+                product(v, j, [&](int nt, int e) { return pb[nt][j][e]; });
+            }
+        } else {
+            // values of tokens that no row keeps: zero, whatever lies there
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) {
+                uint32_t v[4][C::kVBytes / 4];
+                load_v(j, v);
+                bool mixed = false;  // a token that some rows keep and some do not has a value that is not finite
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int kv = base + 16 * j + 2 * t + (r & 1) + (r >> 1) * 8;
+                    const bool any = ph[0][j] >= 0 && kv < hi && (kv >= lo_min || kv < send);
+                    const bool every = kv < all_hi && (kv >= all_lo || kv < p.sinks);
+                    bool odd = false;
+#pragma unroll
+                    for (int c = 0; c < C::kVBytes / 4; ++c) {
+                        if (!any) v[r][c] = 0u;
+                        if constexpr (E4M3)
+                            odd |= __vcmpeq4(v[r][c] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
+                        else
+                            odd |= __vcmpgeu2(v[r][c] & 0x7FFF7FFFu, 0x7F807F80u) != 0u;
+                    }
+                    mixed |= odd && !every;
+                }
+                if (!__any_sync(0xffffffffu, mixed)) {
+                    product(v, j, [&](int nt, int e) { return pb[nt][j][e]; });
+                    continue;
+                }
+                // one query token's rows at a time, with what they do not keep
+                // zeroed; the other rows' columns keep their sums, since their
+                // zero weights must not meet a value that is not finite either
+#pragma unroll 1
+                for (int tok = tmin; tok <= tmax; ++tok) {
+                    const int at = n - p.Q + tok;
+                    float saved[NT][KS][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < KS; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) saved[nt][i][e] = acc[nt][i][e];
+                    load_v(j, v);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int kv = base + 16 * j + 2 * t + (r & 1) + (r >> 1) * 8;
-                        const bool keep = p.causal ? kv <= at && (at - kv < p.window || kv < p.sinks) : at >= 0 && kv < n;
+                        const bool keep =
+                            p.causal ? kv <= at && (at - kv < p.window || kv < p.sinks) : at >= 0 && kv < n;
 #pragma unroll
-                        for (int c = 0; c < C::kVBytes / 4; ++c) v2[j][r][c] = keep ? vw[j][r][c] : 0u;
+                        for (int c = 0; c < C::kVBytes / 4; ++c) v[r][c] = keep ? v[r][c] : 0u;
                     }
-                    // the operand's column is the lane's g
+                    product(v, j, [&](int nt, int e) {  // the operand's column is the lane's g
+                        return (r0 + nt * 8 + g) / p.G == tok ? pb[nt][j][e] : 0u;
+                    });
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const bool own = (r0 + nt * 8 + g) / p.G == tok;
-                        p2[nt][j][0] = own ? pb[nt][j][0] : 0u;
-                        p2[nt][j][1] = own ? pb[nt][j][1] : 0u;
-                    }
-                }
-                // a zero weight of another token's row must not meet a value
-                // that is not finite either: those rows' columns keep their sums
-                float saved[NT][KS][4];
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                        for (int u = 0; u < 2; ++u)
+                            if ((r0 + nt * 8 + 2 * t + u) / p.G != tok) {
 #pragma unroll
-                    for (int i = 0; i < KS; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) saved[nt][i][e] = acc[nt][i][e];
-                product(v2, p2);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        if ((r0 + nt * 8 + 2 * t + u) / p.G != tok) {
-#pragma unroll
-                            for (int i = 0; i < KS; ++i) {
-                                acc[nt][i][u] = saved[nt][i][u];
-                                acc[nt][i][u + 2] = saved[nt][i][u + 2];
+                                for (int i = 0; i < KS; ++i) {
+                                    acc[nt][i][u] = saved[nt][i][u];
+                                    acc[nt][i][u + 2] = saved[nt][i][u + 2];
+                                }
                             }
-                        }
+                }
             }
         }
-        if (more) {
-            load_v(next, ph_next);
+        __syncwarp();  // every lane has read the values
+        if (more) fetch(&map_v, ring + slot * 2 * C::kTile + C::kTile, &ms.v_full[warp][slot], next, ph_next);
 #pragma unroll
-            for (int j = 0; j < SUB; ++j) ph[j] = ph_next[j];
+        for (int s = 0; s + 1 < ST; ++s)
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) ph[s][j] = ph[s + 1][j], ks[s][j] = ks[s + 1][j], vs[s][j] = vs[s + 1][j];
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) ph[ST - 1][j] = ph_next[j], ks[ST - 1][j] = ks_next[j], vs[ST - 1][j] = vs_next[j];
+        if (++slot == ST) {
+            slot = 0;
+            phase ^= 1u;
         }
+    }
+    if (!ok) {
+        // a copy did not arrive in time: report it, and give the copies still
+        // under way (this slot's and the later ones') the same time again
+        // before shared memory is used for anything else
+        ms.abort = 1;
+        if (lane == 0) atomicExch(p.status, kDeviceTimeout);
+        volatile int keep_waiting = 0;
+        for (int s = 0; s < ST; ++s) {
+            const int at = (slot + s) % ST;
+            const uint32_t par = phase ^ (slot + s >= ST ? 1u : 0u);
+            if (tile + s * step >= ntiles) break;
+            mbar_wait(&ms.k_full[warp][at], par, &keep_waiting);
+            mbar_wait(&ms.v_full[warp][at], par, &keep_waiting);
+        }
+        if (refetched) mbar_wait(&ms.k_full[warp][slot], phase ^ 1u, &keep_waiting);
     }
 
     // ------------------------------------------------- join the warps, the CTAs
@@ -534,20 +660,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[nt][u] += __shfl_xor_sync(0xffffffffu, l[nt][u], o);
             if (g == 0) {
-                st.m[warp][nt * 8 + 2 * t + u] = m[nt][u];
-                st.l[warp][nt * 8 + 2 * t + u] = l[nt][u];
+                ms.m[warp][nt * 8 + 2 * t + u] = m[nt][u];
+                ms.l[warp][nt * 8 + 2 * t + u] = l[nt][u];
             }
         }
-    __syncthreads();  // statistics written; Q operand no longer read
+    __syncthreads();  // statistics written; the rings and the Q operand no longer read
     float *accs = reinterpret_cast<float *>(smem);
     if (threadIdx.x < C::kRows) {
-        float top = st.m[0][threadIdx.x], sum = 0.f;
+        float top = ms.m[0][threadIdx.x], sum = 0.f;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, st.m[w][threadIdx.x]);
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, ms.m[w][threadIdx.x]);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += st.l[w][threadIdx.x] * exp2f(st.m[w][threadIdx.x] - top);
-        st.cm[threadIdx.x] = top;
-        st.cl[threadIdx.x] = sum;
+        for (int w = 0; w < kWarps; ++w) sum += ms.l[w][threadIdx.x] * exp2f(ms.m[w][threadIdx.x] - top);
+        ms.cm[threadIdx.x] = top;
+        ms.cl[threadIdx.x] = sum;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -555,9 +681,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int r = nt * 8 + 2 * t + u;
-            float top = st.m[0][r];
+            float top = ms.m[0][r];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, st.m[w][r]);
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, ms.m[w][r]);
             f[u] = exp2f(m[nt][u] - top) * (E4M3 ? vref : 1.f);
         }
 #pragma unroll
@@ -588,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
             s.y += o.y;
         }
         if (csize == 1)
-            store(r, d, s.x, s.y, st.cm[r], st.cl[r]);
+            store(r, d, s.x, s.y, ms.cm[r], ms.cl[r]);
         else
             *reinterpret_cast<float2 *>(accs + r * C::kAccStride + d) = s;
     }
@@ -598,17 +724,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache_attention_ker
     for (int i = rank * kThreads + threadIdx.x; i < pairs; i += csize * kThreads) {
         const int r = i / (D / 2), d = 2 * (i % (D / 2));
         float top = -FLT_MAX, sum = 0.f, a = 0.f, z = 0.f;
-        for (int c = 0; c < csize; ++c) top = fmaxf(top, *cluster.map_shared_rank(&st.cm[r], c));
+        for (int c = 0; c < csize; ++c) top = fmaxf(top, *cluster.map_shared_rank(&ms.cm[r], c));
         for (int c = 0; c < csize; ++c) {
-            const float f = exp2f(*cluster.map_shared_rank(&st.cm[r], c) - top);
+            const float f = exp2f(*cluster.map_shared_rank(&ms.cm[r], c) - top);
             const float2 o = *reinterpret_cast<float2 *>(cluster.map_shared_rank(accs + r * C::kAccStride + d, c));
-            sum += f * *cluster.map_shared_rank(&st.cl[r], c);
+            sum += f * *cluster.map_shared_rank(&ms.cl[r], c);
             a += f * o.x;
             z += f * o.y;
         }
         store(r, d, a, z, top, sum);
     }
     cluster.sync();  // no CTA leaves while its shared memory is read
+}
+
+// The cache's keys or values as [pages * heads][page][D]: boxes of box_rows
+// tokens by one panel.
+template <int D, bool E4M3>
+bool make_cache_map(CUtensorMap *map, const void *base, const KvCache &c, int box_rows) {
+    using C = Cfg<D, E4M3, 1>;
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)c.page, (uint64_t)c.num_pages * c.H};
+    const uint64_t strides[2] = {(uint64_t)C::kRowBytes, (uint64_t)C::kRowBytes * c.page};
+    const uint32_t box[3] = {(uint32_t)(C::kPanelBytes / C::kElem), (uint32_t)box_rows, 1};
+    return make_tile_map_3d(map, base, E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims,
+                            strides, box,
+                            C::kPanelBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 template <int D, bool E4M3, int NT>
@@ -629,6 +768,11 @@ cudaError_t launch_cache(const CacheAttnProblem &p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e == cudaSuccess && csize > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
+    const int box_rows = p.cache.page < C::kTokens ? p.cache.page : C::kTokens;
+    CUtensorMap map_k, map_v;
+    if (!make_cache_map<D, E4M3>(&map_k, p.cache.k, p.cache, box_rows) ||
+        !make_cache_map<D, E4M3>(&map_v, p.cache.v, p.cache, box_rows))
+        return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * csize));
     cfg.blockDim = dim3(kThreads);
@@ -640,7 +784,7 @@ cudaError_t launch_cache(const CacheAttnProblem &p, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, csize, row_tiles);
+    return cudaLaunchKernelEx(&cfg, kernel, map_k, map_v, p, csize, row_tiles, box_rows);
 }
 
 template <int D, bool E4M3>

@@ -53,6 +53,7 @@ struct CacheAttnProblem {
     float score_param, scale;
     uint16_t *out;
     float *lse;
+    int *status;                     // device status word
 };
 
 cudaError_t launch_rope(const RopeProblem &p, int dtype, cudaStream_t stream);
