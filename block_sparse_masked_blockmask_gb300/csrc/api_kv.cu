@@ -1,7 +1,7 @@
 // C-ABI layer of the rotary positions and the paged key/value cache
 // (include/flexattn.h): argument checks on the host and dispatch to the
-// kernels.  None of these calls synchronises; only the attention uses a
-// workspace, the per-device status word.
+// kernels.  None of these calls synchronises, allocates (but the per-device
+// status word of the attention, on its first call) or keeps state.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -75,16 +75,20 @@ int rope(const flex_tensor *q, const flex_tensor *k, const flex_rope_params *r, 
     return launch_rope(p, q->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FLEX_OK : FLEX_ERR_CUDA;
 }
 
-int check_cache(const flex_kv_cache *c, const int32_t *page_table, int32_t max_pages, const int32_t *lens) {
-    if (!c || !c->k || !c->v || !page_table || !lens) return FLEX_ERR_INVALID_ARG;
+int check_tables(const int32_t *page_table, const int32_t *lens) {
+    if (!page_table || !lens) return FLEX_ERR_INVALID_ARG;
+    return aligned(page_table, 4) && aligned(lens, 4) ? FLEX_OK : FLEX_ERR_ALIGNMENT;
+}
+
+int check_cache(const flex_kv_cache *c, int32_t max_pages) {
+    if (!c || !c->k || !c->v) return FLEX_ERR_INVALID_ARG;
     if (c->dtype != FLEX_DTYPE_BF16 && c->dtype != FLEX_DTYPE_E4M3) return FLEX_ERR_INVALID_ARG;
     if (c->dtype == FLEX_DTYPE_E4M3 && (!c->k_scale || !c->v_scale)) return FLEX_ERR_INVALID_ARG;
     if (c->num_pages <= 0 || c->H <= 0 || c->page_size <= 0 || c->D <= 0 || max_pages <= 0) return FLEX_ERR_SHAPE;
     if (c->D != 64 && c->D != 128) return FLEX_ERR_UNSUPPORTED;
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return FLEX_ERR_UNSUPPORTED;
     if (c->H > 32767 || (int64_t)c->num_pages * c->H > INT32_MAX || (int64_t)max_pages * c->page_size > kMaxCacheLen) return FLEX_ERR_UNSUPPORTED;
-    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
-        !aligned(page_table, 4) || !aligned(lens, 4))
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
         return FLEX_ERR_ALIGNMENT;
     return FLEX_OK;
 }
@@ -94,6 +98,46 @@ KvCache cache_of(const flex_kv_cache *c) {
     while ((1 << shift) < c->page_size) ++shift;
     return KvCache{c->num_pages, c->H, c->page_size, c->D, shift, static_cast<uint8_t *>(c->k),
                    static_cast<uint8_t *>(c->v), c->k_scale, c->v_scale};
+}
+
+// The checks of sizes, types and mask that the attention and its workspace
+// share; on success p holds what they describe.
+int cache_problem(const flex_tensor *q, const flex_kv_cache *cache, int32_t max_pages, int32_t mask_kind,
+                  const flex_mask_params *params, CacheAttnProblem &p) {
+    int rc = check_cache(cache, max_pages);
+    if (rc == FLEX_OK) rc = check_dtype_dim(q);
+    if (rc != FLEX_OK) return rc;
+    if (q->dtype != FLEX_DTYPE_BF16) return FLEX_ERR_UNSUPPORTED;
+    switch (mask_kind) {
+        case FLEX_MASK_CAUSAL:
+        case FLEX_MASK_ALL:
+            break;
+        case FLEX_MASK_SLIDING_WINDOW:
+        case FLEX_MASK_WINDOW_SINKS:
+            if (!params || !valid_window(mask_kind, *params)) return FLEX_ERR_INVALID_ARG;
+            break;
+        case FLEX_MASK_CAUSAL_PREFIX:
+        case FLEX_MASK_DOCUMENT:
+            return FLEX_ERR_UNSUPPORTED;
+        default:
+            return FLEX_ERR_INVALID_ARG;
+    }
+    if (q->shape[3] != cache->D || q->shape[1] % cache->H != 0) return FLEX_ERR_SHAPE;
+    if ((rc = check_tensor(q, FLEX_DTYPE_BF16, q->shape[0], q->shape[1], q->shape[2], cache->D)) != FLEX_OK) return rc;
+    p.B = (int)q->shape[0];
+    p.Hq = (int)q->shape[1];
+    p.G = p.Hq / cache->H;
+    p.Q = (int)q->shape[2];
+    // (sequence, head, row tile) triples along grid.x
+    if ((int64_t)p.Q * p.G > kMaxCacheLen || (int64_t)p.B * cache->H * (((int64_t)p.Q * p.G + 7) / 8) > INT32_MAX)
+        return FLEX_ERR_UNSUPPORTED;
+    p.cache = cache_of(cache);
+    p.max_pages = max_pages;
+    const bool windowed = mask_kind == FLEX_MASK_SLIDING_WINDOW || mask_kind == FLEX_MASK_WINDOW_SINKS;
+    p.window = windowed ? params->window : INT_MAX;
+    p.sinks = mask_kind == FLEX_MASK_WINDOW_SINKS ? params->prefix : 0;
+    p.causal = mask_kind != FLEX_MASK_ALL;
+    return FLEX_OK;
 }
 
 }  // namespace
@@ -143,7 +187,8 @@ int flex_rope_bwd(const flex_tensor *dq, const flex_tensor *dk, const flex_rope_
 int flex_kv_cache_append(const flex_kv_cache *cache, const flex_tensor *k, const flex_tensor *v,
                          const int32_t *page_table, int32_t max_pages, const int32_t *cache_lens,
                          const int32_t *new_lens, const flex_rope_params *r, void *stream) {
-    int rc = check_cache(cache, page_table, max_pages, cache_lens);
+    int rc = check_cache(cache, max_pages);
+    if (rc == FLEX_OK) rc = check_tables(page_table, cache_lens);
     if (rc != FLEX_OK) return rc;
     if ((rc = check_dtype_dim(k)) != FLEX_OK) return rc;
     if (k->shape[3] != cache->D || k->shape[1] != cache->H) return FLEX_ERR_SHAPE;
@@ -174,58 +219,41 @@ int flex_kv_cache_append(const flex_kv_cache *cache, const flex_tensor *k, const
                : FLEX_ERR_CUDA;
 }
 
+int flex_kv_cache_attention_workspace(const flex_tensor *q, const flex_kv_cache *cache, int32_t max_pages,
+                                      int32_t mask_kind, const flex_mask_params *params, int64_t *bytes) {
+    if (!bytes) return FLEX_ERR_INVALID_ARG;
+    CacheAttnProblem p = {};
+    const int rc = cache_problem(q, cache, max_pages, mask_kind, params, p);
+    if (rc != FLEX_OK) return rc;
+    *bytes = cache_attention_workspace(p, cache->dtype);
+    return FLEX_OK;
+}
+
 int flex_kv_cache_attention(const flex_tensor *q, const flex_kv_cache *cache, const int32_t *page_table,
                             int32_t max_pages, const int32_t *kv_lens, int32_t mask_kind,
                             const flex_mask_params *params, int32_t score_kind, float score_param, float scale,
-                            void *out, float *lse, void *stream) {
-    int rc = check_cache(cache, page_table, max_pages, kv_lens);
+                            void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream) {
+    CacheAttnProblem p = {};
+    int rc = cache_problem(q, cache, max_pages, mask_kind, params, p);
+    if (rc == FLEX_OK) rc = check_tables(page_table, kv_lens);
     if (rc != FLEX_OK) return rc;
-    if (!out || !lse) return FLEX_ERR_INVALID_ARG;
-    if ((rc = check_dtype_dim(q)) != FLEX_OK) return rc;
-    if (q->dtype != FLEX_DTYPE_BF16) return FLEX_ERR_UNSUPPORTED;
+    if (!out || !lse || !workspace) return FLEX_ERR_INVALID_ARG;
     if (score_kind < FLEX_SCORE_IDENTITY || score_kind > FLEX_SCORE_ALIBI) return FLEX_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return FLEX_ERR_INVALID_ARG;
     if (score_kind == FLEX_SCORE_SOFTCAP && !(score_param > 0.f && std::isfinite(score_param)))
         return FLEX_ERR_INVALID_ARG;
-    switch (mask_kind) {
-        case FLEX_MASK_CAUSAL:
-        case FLEX_MASK_ALL:
-            break;
-        case FLEX_MASK_SLIDING_WINDOW:
-        case FLEX_MASK_WINDOW_SINKS:
-            if (!params || !valid_window(mask_kind, *params)) return FLEX_ERR_INVALID_ARG;
-            break;
-        case FLEX_MASK_CAUSAL_PREFIX:
-        case FLEX_MASK_DOCUMENT:
-            return FLEX_ERR_UNSUPPORTED;
-        default:
-            return FLEX_ERR_INVALID_ARG;
-    }
-    if (q->shape[3] != cache->D || q->shape[1] % cache->H != 0) return FLEX_ERR_SHAPE;
-    if ((rc = check_tensor(q, FLEX_DTYPE_BF16, q->shape[0], q->shape[1], q->shape[2], cache->D)) != FLEX_OK) return rc;
-    if (!aligned(out, 16) || !aligned(lse, 4)) return FLEX_ERR_ALIGNMENT;
-    if (q->shape[2] > kMaxCacheLen) return FLEX_ERR_UNSUPPORTED;
-    CacheAttnProblem p = {};
-    p.B = (int)q->shape[0];
-    p.Hq = (int)q->shape[1];
-    p.G = p.Hq / cache->H;
-    p.Q = (int)q->shape[2];
-    if ((int64_t)p.Q * p.G > kMaxCacheLen) return FLEX_ERR_UNSUPPORTED;
-    p.cache = cache_of(cache);
+    if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16)) return FLEX_ERR_ALIGNMENT;
+    if (workspace_bytes < cache_attention_workspace(p, cache->dtype)) return FLEX_ERR_SHAPE;
     p.q = static_cast<const uint16_t *>(q->data);
     take_strides(q, p.q_stride);
     p.page_table = page_table;
-    p.max_pages = max_pages;
     p.kv_lens = kv_lens;
-    const bool windowed = mask_kind == FLEX_MASK_SLIDING_WINDOW || mask_kind == FLEX_MASK_WINDOW_SINKS;
-    p.window = windowed ? params->window : INT_MAX;
-    p.sinks = mask_kind == FLEX_MASK_WINDOW_SINKS ? params->prefix : 0;
-    p.causal = mask_kind != FLEX_MASK_ALL;
     p.score_kind = score_kind;
     p.score_param = score_param;
     p.scale = scale;
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
+    p.workspace = workspace;
     p.status = device_status_word(&rc);
     if (!p.status) return rc;
     return launch_cache_attention(p, cache->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FLEX_OK

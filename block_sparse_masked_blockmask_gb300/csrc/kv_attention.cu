@@ -30,9 +30,15 @@
 //    operand P^T.  Statistics, sums and accumulators are float32.
 //  * The maximum is only raised when a score exceeds it by 2^8 (votes instead of
 //    reductions on most steps); weights then stay below 2^8.
-//  * A sequence's tokens are split over the warps of a cluster of up to 16 CTAs,
-//    tile by tile; the partial results meet in distributed shared memory, so
-//    there is no workspace, no second launch and no atomic.
+//  * The steps (4 KB of keys and 4 KB of values) of all sequences, heads and
+//    row tiles form one list, which the warps of one wave of CTAs share out
+//    evenly, so that ragged batches and a few long sequences fill the SMs
+//    alike.  A warp works alone: its TMA-filled ring runs on from one (sequence,
+//    head, row tile) to the next, and no barrier joins it to other warps.
+//    Where it covers all steps of one it writes the rows; where a cut falls
+//    inside one, the pieces' statistics and accumulators go to the workspace
+//    and a second, dependent launch joins them.  Nothing is joined by atomics:
+//    results do not depend on the order in which warps run.
 //  * Only tiles at an edge (the last tokens, a window's ends, a bad page)
 //    evaluate the mask; there the values of tokens that no row keeps are
 //    zeroed, so that whatever lies in those slots has no effect, and where
@@ -41,7 +47,6 @@
 #include <cfloat>
 #include <climits>
 
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -53,8 +58,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kJoinThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Entering and finishing a (sequence, head, row tile) costs a warp about as
+// much time as two steps: the list counts that many more for each.
+constexpr int kEnterCost = 2;
+constexpr int kMinShare = 4;  // fewest of the list's units a warp takes
 constexpr float kRaise = 8.f;  // raise the running max only beyond 2^8
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -119,50 +129,85 @@ struct Cfg {
     static constexpr int kTile = 4096;                  // bytes of keys (of values) per step of a warp
     static constexpr int kTokens = kTile / kRowBytes;
     static constexpr int kSub = kTokens / 16;           // groups of 16 tokens per step
-    static constexpr int kStages = NT == 1 ? 2 : 3;     // steps in flight per warp
+    static constexpr int kStages = 2;                   // steps in flight per warp
     static constexpr int kSteps = D / 16;               // k16 steps of S, m16 tiles of O
     static constexpr int kKWords = kRowBytes / 16;      // words of one key a thread holds
     static constexpr int kVBytes = kRowBytes / 8;       // bytes of one value a thread holds
     static constexpr int kVLoad = kVBytes < 16 ? 8 : 16;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kAccStride = D + 4;
-    // shared memory: the warps' rings (over them, at the end, the partial
-    // accumulators), then the Q operand
-    static constexpr int kRing = kWarps * kStages * 2 * kTile;
+    // shared memory of a warp: its ring and its Q operand
+    static constexpr int kRing = kStages * 2 * kTile;
     static constexpr int kQBytes = NT * kSteps * 32 * 8;
-    static_assert(kWarps * kRows * kAccStride * 4 <= kRing, "partial accumulators fit the rings");
-    static constexpr int kSmem = 1024 + kRing + kQBytes;  // 1024: alignment of the swizzle
+    static constexpr int kSmem = 1024 + kWarps * (kRing + kQBytes);  // 1024: alignment of the swizzle
 };
 
 struct Misc {
-    uint64_t k_full[kWarps][3], v_full[kWarps][3];
-    float m[kWarps][16], l[kWarps][16];  // per warp and row
-    float cm[16], cl[16];                // of the CTA
-    float qf[16];                        // the power of two taken off a query row
+    uint64_t k_full[kWarps][2], v_full[kWarps][2];
+    int64_t sums[kWarps];
     int abort;
 };
+
+// Steps of a sequence: tokens that any of its query rows keeps, [0, send) and
+// [lo_min, hi), in whole steps.
+struct Steps {
+    int n, hi, send, lo, nsink, count;
+    int64_t lo_min;
+    __device__ __forceinline__ int base(int i, int tokens) const {
+        return i < nsink ? i * tokens : lo + (i - nsink) * tokens;
+    }
+};
+template <int TOKENS>
+__device__ __forceinline__ Steps steps_of(const CacheAttnProblem &p, int kv_len) {
+    Steps s;
+    s.n = (int)min((int64_t)max(kv_len, 0), (int64_t)p.max_pages * p.cache.page);
+    s.hi = s.n;  // the last query token is the last token
+    s.lo_min = p.causal ? max((int64_t)s.n - p.Q - p.window + 1, (int64_t)0) : 0;
+    s.lo = (int)min(s.lo_min, (int64_t)s.hi) / TOKENS * TOKENS;
+    s.send = min(p.sinks, s.hi);
+    s.nsink = (s.send + TOKENS - 1) / TOKENS;
+    if (s.nsink * (int64_t)TOKENS >= s.lo) {
+        s.nsink = 0;
+        s.lo = 0;
+    }
+    s.count = max(s.nsink + (s.hi - s.lo + TOKENS - 1) / TOKENS, 1);  // an empty sequence: one empty step
+    return s;
+}
+
+// The workspace: the size of a warp's share of the list, where each sequence
+// begins in it, and two partial results per warp (rows x (D + 2) floats:
+// accumulators, maximum, sum): of a piece that begins inside its (sequence,
+// head, row tile), and of one that begins with it but does not end it.
+__host__ __device__ constexpr int64_t workspace_partials(int64_t B) { return (8 * (B + 1) + 15) / 16 * 16; }
+__host__ __device__ constexpr int64_t partial_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
+
+// Two neighbouring output values of query row `row` of a head group, and its lse.
+template <int D>
+__device__ __forceinline__ void store_pair(const CacheAttnProblem &p, int b, int hk, int row, int d, float a, float z,
+                                           float top, float sum) {
+    const int64_t o = ((int64_t)b * p.Hq + hk * p.G + row % p.G) * p.Q + row / p.G;
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays
+    *reinterpret_cast<uint32_t *>(p.out + o * D + d) = pack_bf16x2(a * inv, z * inv);
+    if (d == 0) p.lse[o] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
 
 template <int D, bool E4M3, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     cache_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                           const CacheAttnProblem p, int csize, int row_tiles, int box_rows) {
+                           const CacheAttnProblem p, int row_tiles, int box_rows) {
     using C = Cfg<D, E4M3, NT>;
     constexpr int SUB = C::kSub, KS = C::kSteps, ST = C::kStages;
-    namespace cg = cooperative_groups;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Misc ms;
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint2 *qs = reinterpret_cast<uint2 *>(smem + C::kRing);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
-    const int rank = (int)(blockIdx.x % csize);
-    const int pair = (int)(blockIdx.x / csize);
-    const int rt = pair % row_tiles, bh = pair / row_tiles, hk = bh % p.cache.H, b = bh / p.cache.H;
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
+                    warp * C::kRing;
     const int page = p.cache.page;
-    const int kv_len = __ldg(p.kv_lens + b);
+    // the joining launch may start while this one runs: it waits for its end
+    asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
-        for (int i = 0; i < kWarps * 3; ++i) {
+        for (int i = 0; i < kWarps * ST; ++i) {
             mbar_init(&ms.k_full[0][0] + i, 1);
             mbar_init(&ms.v_full[0][0] + i, 1);
         }
@@ -170,43 +215,127 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         fence_barrier_init();
     }
 
-    // rows of this tile: r = query token * G + head within the group
-    const int rows = p.Q * p.G, r0 = rt * C::kRows, r1 = min(r0 + C::kRows, rows) - 1;
-    const int tmin = r0 / p.G, tmax = r1 / p.G;
-    const int n = (int)min((int64_t)max(kv_len, 0), (int64_t)p.max_pages * page);
-    // what any row of the tile keeps: [0, send) and [lo_min, hi)
-    const int hi = p.causal ? max(n - p.Q + tmax + 1, 0) : n;
-    const int64_t lo_min = p.causal ? max((int64_t)n - p.Q + tmin - p.window + 1, (int64_t)0) : 0;
-    int lo = (int)min(lo_min, (int64_t)hi) / C::kTokens * C::kTokens;
-    const int send = min(p.sinks, hi);
-    int nsink = (send + C::kTokens - 1) / C::kTokens;
-    if (nsink * (int64_t)C::kTokens >= lo) {
-        nsink = 0;
-        lo = 0;
+    // ---- the warp's share of the list.  Thread i adds up a run of sequences;
+    // the block's prefix sums then give the total and where a step falls.
+    const int pairs_per_seq = p.cache.H * row_tiles;  // (head, row tile) pairs, the row tiles innermost
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b_first = min((int)threadIdx.x * per, p.B), b_last = min(b_first + per, p.B);
+    auto seq_units = [&](int i) {
+        return (int64_t)(steps_of<C::kTokens>(p, __ldg(p.kv_lens + i)).count + kEnterCost) * pairs_per_seq;
+    };
+    int64_t mine = 0;
+    for (int i = b_first; i < b_last; ++i) mine += seq_units(i);
+    int64_t upto = mine;  // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
     }
-    const int ntiles = nsink + (hi - lo + C::kTokens - 1) / C::kTokens;
-    // what every row keeps, for tiles without mask work
-    const int all_hi = p.causal ? n - p.Q + tmin + 1 : (n - p.Q + tmin >= 0 ? n : 0);
-    const int64_t all_lo = p.causal ? (int64_t)n - p.Q + tmax - p.window + 1 : 0;
-    auto tile_base = [&](int i) { return i < nsink ? i * C::kTokens : lo + (i - nsink) * C::kTokens; };
+    if (lane == 31) ms.sums[warp] = upto;
+    __syncthreads();
+    int64_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += ms.sums[w];
+        total += ms.sums[w];
+    }
+    const int64_t workers = (int64_t)gridDim.x * kWarps;
+    const int64_t share = max((total + workers - 1) / workers, (int64_t)kMinShare);
+    int64_t *head = reinterpret_cast<int64_t *>(p.workspace);
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) head[0] = share;
+        int64_t at = before + upto - mine;
+        for (int i = b_first; i < b_last; ++i) {
+            head[1 + i] = at;
+            at += seq_units(i);
+        }
+    }
+    // neighbouring shares go to different CTAs, so that few steps spread over
+    // the SMs
+    const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
+    const int64_t begin = worker * share;
+    if (begin >= total) return;
+    // the sequence that `begin` falls in: first the block's warp, then its lane, then its run
+    int b = 0;
+    int64_t off = begin;
+    {
+        int64_t skipped = 0;
+        int w0 = 0;
+        while (w0 + 1 < kWarps && begin >= skipped + ms.sums[w0]) skipped += ms.sums[w0++];
+        off = begin - skipped;
+        b = w0 * 32 * per;
+        for (int i0 = 0; i0 < 32 * per; i0 += 32) {  // 32 sequences at a time
+            const int64_t size = b + lane < p.B ? seq_units(b + lane) : 0;
+            int64_t sum = size;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, sum > off);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                off -= __shfl_sync(0xffffffffu, sum - size, f);
+                b += f;
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, sum, 31);
+            b += 32;
+        }
+    }
 
-    const int *table = p.page_table + (int64_t)b * p.max_pages;
-    const int step = csize * kWarps;
-    int tile = rank * kWarps + warp;
-    // Of the 16-token groups of a step: page * heads + head, or -1 where there
-    // is nothing that a row keeps, and the page's scales.  The groups of one
-    // box share a page.  Lane i holds those of the warp's step 32 k + i, so that
-    // the loads' latencies are met once in 32 steps.
-    int ph_lane[SUB];
+    // from units of the list to the steps among them: those of this warp, and
+    // the first of them within its sequence
+    int steps = 0;
+    {
+        int64_t left = min(share, total - begin), from = off;
+        for (int i = b; left > 0; ++i) {
+            const int count = steps_of<C::kTokens>(p, __ldg(p.kv_lens + i)).count, unit = count + kEnterCost;
+            auto real = [&](int64_t o) { return o / unit * count + max((int)(o % unit) - kEnterCost, 0); };
+            const int64_t to = min(from + left, (int64_t)unit * pairs_per_seq);
+            const int64_t here = real(to) - real(from);
+            if (steps == 0) {
+                b = i;
+                off = real(from);
+            }
+            steps += (int)here;
+            left -= to - from;
+            from = 0;
+        }
+    }
+    if (steps == 0) return;
+
+    // ---- steps ahead of the computation.  Lane i looks up the warp's step
+    // 32 k + i, so that the loads' latencies are met once in 32 steps: its first
+    // token, and of its 16-token groups page * heads + head, or -1 where there
+    // is nothing that a row keeps, and the page's scales.  The groups of one box
+    // share a page.
+    int look_b = b;
+    int64_t look_off = off;
+    int looked = 0;
+    int base_lane = 0, ph_lane[SUB];
     float ks_lane[SUB], vs_lane[SUB];
-    auto lookup = [&](int first) {
-        const int mine = first + lane * step;
-        const int base = tile_base(mine);
+    auto lookup = [&]() {
+        int lb = look_b;
+        int64_t lo_ = look_off + lane;
+        Steps sq = steps_of<C::kTokens>(p, __ldg(p.kv_lens + lb));
+        while (lo_ >= (int64_t)sq.count * pairs_per_seq && lb + 1 < p.B) {
+            lo_ -= (int64_t)sq.count * pairs_per_seq;
+            sq = steps_of<C::kTokens>(p, __ldg(p.kv_lens + ++lb));
+        }
+        const bool live = looked + lane < steps;
+        const int pair = (int)(lo_ / sq.count), hk = pair / row_tiles, r0 = pair % row_tiles * C::kRows;
+        const int tmin = r0 / p.G, tmax = (min(r0 + C::kRows, p.Q * p.G) - 1) / p.G;
+        const int hi = p.causal ? max(sq.n - p.Q + tmax + 1, 0) : sq.n;
+        const int64_t lo_min = p.causal ? max((int64_t)sq.n - p.Q + tmin - p.window + 1, (int64_t)0) : 0;
+        const int send = min(p.sinks, hi);
+        base_lane = sq.base((int)(lo_ % sq.count), C::kTokens);
+        const int *table = p.page_table + (int64_t)lb * p.max_pages;
 #pragma unroll
         for (int j = 0; j < SUB; ++j) {
-            const int at = base + 16 * j, box = at & ~(box_rows - 1);
+            const int at = base_lane + 16 * j, box = at & ~(box_rows - 1);
             ph_lane[j] = -1;
-            if (mine < ntiles && box < hi && (box + box_rows > lo_min || box < send)) {
+            if (live && box < hi && (box + box_rows > lo_min || box < send)) {
                 const int id = __ldg(table + (at >> p.cache.page_shift));
                 if (id >= 0 && id < p.cache.num_pages) ph_lane[j] = id * p.cache.H + hk;
             }
@@ -220,16 +349,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                     vs_lane[j] = __ldg(p.cache.v_scale + ph_lane[j]);
                 }
         }
+        // the next batch begins where lane 31's successor would be
+        look_b = __shfl_sync(0xffffffffu, lb, 31);
+        look_off = __shfl_sync(0xffffffffu, lo_, 31) + 1;
+        looked += 32;
     };
-    auto take = [&](int i, int (&ph)[SUB], float (&ks)[SUB], float (&vs)[SUB]) {
-#pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-            ph[j] = __shfl_sync(0xffffffffu, ph_lane[j], i);
-            ks[j] = E4M3 ? __shfl_sync(0xffffffffu, ks_lane[j], i) : 1.f;
-            vs[j] = E4M3 ? __shfl_sync(0xffffffffu, vs_lane[j], i) : 1.f;
-        }
-    };
-    uint8_t *ring = smem + warp * ST * 2 * C::kTile;
     // one step's keys (or values) into ring slot s (lane 0)
     auto fetch = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int base, const int (&ph)[SUB]) {
         if (lane == 0) {
@@ -246,96 +370,34 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                                     c * (C::kPanelBytes / C::kElem), (base + 16 * j) & (page - 1), ph[j]);
         }
     };
-    __syncthreads();  // barriers initialised
-
-    // the first steps in flight; ph, ks, vs: of the current step and the ST - 1 behind it
-    int ph[ST][SUB];
+    // of the current step and the ST - 1 behind it
+    int base_of[ST], ph[ST][SUB];
     float ks[ST][SUB], vs[ST][SUB];
-    lookup(tile);
+    auto take_place = [&](int i, int &base, int (&to)[SUB]) {
+        base = __shfl_sync(0xffffffffu, base_lane, i);
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) to[j] = __shfl_sync(0xffffffffu, ph_lane[j], i);
+    };
+    auto take_scales = [&](int i, float (&k)[SUB], float (&v)[SUB]) {
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) {
+            k[j] = E4M3 ? __shfl_sync(0xffffffffu, ks_lane[j], i) : 1.f;
+            v[j] = E4M3 ? __shfl_sync(0xffffffffu, vs_lane[j], i) : 1.f;
+        }
+    };
+    lookup();
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
-        take(s, ph[s], ks[s], vs[s]);
-        if (tile + s * step < ntiles) {
-            const int base = tile_base(tile + s * step);
-            uint8_t *slot = ring + s * 2 * C::kTile;
-            fetch(&map_k, slot, &ms.k_full[warp][s], base, ph[s]);
-            fetch(&map_v, slot + C::kTile, &ms.v_full[warp][s], base, ph[s]);
+        take_place(s, base_of[s], ph[s]);
+        if (s < steps) {
+            uint8_t *dst = ring + s * 2 * C::kTile;
+            fetch(&map_k, dst, &ms.k_full[warp][s], base_of[s], ph[s]);
+            fetch(&map_v, dst + C::kTile, &ms.v_full[warp][s], base_of[s], ph[s]);
         }
     }
-    int ahead = ST;  // of the warp's steps, the next to be asked for
+#pragma unroll
+    for (int s = 0; s < ST; ++s) take_scales(s, ks[s], vs[s]);
 
-    // Q operand: the rows' largest magnitudes first (e4m3), then the fragments
-    auto q_row = [&](int r) {
-        const int row = r0 + r;
-        return p.q + b * p.q_stride[0] + (int64_t)(hk * p.G + row % p.G) * p.q_stride[1] +
-               (int64_t)(row / p.G) * p.q_stride[2];
-    };
-    if constexpr (E4M3) {
-        for (int r = warp; r < C::kRows; r += kWarps) {
-            uint32_t top = 0u;
-            if (r0 + r <= r1) {
-                const uint16_t *src = q_row(r);
-                for (int d = 4 * lane; d < D; d += 128) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(src + d);
-                    top = max(max(w.x & 0x7FFFu, (w.x >> 16) & 0x7FFFu), max(w.y & 0x7FFFu, (w.y >> 16) & 0x7FFFu));
-                }
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            // exponent field of the largest value; 1 for a row of zeros and
-            // for rows with infinities or NaN, whose scores are not finite
-            const uint32_t e = top >> 7;
-            if (lane == 0) ms.qf[r] = e == 0u || e == 255u ? 1.f : __uint_as_float(e << 23);
-        }
-        __syncthreads();
-    }
-    for (int i = threadIdx.x; i < NT * KS * 32; i += kThreads) {
-        const int l = i % 32, j = (i / 32) % KS, nt = i / (32 * KS), r = nt * 8 + (l >> 2), lt = l & 3;
-        // the four head dims of step j that lane l's key words hold
-        const int d = C::kPanelBytes == 64 ? lt * 16 + j * 4
-                      : E4M3               ? (2 * lt + j / 4) * 16 + (j % 4) * 4
-                                           : (j / 4) * 64 + (2 * lt + (j % 4) / 2) * 8 + (j % 2) * 4;
-        uint2 w = make_uint2(0u, 0u);
-        if (r0 + r <= r1) {
-            w = *reinterpret_cast<const uint2 *>(q_row(r) + d);
-            if constexpr (E4M3) {
-                const float f = 1.f / ms.qf[r];
-                w.x = pack_f16x2(__uint_as_float(w.x << 16) * f, __uint_as_float(w.x & 0xFFFF0000u) * f);
-                w.y = pack_f16x2(__uint_as_float(w.y << 16) * f, __uint_as_float(w.y & 0xFFFF0000u) * f);
-            }
-        }
-        qs[i] = w;
-    }
-    __syncthreads();
-    uint2 qr[NT == 1 ? KS : 1];  // one row tile: the operand stays in registers
-    if constexpr (NT == 1) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) qr[s] = qs[s * 32 + lane];
-    }
-
-    // this thread's rows: columns 2t and 2t + 1 of every row tile
-    float slope[NT][2], qscale[NT][2];  // in base-2 units
-    int pos[NT][2], seen[NT][2];        // position, and the last kv it keeps (-1: nothing)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = nt * 8 + 2 * t + u, row = r0 + r;
-            const bool live = row <= r1;
-            const int h = hk * p.G + (live ? row % p.G : 0);
-            pos[nt][u] = n - p.Q + (live ? row / p.G : 0);
-            seen[nt][u] = live && pos[nt][u] >= 0 ? (p.causal ? pos[nt][u] : n - 1) : -1;
-            qscale[nt][u] = p.scale * (E4M3 ? ms.qf[r] : 1.f) * (p.score_kind == FLEX_SCORE_SOFTCAP ? 1.f : kLog2e);
-            slope[nt][u] = exp2f(-8.f * (float)(h + 1) / (float)p.Hq) * kLog2e;
-        }
-
-    float m[NT][2], l[NT][2], acc[NT][KS][4], vref = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        m[nt][0] = m[nt][1] = -FLT_MAX;
-        l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
-    }
     // byte offsets of this thread's pieces within a staged tile
     const uint32_t ring_at = smem_u32(ring);
     uint32_t koff[2], voff[2];
@@ -350,18 +412,137 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         voff[1] = voff[0] + 64;
     }
 
+    // ---- the pair being computed
+    Steps sq = steps_of<C::kTokens>(p, __ldg(p.kv_lens + b));
+    int pair = (int)(off / sq.count), at_step = (int)(off % sq.count);
+    bool entering = true, whole_start = false;
+    int hk = 0, r0 = 0, r1 = 0, tmin = 0, tmax = 0, n = 0, hi = 0, send = 0, all_hi = 0;
+    int lo_min = 0, all_lo = 0;
+    float slope[NT][2], qscale[NT][2];  // of this thread's rows, columns 2t and 2t + 1 of each row tile (base-2 units)
+    int pos[NT][2], seen[NT][2];        // position, and the last kv it keeps (-1: nothing)
+    float m[NT][2], l[NT][2], acc[NT][KS][4], vref = 0.f;
+    uint2 *qs = reinterpret_cast<uint2 *>(ring - warp * C::kRing + kWarps * C::kRing + warp * C::kQBytes);
+
+    // ---- the end of a piece: the pair's rows where the warp covered all of its
+    // steps, else a partial result
+    auto finish = [&](bool whole_end) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[nt][u] += __shfl_xor_sync(0xffffffffu, l[nt][u], o);
+        const float f = E4M3 ? vref : 1.f;
+        float *part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(p.workspace) + workspace_partials(p.B)) +
+                      (2 * (int64_t)worker + whole_start) * partial_floats(C::kRows, D);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int r = nt * 8 + 2 * t + u;
+                if (r0 + r > r1) continue;
+                // head dims of accumulator rows g and g + 8 of tile i: neighbours
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    const int d = E4M3 ? g * (D / 8) + 2 * i : (i / 4) * 64 + g * 8 + 2 * (i % 4);
+                    const float a = acc[nt][i][u] * f, z = acc[nt][i][u + 2] * f;
+                    if (whole_start && whole_end)
+                        store_pair<D>(p, b, hk, r0 + r, d, a, z, m[nt][u], l[nt][u]);
+                    else
+                        *reinterpret_cast<float2 *>(part + r * D + d) = make_float2(a, z);
+                }
+                if (!(whole_start && whole_end) && g == 0)
+                    *reinterpret_cast<float2 *>(part + C::kRows * D + 2 * r) = make_float2(m[nt][u], l[nt][u]);
+            }
+    };
+
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true, refetched = false;  // refetched: this slot's next keys were already asked for
-    for (; tile < ntiles; tile += step) {
-        const int base = tile_base(tile);
-        const bool more = tile + ST * step < ntiles;
-        const int next = more ? tile_base(tile + ST * step) : 0;
-        int ph_next[SUB];
+    int it = 0;
+    for (; it < steps; ++it) {
+        if (entering) {
+            entering = false;
+            whole_start = at_step == 0;
+            n = sq.n;
+            hk = pair / row_tiles;
+            // rows of this tile: r = query token * G + head within the group
+            r0 = pair % row_tiles * C::kRows;
+            r1 = min(r0 + C::kRows, p.Q * p.G) - 1;
+            tmin = r0 / p.G;
+            tmax = r1 / p.G;
+            // what any row of the tile keeps: [0, send) and [lo_min, hi)
+            hi = p.causal ? max(n - p.Q + tmax + 1, 0) : n;
+            lo_min = p.causal ? (int)max((int64_t)n - p.Q + tmin - p.window + 1, (int64_t)0) : 0;
+            send = min(p.sinks, hi);
+            // what every row keeps, for steps without mask work
+            all_hi = p.causal ? n - p.Q + tmin + 1 : (n - p.Q + tmin >= 0 ? n : 0);
+            all_lo = p.causal ? (int)max((int64_t)n - p.Q + tmax - p.window + 1, (int64_t)0) : 0;
+            // Q operand: lane (g, t) takes row g at the head dims of its key words
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int row = r0 + nt * 8 + g;
+                const bool live = row <= r1;
+                const uint16_t *src = p.q + b * p.q_stride[0] +
+                                      (int64_t)(hk * p.G + (live ? row % p.G : 0)) * p.q_stride[1] +
+                                      (int64_t)(live ? row / p.G : 0) * p.q_stride[2];
+                uint2 w[KS];
+#pragma unroll
+                for (int s = 0; s < KS; s += 2) {  // 16 bytes: two steps
+                    const int d = C::kPanelBytes == 64 ? t * 16 + s * 4
+                                  : E4M3               ? (2 * t + s / 4) * 16 + (s % 4) * 4
+                                                       : (s / 4) * 64 + (2 * t + (s % 4) / 2) * 8;
+                    const uint4 v = live ? *reinterpret_cast<const uint4 *>(src + d) : make_uint4(0, 0, 0, 0);
+                    w[s] = make_uint2(v.x, v.y);
+                    w[s + 1] = make_uint2(v.z, v.w);
+                }
+                float qf = 1.f;
+                if constexpr (E4M3) {
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+                        top = max(max(top, max(w[s].x & 0x7FFFu, (w[s].x >> 16) & 0x7FFFu)),
+                                  max(w[s].y & 0x7FFFu, (w[s].y >> 16) & 0x7FFFu));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // the power of two of the row's largest magnitude; 1 for a
+                    // row of zeros and for rows with infinities or NaN, whose
+                    // scores are not finite
+                    const uint32_t e = top >> 7;
+                    qf = e == 0u || e == 255u ? 1.f : __uint_as_float(e << 23);
+                    const float f = 1.f / qf;
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) {
+                        w[s].x = pack_f16x2(__uint_as_float(w[s].x << 16) * f, __uint_as_float(w[s].x & 0xFFFF0000u) * f);
+                        w[s].y = pack_f16x2(__uint_as_float(w[s].y << 16) * f, __uint_as_float(w[s].y & 0xFFFF0000u) * f);
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < KS; ++s) qs[(nt * KS + s) * 32 + lane] = w[s];  // read back by this lane alone
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int rw = r0 + nt * 8 + 2 * t + u;
+                    const bool in = rw <= r1;
+                    pos[nt][u] = n - p.Q + (in ? rw / p.G : 0);
+                    seen[nt][u] = in && pos[nt][u] >= 0 ? (p.causal ? pos[nt][u] : n - 1) : -1;
+                    qscale[nt][u] = p.scale * __shfl_sync(0xffffffffu, qf, (2 * t + u) * 4) *
+                                    (p.score_kind == FLEX_SCORE_SOFTCAP ? 1.f : kLog2e);
+                    slope[nt][u] = exp2f(-8.f * (float)(hk * p.G + (in ? rw % p.G : 0) + 1) / (float)p.Hq) * kLog2e;
+                    m[nt][u] = -FLT_MAX;
+                    l[nt][u] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < KS; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+            }
+            vref = 0.f;
+        }
+        const int base = base_of[0];
+        const bool more = it + ST < steps;
+        int base_next, ph_next[SUB];
         float ks_next[SUB], vs_next[SUB];
-        if (more && ahead % 32 == 0) lookup(tile + ST * step);
-        take(ahead % 32, ph_next, ks_next, vs_next);
-        ++ahead;
+        if (more && it + ST == looked) lookup();
+        take_place((it + ST) % 32, base_next, ph_next);
+        take_scales((it + ST) % 32, ks_next, vs_next);
         bool whole = base + C::kTokens <= all_hi && (base >= all_lo || base + C::kTokens <= p.sinks);
 #pragma unroll
         for (int j = 0; j < SUB; ++j) whole = whole && ph[0][j] >= 0;
@@ -385,7 +566,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                                                           (16 * j + 8 * r) * C::kPanelBytes);
         }
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+        for (int s = 0; s < KS; ++s) {
+            uint2 q[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) q[nt] = qs[(nt * KS + s) * 32 + lane];
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
                 uint32_t a0, a1, a2, a3;
@@ -401,13 +585,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                     a3 = kw[j][1][2 * s + 1];
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint2 q = NT == 1 ? qr[NT == 1 ? s : 0] : qs[(nt * KS + s) * 32 + lane];
-                    mma16816<E4M3>(x[nt][j], a0, a1, a2, a3, q.x, q.y);
-                }
+                for (int nt = 0; nt < NT; ++nt) mma16816<E4M3>(x[nt][j], a0, a1, a2, a3, q[nt].x, q[nt].y);
             }
+        }
         __syncwarp();  // every lane has read the keys
-        if (more) fetch(&map_k, ring + slot * 2 * C::kTile, &ms.k_full[warp][slot], next, ph_next);
+        if (more) fetch(&map_k, ring + slot * 2 * C::kTile, &ms.k_full[warp][slot], base_next, ph_next);
 
         // ---- scores in base-2 units, masked
         float top[NT][2];
@@ -623,118 +805,101 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
             }
         }
         __syncwarp();  // every lane has read the values
-        if (more) fetch(&map_v, ring + slot * 2 * C::kTile + C::kTile, &ms.v_full[warp][slot], next, ph_next);
+        if (more) fetch(&map_v, ring + slot * 2 * C::kTile + C::kTile, &ms.v_full[warp][slot], base_next, ph_next);
 #pragma unroll
-        for (int s = 0; s + 1 < ST; ++s)
+        for (int s = 0; s + 1 < ST; ++s) {
+            base_of[s] = base_of[s + 1];
 #pragma unroll
             for (int j = 0; j < SUB; ++j) ph[s][j] = ph[s + 1][j], ks[s][j] = ks[s + 1][j], vs[s][j] = vs[s + 1][j];
+        }
+        base_of[ST - 1] = base_next;
 #pragma unroll
         for (int j = 0; j < SUB; ++j) ph[ST - 1][j] = ph_next[j], ks[ST - 1][j] = ks_next[j], vs[ST - 1][j] = vs_next[j];
         if (++slot == ST) {
             slot = 0;
             phase ^= 1u;
         }
+        if (++at_step == sq.count || it + 1 == steps) {
+            finish(at_step == sq.count);
+            if (at_step == sq.count) {
+                at_step = 0;
+                entering = true;
+                if (++pair == pairs_per_seq && it + 1 < steps) {
+                    pair = 0;
+                    sq = steps_of<C::kTokens>(p, __ldg(p.kv_lens + ++b));
+                }
+            }
+        }
     }
     if (!ok) {
         // a copy did not arrive in time: report it, and give the copies still
-        // under way (this slot's and the later ones') the same time again
-        // before shared memory is used for anything else
+        // under way the same time again before this CTA's shared memory is
+        // given up
         ms.abort = 1;
         if (lane == 0) atomicExch(p.status, kDeviceTimeout);
         volatile int keep_waiting = 0;
-        for (int s = 0; s < ST; ++s) {
+        for (int s = 0; s < ST && it + s < steps; ++s) {
             const int at = (slot + s) % ST;
             const uint32_t par = phase ^ (slot + s >= ST ? 1u : 0u);
-            if (tile + s * step >= ntiles) break;
             mbar_wait(&ms.k_full[warp][at], par, &keep_waiting);
             mbar_wait(&ms.v_full[warp][at], par, &keep_waiting);
         }
         if (refetched) mbar_wait(&ms.k_full[warp][slot], phase ^ 1u, &keep_waiting);
     }
+}
 
-    // ------------------------------------------------- join the warps, the CTAs
+// Joins the pieces of one query row, one CTA each; nothing to do for a row
+// whose (sequence, head, row tile) a single warp covered.  The threads take two
+// head dims each, in groups that share out the pieces.
+template <int D, int ROWS, int TOKENS>
+__global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(const CacheAttnProblem p, int row_tiles) {
+    constexpr int kGroups = kJoinThreads / (D / 2);
+    __shared__ float top_s[kJoinThreads / 32];
+    __shared__ float3 sums[kJoinThreads];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int pairs_per_seq = p.cache.H * row_tiles;
+    const int b = (int)(blockIdx.x / pairs_per_seq), pair = (int)(blockIdx.x % pairs_per_seq), r = (int)blockIdx.y;
+    const int64_t *head = reinterpret_cast<const int64_t *>(p.workspace);
+    const int64_t share = head[0];
+    const int count = steps_of<TOKENS>(p, __ldg(p.kv_lens + b)).count;
+    const int64_t begin = head[1 + b] + (int64_t)pair * (count + kEnterCost) + kEnterCost;  // of its first step
+    const int c0 = (int)(begin / share), c1 = (int)((begin + count - 1) / share);
+    const int r0 = pair % row_tiles * ROWS;
+    if (c0 == c1 || r0 + r >= p.Q * p.G) return;
+    const float *parts =
+        reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(p.workspace) + workspace_partials(p.B));
+    auto part = [&](int c) { return parts + (2 * (int64_t)c + (c == c0)) * partial_floats(ROWS, D); };
+    auto stats = [&](int c) { return *reinterpret_cast<const float2 *>(part(c) + ROWS * D + 2 * r); };
+    float top = -FLT_MAX;
+    for (int c = c0 + threadIdx.x; c <= c1; c += kJoinThreads) top = fmaxf(top, stats(c).x);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l[nt][u] += __shfl_xor_sync(0xffffffffu, l[nt][u], o);
-            if (g == 0) {
-                ms.m[warp][nt * 8 + 2 * t + u] = m[nt][u];
-                ms.l[warp][nt * 8 + 2 * t + u] = l[nt][u];
-            }
-        }
-    __syncthreads();  // statistics written; the rings and the Q operand no longer read
-    float *accs = reinterpret_cast<float *>(smem);
-    if (threadIdx.x < C::kRows) {
-        float top = ms.m[0][threadIdx.x], sum = 0.f;
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, ms.m[w][threadIdx.x]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += ms.l[w][threadIdx.x] * exp2f(ms.m[w][threadIdx.x] - top);
-        ms.cm[threadIdx.x] = top;
-        ms.cl[threadIdx.x] = sum;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float f[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = nt * 8 + 2 * t + u;
-            float top = ms.m[0][r];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, ms.m[w][r]);
-            f[u] = exp2f(m[nt][u] - top) * (E4M3 ? vref : 1.f);
-        }
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            // head dims of accumulator rows g and g + 8: neighbours
-            const int d = E4M3 ? g * (D / 8) + 2 * i : (i / 4) * 64 + g * 8 + 2 * (i % 4);
-            float *at = accs + (warp * C::kRows + nt * 8 + 2 * t) * C::kAccStride + d;
-            *reinterpret_cast<float2 *>(at) = make_float2(acc[nt][i][0] * f[0], acc[nt][i][2] * f[0]);
-            *reinterpret_cast<float2 *>(at + C::kAccStride) = make_float2(acc[nt][i][1] * f[1], acc[nt][i][3] * f[1]);
-        }
-    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (threadIdx.x % 32 == 0) top_s[threadIdx.x / 32] = top;
     __syncthreads();
-    auto store = [&](int r, int d, float a, float z, float top, float sum) {
-        const int row = r0 + r, h = hk * p.G + row % p.G, tok = row / p.G;
-        const int64_t o = ((int64_t)b * p.Hq + h) * p.Q + tok;
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays
-        *reinterpret_cast<uint32_t *>(p.out + o * D + d) = pack_bf16x2(a * inv, z * inv);
-        if (d == 0) p.lse[o] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    };
-    const int pairs = (r1 - r0 + 1) * (D / 2);
-    for (int i = threadIdx.x; i < pairs; i += kThreads) {
-        const int r = i / (D / 2), d = 2 * (i % (D / 2));
-        float2 s = *reinterpret_cast<float2 *>(accs + r * C::kAccStride + d);
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            const float2 o = *reinterpret_cast<float2 *>(accs + (w * C::kRows + r) * C::kAccStride + d);
-            s.x += o.x;
-            s.y += o.y;
-        }
-        if (csize == 1)
-            store(r, d, s.x, s.y, ms.cm[r], ms.cl[r]);
-        else
-            *reinterpret_cast<float2 *>(accs + r * C::kAccStride + d) = s;
+    for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, top_s[w]);
+    const int d = 2 * (threadIdx.x % (D / 2)), group = threadIdx.x / (D / 2);
+    float3 s = make_float3(0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = c0 + group; c <= c1; c += kGroups) {
+        const float2 ml = stats(c);
+        const float2 o = *reinterpret_cast<const float2 *>(part(c) + r * D + d);
+        const float f = exp2f(ml.x - top);
+        s.x += o.x * f;
+        s.y += o.y * f;
+        s.z += ml.y * f;
     }
-    if (csize == 1) return;
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();  // every CTA's partial result is in its shared memory
-    for (int i = rank * kThreads + threadIdx.x; i < pairs; i += csize * kThreads) {
-        const int r = i / (D / 2), d = 2 * (i % (D / 2));
-        float top = -FLT_MAX, sum = 0.f, a = 0.f, z = 0.f;
-        for (int c = 0; c < csize; ++c) top = fmaxf(top, *cluster.map_shared_rank(&ms.cm[r], c));
-        for (int c = 0; c < csize; ++c) {
-            const float f = exp2f(*cluster.map_shared_rank(&ms.cm[r], c) - top);
-            const float2 o = *reinterpret_cast<float2 *>(cluster.map_shared_rank(accs + r * C::kAccStride + d, c));
-            sum += f * *cluster.map_shared_rank(&ms.cl[r], c);
-            a += f * o.x;
-            z += f * o.y;
-        }
-        store(r, d, a, z, top, sum);
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int k = 1; k < kGroups; ++k) {
+        const float3 o = sums[threadIdx.x + k * (D / 2)];
+        s.x += o.x;
+        s.y += o.y;
+        s.z += o.z;
     }
-    cluster.sync();  // no CTA leaves while its shared memory is read
+    store_pair<D>(p, b, pair / row_tiles, r0 + r, d, s.x, s.y, top, s.z);
 }
 
 // The cache's keys or values as [pages * heads][page][D]: boxes of box_rows
@@ -750,51 +915,69 @@ bool make_cache_map(CUtensorMap *map, const void *base, const KvCache &c, int bo
                             C::kPanelBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+// Query rows per tile: 8, or 16 from nine rows on (the keys are converted once
+// for both halves).
+int tile_rows(const CacheAttnProblem &p) { return (int64_t)p.Q * p.G <= 8 ? 8 : 16; }
+
+// CTAs of the main launch: one wave, or as many as there can be steps, from
+// what the host knows of the lengths.
+int64_t main_ctas(const CacheAttnProblem &p, int tokens) {
+    const int rows = tile_rows(p);
+    const int64_t pairs = (int64_t)p.B * p.cache.H * (((int64_t)p.Q * p.G + rows - 1) / rows);
+    int64_t most = (int64_t)p.max_pages * p.cache.page;
+    if (p.window != INT_MAX) {
+        const int64_t w = (int64_t)p.window + p.sinks + p.Q + 2 * tokens;
+        most = most < w ? most : w;
+    }
+    const int64_t steps = pairs * ((most + tokens - 1) / tokens + 1), wave = 152 * (rows == 8 ? 3 : 2);
+    return steps < wave ? steps : wave;
+}
+
 template <int D, bool E4M3, int NT>
 cudaError_t launch_cache(const CacheAttnProblem &p, cudaStream_t stream) {
     using C = Cfg<D, E4M3, NT>;
     auto kernel = cache_attention_kernel<D, E4M3, NT>;
     const int row_tiles = (p.Q * p.G + C::kRows - 1) / C::kRows;
     const int64_t pairs = (int64_t)p.B * p.cache.H * row_tiles;
-    // tokens a row tile may have to read, from what the host knows
-    int64_t tokens = (int64_t)p.max_pages * p.cache.page;
-    if (p.window != INT_MAX) tokens = tokens < (int64_t)p.window + p.sinks + p.Q ? tokens : (int64_t)p.window + p.sinks + p.Q;
-    const int64_t tiles = (tokens + C::kTokens - 1) / C::kTokens;
-    // CTAs per sequence and head: enough to fill the GPU, while each warp
-    // still has a tile
-    int csize = 1;
-    while (csize < 16 && pairs * csize < 152 * 6 && (int64_t)csize * kWarps < tiles) csize *= 2;
-    if (pairs * csize > INT_MAX) return cudaErrorInvalidValue;
+    if (pairs > INT_MAX) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e == cudaSuccess && csize > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     const int box_rows = p.cache.page < C::kTokens ? p.cache.page : C::kTokens;
     CUtensorMap map_k, map_v;
     if (!make_cache_map<D, E4M3>(&map_k, p.cache.k, p.cache, box_rows) ||
         !make_cache_map<D, E4M3>(&map_v, p.cache.v, p.cache, box_rows))
         return cudaErrorInvalidValue;
+    kernel<<<(unsigned)main_ctas(p, C::kTokens), kThreads, C::kSmem, stream>>>(map_k, map_v, p, row_tiles, box_rows);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // the join is launched while the main kernel runs and waits for its end on
+    // the device, which hides its launch
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pairs * csize));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.gridDim = dim3((unsigned)pairs, C::kRows);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)csize;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, map_k, map_v, p, csize, row_tiles, box_rows);
+    return cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<D, C::kRows, C::kTokens>, p, row_tiles);
 }
 
 template <int D, bool E4M3>
 cudaError_t launch_cache_rows(const CacheAttnProblem &p, cudaStream_t stream) {
-    const int64_t rows = (int64_t)p.Q * p.G;
-    if (rows <= 8) return launch_cache<D, E4M3, 1>(p, stream);
-    return launch_cache<D, E4M3, 2>(p, stream);
+    return tile_rows(p) == 8 ? launch_cache<D, E4M3, 1>(p, stream) : launch_cache<D, E4M3, 2>(p, stream);
+}
+
+int step_tokens(const CacheAttnProblem &p, int cache_dtype) {
+    return 4096 / (p.cache.D * (cache_dtype == FLEX_DTYPE_E4M3 ? 1 : 2));
 }
 
 }  // namespace
+
+int64_t cache_attention_workspace(const CacheAttnProblem &p, int cache_dtype) {
+    return workspace_partials(p.B) +
+           2 * kWarps * main_ctas(p, step_tokens(p, cache_dtype)) * partial_floats(tile_rows(p), p.cache.D) * 4;
+}
 
 cudaError_t launch_cache_attention(const CacheAttnProblem &p, int cache_dtype, cudaStream_t stream) {
     if (cache_dtype == FLEX_DTYPE_E4M3)

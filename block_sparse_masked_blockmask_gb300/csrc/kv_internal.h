@@ -54,10 +54,12 @@ struct CacheAttnProblem {
     uint16_t *out;
     float *lse;
     int *status;                     // device status word
+    void *workspace;                 // cache_attention_workspace() bytes
 };
 
 cudaError_t launch_rope(const RopeProblem &p, int dtype, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendProblem &p, int src_dtype, int cache_dtype, cudaStream_t stream);
+int64_t cache_attention_workspace(const CacheAttnProblem &p, int cache_dtype);  // bytes
 cudaError_t launch_cache_attention(const CacheAttnProblem &p, int cache_dtype, cudaStream_t stream);
 
 // Angles are kept as turns in 64-bit fixed point: position * frequency wraps

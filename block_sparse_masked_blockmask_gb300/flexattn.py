@@ -51,7 +51,7 @@ EXPORTED = ("flex_block_mask_sizes", "flex_block_mask_sizes_qkv", "flex_block_ma
             "flex_block_mask_transpose", "flex_attention_fwd",
             "flex_attention_fwd_opts", "flex_attention_bwd", "flex_attention_fwd_noalloc", "flex_attention_fwd_host", "flex_device_status",
             "flex_selftest_wait_timeout", "flex_status_string", "flex_rope_frequencies", "flex_rope_fwd", "flex_rope_bwd",
-            "flex_kv_cache_append", "flex_kv_cache_attention")
+            "flex_kv_cache_append", "flex_kv_cache_attention", "flex_kv_cache_attention_workspace")
 
 
 class FlexError(RuntimeError):
@@ -176,8 +176,10 @@ def load_library():
             lib.flex_kv_cache_append.argtypes = [cp, tp, tp, vp, i32, vp, vp, ctypes.POINTER(flex_rope_params), vp]
             lib.flex_kv_cache_append.restype = ctypes.c_int
             lib.flex_kv_cache_attention.argtypes = [tp, cp, vp, i32, vp, i32, ctypes.POINTER(flex_mask_params), i32,
-                                                    ctypes.c_float, ctypes.c_float, vp, vp, vp]
+                                                    ctypes.c_float, ctypes.c_float, vp, vp, vp, ctypes.c_int64, vp]
             lib.flex_kv_cache_attention.restype = ctypes.c_int
+            lib.flex_kv_cache_attention_workspace.argtypes = [tp, cp, i32, i32, ctypes.POINTER(flex_mask_params), i64p]
+            lib.flex_kv_cache_attention_workspace.restype = ctypes.c_int
             lib.flex_status_string.argtypes = [ctypes.c_int]
             lib.flex_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -646,11 +648,13 @@ def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.T
                             mask_kind: int = FLEX_MASK_CAUSAL, window: int = 0, sinks: int = 0,
                             score_kind: int = FLEX_SCORE_IDENTITY, score_param: float = 0.0,
                             scale: float | None = None, out: torch.Tensor | None = None,
-                            lse: torch.Tensor | None = None, stream=None):
+                            lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """The newest tokens' queries q [B, Hq, Q, D] against the cache; returns (out, lse).
 
     kv_lens int32 [B] counts the tokens in the cache, the query tokens among
-    them.  Asynchronous on `stream`.
+    them.  workspace: a uint8 tensor of flex_kv_cache_attention_workspace()
+    bytes, not shared with calls that may run at the same time (allocated when
+    none is given).  Asynchronous on `stream`.
     """
     device = cache.k.device
     if q.dim() != 4 or q.device != device:
@@ -670,14 +674,38 @@ def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.T
     lse_at = _device_array(lse, "lse", torch.float32, device, (B, Hq, Q))
     params = _mask_params(mask_kind, window, 0, sinks)
     tq = _tensor(q)
+    lib = load_library()
+    if workspace is None:
+        size = _cache_workspace_bytes(lib, tq, cache, page_table.shape[1], mask_kind, params)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        if stream is not None:  # not the stream it was allocated on: keep it from being reused before that is done
+            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else
+                                    torch.cuda.ExternalStream(int(stream), device))
+    workspace_at = _device_array(workspace, "workspace", torch.uint8, device, workspace.shape)
     with torch.cuda.device(device):
-        rc = load_library().flex_kv_cache_attention(ctypes.byref(tq), ctypes.byref(cache.struct), table,
-                                                    page_table.shape[1], lens, mask_kind, ctypes.byref(params),
-                                                    score_kind, float(score_param), float(scale), out_at, lse_at,
-                                                    _stream_handle(stream, device))
+        rc = lib.flex_kv_cache_attention(ctypes.byref(tq), ctypes.byref(cache.struct), table, page_table.shape[1], lens,
+                                         mask_kind, ctypes.byref(params), score_kind, float(score_param), float(scale),
+                                         out_at, lse_at, workspace_at, workspace.numel(),
+                                         _stream_handle(stream, device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_kv_cache_attention")
     return out, lse
+
+
+def _cache_workspace_bytes(lib, tq, cache: KVCache, max_pages: int, mask_kind: int, params) -> int:
+    size = ctypes.c_int64()
+    rc = lib.flex_kv_cache_attention_workspace(ctypes.byref(tq), ctypes.byref(cache.struct), max_pages, mask_kind,
+                                               ctypes.byref(params), ctypes.byref(size))
+    if rc != FLEX_OK:
+        raise FlexError(rc, "flex_kv_cache_attention_workspace")
+    return size.value
+
+
+def flex_kv_cache_attention_workspace(q: torch.Tensor, cache: KVCache, max_pages: int,
+                                      mask_kind: int = FLEX_MASK_CAUSAL, window: int = 0, sinks: int = 0) -> int:
+    """Bytes of workspace that flex_kv_cache_attention needs for these sizes."""
+    return _cache_workspace_bytes(load_library(), _tensor(q), cache, max_pages, mask_kind,
+                                  _mask_params(mask_kind, window, 0, sinks))
 
 
 def flex_selftest_wait_timeout(limit_ms: int = 50, stream=None, device=None) -> None:

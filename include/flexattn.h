@@ -534,13 +534,28 @@ FLEX_API int flex_kv_cache_append(const flex_kv_cache *cache, const flex_tensor 
  * it, NaN included.  Made for few query tokens (a decoding step, a handful of
  * tokens to check); any Q is computed, at the rate of a step of 16 rows per
  * key head.  Errors: as flex_kv_cache_append, and FLEX_ERR_UNSUPPORTED for
- * fp32 q and for the prefix and document masks.  Asynchronous on `stream`; no
- * workspace.
+ * fp32 q and for the prefix and document masks.
+ *   workspace : device, 16-byte aligned, at least as many bytes as
+ *               flex_kv_cache_attention_workspace gives (else FLEX_ERR_SHAPE);
+ *               any contents.  Calls that may run at the same time (other
+ *               streams, two captured graphs) need their own.
+ * Asynchronous on `stream`: two launches, the second of which joins partial
+ * results in a fixed order (equal inputs give equal bits).  A wait on a copy
+ * that exceeds its limit is reported by flex_device_status.
  */
 FLEX_API int flex_kv_cache_attention(const flex_tensor *q, const flex_kv_cache *cache, const int32_t *page_table,
                                      int32_t max_pages, const int32_t *kv_lens, int32_t mask_kind,
                                      const flex_mask_params *params, int32_t score_kind, float score_param,
-                                     float scale, void *out, float *lse, void *stream);
+                                     float scale, void *out, float *lse, void *workspace, int64_t workspace_bytes,
+                                     void *stream);
+
+/*
+ * Bytes of workspace of flex_kv_cache_attention for these sizes (pointers in
+ * q are checked, not read).  At most 6 MB and 8 bytes per sequence.  Errors: as
+ * flex_kv_cache_attention.
+ */
+FLEX_API int flex_kv_cache_attention_workspace(const flex_tensor *q, const flex_kv_cache *cache, int32_t max_pages,
+                                               int32_t mask_kind, const flex_mask_params *params, int64_t *bytes);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of

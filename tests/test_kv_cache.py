@@ -124,9 +124,9 @@ def test_attention_refusals(lib):
     good = fa.flex_mask_params(4, 1, None)
 
     def call(q=q, cache=CACHE, table=0x5000, width=4, lens=0x6000, kind=fa.FLEX_MASK_CAUSAL, params=good,
-             score=fa.FLEX_SCORE_IDENTITY, param=0.0, scale=0.1, out=0x7000, lse=0x8000):
+             score=fa.FLEX_SCORE_IDENTITY, param=0.0, scale=0.1, out=0x7000, lse=0x8000, work=0x9000, size=1 << 24):
         return lib.flex_kv_cache_attention(ref(q), ref(cache), table, width, lens, kind, ref(params), score, param,
-                                           scale, out, lse, None)
+                                           scale, out, lse, work, size, None)
 
     for fields, code in BAD_CACHE:
         assert call(cache=changed(CACHE, **fields)) == code, fields
@@ -149,6 +149,19 @@ def test_attention_refusals(lib):
     assert call(score=3) == fa.FLEX_ERR_INVALID_ARG
     assert call(score=fa.FLEX_SCORE_SOFTCAP) == fa.FLEX_ERR_INVALID_ARG
     assert call(scale=math.nan) == fa.FLEX_ERR_INVALID_ARG
+    assert call(table=None) == fa.FLEX_ERR_INVALID_ARG
+    assert call(lens=0x6002) == fa.FLEX_ERR_ALIGNMENT
+    assert call(work=None) == fa.FLEX_ERR_INVALID_ARG
+    assert call(work=0x9008) == fa.FLEX_ERR_ALIGNMENT
+    size = ctypes.c_int64()
+    need = lambda q=q, cache=CACHE, kind=fa.FLEX_MASK_CAUSAL: lib.flex_kv_cache_attention_workspace(  # noqa: E731
+        ref(q), ref(cache), 4, kind, ref(good), ctypes.byref(size))
+    assert need() == fa.FLEX_OK and 0 < size.value <= 4 << 20
+    assert call(size=size.value - 1) == fa.FLEX_ERR_SHAPE
+    assert need(q=_tensor(BF, [3, 5, 1, 128])) == fa.FLEX_ERR_SHAPE
+    assert need(kind=fa.FLEX_MASK_DOCUMENT) == fa.FLEX_ERR_UNSUPPORTED
+    assert need(q=_tensor(BF, [60000, 6, 1 << 20, 128])) == fa.FLEX_ERR_UNSUPPORTED
+    assert lib.flex_kv_cache_attention_workspace(ref(q), ref(CACHE), 4, 0, None, None) == fa.FLEX_ERR_INVALID_ARG
 
 
 def test_python_refusals(lib):
