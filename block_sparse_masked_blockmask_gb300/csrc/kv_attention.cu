@@ -59,12 +59,14 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kJoinThreads = 256;
+constexpr int kJoinMany = 8;       // warps of the main launch per pair, from which a CTA joins one row
+constexpr int kMaxCtas = 152 * 2;  // of the main launch: two on every SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Entering and finishing a (sequence, head, row tile) costs a warp about as
 // much time as two steps: the list counts that many more for each.
 constexpr int kEnterCost = 2;
-constexpr int kMinShare = 4;  // fewest of the list's units a warp takes
+constexpr int kMinShare = 2;  // fewest of the list's units a warp takes
 constexpr float kRaise = 8.f;  // raise the running max only beyond 2^8
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -119,6 +121,11 @@ __device__ __forceinline__ void load_shared(uint32_t *w, uint32_t addr) {
                      : "r"(addr));
 }
 
+// Zero, once the loads that a depends on have returned (a warp's loads from
+// shared memory return in order): a slot is refilled only after its last word
+// was read.  The bit test cannot be folded away, and lane 0 alone uses it.
+__device__ __forceinline__ uint32_t zero_after(uint32_t a, uint32_t zero) { return a & zero; }
+
 // D: head dim; E4M3: cache type (else bf16); NT: tiles of 8 query rows.
 template <int D, bool E4M3, int NT>
 struct Cfg {
@@ -126,10 +133,11 @@ struct Cfg {
     static constexpr int kRowBytes = D * kElem;
     static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;  // a row of a staged panel (TMA swizzle span)
     static constexpr int kPanels = kRowBytes / kPanelBytes;
-    static constexpr int kTile = 4096;                  // bytes of keys (of values) per step of a warp
+    // bytes of keys (of values) per step of a warp: 64 tokens at most
+    static constexpr int kTile = NT == 1 && kRowBytes >= 128 ? 8192 : 4096;
     static constexpr int kTokens = kTile / kRowBytes;
     static constexpr int kSub = kTokens / 16;           // groups of 16 tokens per step
-    static constexpr int kStages = 2;                   // steps in flight per warp
+    static constexpr int kStages = 8192 / kTile;        // steps in flight per warp, beside the one in registers
     static constexpr int kSteps = D / 16;               // k16 steps of S, m16 tiles of O
     static constexpr int kKWords = kRowBytes / 16;      // words of one key a thread holds
     static constexpr int kVBytes = kRowBytes / 8;       // bytes of one value a thread holds
@@ -191,7 +199,7 @@ __device__ __forceinline__ void store_pair(const CacheAttnProblem &p, int b, int
 }
 
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
     cache_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                            const CacheAttnProblem p, int row_tiles, int box_rows) {
     using C = Cfg<D, E4M3, NT>;
@@ -207,10 +215,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     if (threadIdx.x == 0) {
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
-        for (int i = 0; i < kWarps * ST; ++i) {
-            mbar_init(&ms.k_full[0][0] + i, 1);
-            mbar_init(&ms.v_full[0][0] + i, 1);
-        }
+        for (int w = 0; w < kWarps; ++w)
+            for (int s = 0; s < ST; ++s) {
+                mbar_init(&ms.k_full[w][s], 1);
+                mbar_init(&ms.v_full[w][s], 1);
+            }
         ms.abort = 0;
         fence_barrier_init();
     }
@@ -398,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 #pragma unroll
     for (int s = 0; s < ST; ++s) take_scales(s, ks[s], vs[s]);
 
+    const uint32_t nothing = (uint32_t)p.cache.page & 1u;  // 0, which the compiler does not know
     // byte offsets of this thread's pieces within a staged tile
     const uint32_t ring_at = smem_u32(ring);
     uint32_t koff[2], voff[2];
@@ -552,19 +562,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
             ok = false;
             break;
         }
-        float x[NT][SUB][4];
         uint32_t kw[SUB][2][C::kKWords];
 #pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) x[nt][j][0] = x[nt][j][1] = x[nt][j][2] = x[nt][j][3] = 0.f;
+        for (int j = 0; j < SUB; ++j)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int c = 0; c < C::kKWords / 4; ++c)
                     load_shared<16>(&kw[j][r][4 * c], k_at + koff[c & 1] + (c >> 1) * C::kTokens * C::kPanelBytes +
                                                           (16 * j + 8 * r) * C::kPanelBytes);
-        }
+        __syncwarp();
+        if (more)  // the slot is free as soon as its words are in registers
+            fetch(&map_k, ring + slot * 2 * C::kTile + zero_after(kw[SUB - 1][1][C::kKWords - 1], nothing),
+                  &ms.k_full[warp][slot], base_next, ph_next);
+        float x[NT][SUB][4];
+#pragma unroll
+        for (int j = 0; j < SUB; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[nt][j][0] = x[nt][j][1] = x[nt][j][2] = x[nt][j][3] = 0.f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             uint2 q[NT];
@@ -588,8 +603,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                 for (int nt = 0; nt < NT; ++nt) mma16816<E4M3>(x[nt][j], a0, a1, a2, a3, q[nt].x, q[nt].y);
             }
         }
-        __syncwarp();  // every lane has read the keys
-        if (more) fetch(&map_k, ring + slot * 2 * C::kTile, &ms.k_full[warp][slot], base_next, ph_next);
+        // ---- the values into registers, and their slot free again
+        if (!__all_sync(0xffffffffu, mbar_wait(&ms.v_full[warp][slot], phase, &ms.abort))) {
+            ok = false;
+            refetched = more;
+            break;
+        }
+        uint32_t v[SUB][4][C::kVBytes / 4];
+#pragma unroll
+        for (int j = 0; j < SUB; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < C::kVBytes / C::kVLoad; ++c)
+                    load_shared<C::kVLoad>(&v[j][r][c * 4], v_at + voff[r & 1] + c * C::kTokens * C::kPanelBytes +
+                                                                (16 * j + 8 * (r >> 1)) * C::kPanelBytes);
+        __syncwarp();
+        if (more)
+            fetch(&map_v, ring + slot * 2 * C::kTile + C::kTile + zero_after(v[SUB - 1][3][C::kVBytes / 4 - 1], nothing),
+                  &ms.v_full[warp][slot], base_next, ph_next);
 
         // ---- scores in base-2 units, masked
         float top[NT][2];
@@ -695,56 +727,36 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
             }
         }
         // ---- O^T += V^T P^T
-        if (!__all_sync(0xffffffffu, mbar_wait(&ms.v_full[warp][slot], phase, &ms.abort))) {
-            ok = false;
-            refetched = more;
-            break;
-        }
-        auto load_v = [&](int j, uint32_t (&v)[4][C::kVBytes / 4]) {
+        auto product = [&](auto &&value, auto &&weight) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int j = 0; j < SUB; ++j)
 #pragma unroll
-                for (int c = 0; c < C::kVBytes / C::kVLoad; ++c)
-                    load_shared<C::kVLoad>(&v[r][c * 4], v_at + voff[r & 1] + c * C::kTokens * C::kPanelBytes +
-                                                             (16 * j + 8 * (r >> 1)) * C::kPanelBytes);
-        };
-        auto product = [&](const uint32_t (&v)[4][C::kVBytes / 4], int j, auto &&weight) {
+                for (int i = 0; i < KS; ++i) {
+                    uint32_t a0, a1, a2, a3;
+                    if constexpr (E4M3) {
+                        const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
+                        const uint32_t lo2 = prmt(value(j, 0, i / 2), value(j, 1, i / 2), sel);
+                        const uint32_t hi2 = prmt(value(j, 2, i / 2), value(j, 3, i / 2), sel);
+                        a0 = e4m3_lo(lo2);
+                        a1 = e4m3_hi(lo2);
+                        a2 = e4m3_lo(hi2);
+                        a3 = e4m3_hi(hi2);
+                    } else {
+                        a0 = prmt(value(j, 0, i), value(j, 1, i), 0x5410u);
+                        a1 = prmt(value(j, 0, i), value(j, 1, i), 0x7632u);
+                        a2 = prmt(value(j, 2, i), value(j, 3, i), 0x5410u);
+                        a3 = prmt(value(j, 2, i), value(j, 3, i), 0x7632u);
+                    }
 #pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                uint32_t a0, a1, a2, a3;
-                if constexpr (E4M3) {
-                    const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
-                    const uint32_t lo2 = prmt(v[0][i / 2], v[1][i / 2], sel);
-                    const uint32_t hi2 = prmt(v[2][i / 2], v[3][i / 2], sel);
-                    a0 = e4m3_lo(lo2);
-                    a1 = e4m3_hi(lo2);
-                    a2 = e4m3_lo(hi2);
-                    a3 = e4m3_hi(hi2);
-                } else {
-                    a0 = prmt(v[0][i], v[1][i], 0x5410u);
-                    a1 = prmt(v[0][i], v[1][i], 0x7632u);
-                    a2 = prmt(v[2][i], v[3][i], 0x5410u);
-                    a3 = prmt(v[2][i], v[3][i], 0x7632u);
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816<E4M3>(acc[nt][i], a0, a1, a2, a3, weight(nt, j, 0), weight(nt, j, 1));
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma16816<E4M3>(acc[nt][i], a0, a1, a2, a3, weight(nt, 0), weight(nt, 1));
-            }
         };
-        if (whole) {
-#pragma unroll
-            for (int j = 0; j < SUB; ++j) {
-                uint32_t v[4][C::kVBytes / 4];
-                load_v(j, v);
-                product(v, j, [&](int nt, int e) { return pb[nt][j][e]; });
-            }
-        } else {
+        bool mixed = false;  // a token that some rows keep and some do not has a value that is not finite
+        if (!whole) {
             // values of tokens that no row keeps: zero, whatever lies there
 #pragma unroll
-            for (int j = 0; j < SUB; ++j) {
-                uint32_t v[4][C::kVBytes / 4];
-                load_v(j, v);
-                bool mixed = false;  // a token that some rows keep and some do not has a value that is not finite
+            for (int j = 0; j < SUB; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int kv = base + 16 * j + 2 * t + (r & 1) + (r >> 1) * 8;
@@ -753,59 +765,55 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                     bool odd = false;
 #pragma unroll
                     for (int c = 0; c < C::kVBytes / 4; ++c) {
-                        if (!any) v[r][c] = 0u;
+                        if (!any) v[j][r][c] = 0u;
                         if constexpr (E4M3)
-                            odd |= __vcmpeq4(v[r][c] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
+                            odd |= __vcmpeq4(v[j][r][c] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
                         else
-                            odd |= __vcmpgeu2(v[r][c] & 0x7FFF7FFFu, 0x7F807F80u) != 0u;
+                            odd |= __vcmpgeu2(v[j][r][c] & 0x7FFF7FFFu, 0x7F807F80u) != 0u;
                     }
                     mixed |= odd && !every;
                 }
-                if (!__any_sync(0xffffffffu, mixed)) {
-                    product(v, j, [&](int nt, int e) { return pb[nt][j][e]; });
-                    continue;
-                }
-                // one query token's rows at a time, with what they do not keep
-                // zeroed; the other rows' columns keep their sums, since their
-                // zero weights must not meet a value that is not finite either
+            mixed = __any_sync(0xffffffffu, mixed);
+        }
+        if (!mixed) {
+            product([&](int j, int r, int c) { return v[j][r][c]; }, [&](int nt, int j, int e) { return pb[nt][j][e]; });
+        } else {
+            // one query token's rows at a time, with what they do not keep
+            // zeroed; the other rows' columns keep their sums, since their
+            // zero weights must not meet a value that is not finite either
 #pragma unroll 1
-                for (int tok = tmin; tok <= tmax; ++tok) {
-                    const int at = n - p.Q + tok;
-                    float saved[NT][KS][4];
+            for (int tok = tmin; tok <= tmax; ++tok) {
+                const int at = n - p.Q + tok;
+                float saved[NT][KS][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < KS; ++i)
+                    for (int i = 0; i < KS; ++i)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) saved[nt][i][e] = acc[nt][i][e];
-                    load_v(j, v);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
+                        for (int e = 0; e < 4; ++e) saved[nt][i][e] = acc[nt][i][e];
+                product(
+                    [&](int j, int r, int c) {
                         const int kv = base + 16 * j + 2 * t + (r & 1) + (r >> 1) * 8;
                         const bool keep =
                             p.causal ? kv <= at && (at - kv < p.window || kv < p.sinks) : at >= 0 && kv < n;
-#pragma unroll
-                        for (int c = 0; c < C::kVBytes / 4; ++c) v[r][c] = keep ? v[r][c] : 0u;
-                    }
-                    product(v, j, [&](int nt, int e) {  // the operand's column is the lane's g
+                        return keep ? v[j][r][c] : 0u;
+                    },
+                    [&](int nt, int j, int e) {  // the operand's column is the lane's g
                         return (r0 + nt * 8 + g) / p.G == tok ? pb[nt][j][e] : 0u;
                     });
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            if ((r0 + nt * 8 + 2 * t + u) / p.G != tok) {
+                    for (int u = 0; u < 2; ++u)
+                        if ((r0 + nt * 8 + 2 * t + u) / p.G != tok) {
 #pragma unroll
-                                for (int i = 0; i < KS; ++i) {
-                                    acc[nt][i][u] = saved[nt][i][u];
-                                    acc[nt][i][u + 2] = saved[nt][i][u + 2];
-                                }
+                            for (int i = 0; i < KS; ++i) {
+                                acc[nt][i][u] = saved[nt][i][u];
+                                acc[nt][i][u + 2] = saved[nt][i][u + 2];
                             }
-                }
+                        }
             }
         }
-        __syncwarp();  // every lane has read the values
-        if (more) fetch(&map_v, ring + slot * 2 * C::kTile + C::kTile, &ms.v_full[warp][slot], base_next, ph_next);
 #pragma unroll
         for (int s = 0; s + 1 < ST; ++s) {
             base_of[s] = base_of[s + 1];
@@ -848,13 +856,76 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     }
 }
 
-// Joins the pieces of one query row, one CTA each; nothing to do for a row
-// whose (sequence, head, row tile) a single warp covered.  The threads take two
-// head dims each, in groups that share out the pieces.
+// Joins the pieces of one (sequence, head, row tile), one warp a row; nothing
+// to do for one that a single warp covered.  For lists that a pair is a few
+// warps' share of: a CTA for each row as below costs 10 us more at 512 pairs.
+template <int D, int ROWS, int TOKENS>
+__global__ void __launch_bounds__(32 * ROWS) cache_attention_join_few_kernel(const CacheAttnProblem p, int row_tiles) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int V = D / 32;  // values per lane
+    const int pairs_per_seq = p.cache.H * row_tiles;
+    const int b = (int)(blockIdx.x / pairs_per_seq), pair = (int)(blockIdx.x % pairs_per_seq);
+    const int r = threadIdx.x / 32, d = threadIdx.x % 32 * V, r0 = pair % row_tiles * ROWS;
+    if (r0 + r >= p.Q * p.G) return;
+    const int64_t *head = reinterpret_cast<const int64_t *>(p.workspace);
+    const int64_t share = head[0];
+    const int count = steps_of<TOKENS>(p, __ldg(p.kv_lens + b)).count;
+    const int64_t begin = head[1 + b] + (int64_t)pair * (count + kEnterCost) + kEnterCost;  // of its first step
+    const int c0 = (int)(begin / share), c1 = (int)((begin + count - 1) / share);
+    if (c0 == c1) return;
+    const float *parts =
+        reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(p.workspace) + workspace_partials(p.B));
+    float top = -FLT_MAX, sum = 0.f, acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    constexpr int U = 4;  // pieces in flight
+    for (int c = c0; c <= c1; c += U) {
+        float2 ml[U];
+        float o[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            ml[u] = make_float2(-FLT_MAX, 0.f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[u][v] = 0.f;
+            if (c + u <= c1) {
+                const float *part = parts + (2 * (int64_t)(c + u) + (c + u == c0)) * partial_floats(ROWS, D);
+                ml[u] = __ldcg(reinterpret_cast<const float2 *>(part + ROWS * D + 2 * r));
+#pragma unroll
+                for (int v = 0; v < V; v += 2) {
+                    const float2 w = __ldcg(reinterpret_cast<const float2 *>(part + r * D + d + v));
+                    o[u][v] = w.x;
+                    o[u][v + 1] = w.y;
+                }
+            }
+        }
+        float now = top;
+#pragma unroll
+        for (int u = 0; u < U; ++u) now = fmaxf(now, ml[u].x);
+        const float f0 = exp2f(top - now);
+        top = now;
+        sum *= f0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= f0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = exp2f(ml[u].x - now);
+            sum += f * ml[u].y;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] += f * o[u][v];
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+        store_pair<D>(p, b, pair / row_tiles, r0 + r, d + v, acc[v], acc[v + 1], top, sum);
+}
+
+// The same, one CTA a row: for pairs that many warps share.  The threads take
+// two head dims each, in groups that share out the pieces (76 pieces of 16
+// pairs: 5 us, against 13 with one warp a row).
 template <int D, int ROWS, int TOKENS>
 __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(const CacheAttnProblem p, int row_tiles) {
     constexpr int kGroups = kJoinThreads / (D / 2);
-    __shared__ float top_s[kJoinThreads / 32];
+    __shared__ float top_s[kJoinThreads / 32], factor[kMaxCtas * kWarps];
     __shared__ float3 sums[kJoinThreads];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int pairs_per_seq = p.cache.H * row_tiles;
@@ -870,25 +941,36 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(cons
         reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(p.workspace) + workspace_partials(p.B));
     auto part = [&](int c) { return parts + (2 * (int64_t)c + (c == c0)) * partial_floats(ROWS, D); };
     auto stats = [&](int c) { return *reinterpret_cast<const float2 *>(part(c) + ROWS * D + 2 * r); };
+    // the pieces' maxima, and what each is worth relative to the largest
+    const int pieces = c1 - c0 + 1;
     float top = -FLT_MAX;
-    for (int c = c0 + threadIdx.x; c <= c1; c += kJoinThreads) top = fmaxf(top, stats(c).x);
+    for (int c = threadIdx.x; c < pieces; c += kJoinThreads) {
+        factor[c] = stats(c0 + c).x;
+        top = fmaxf(top, factor[c]);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (threadIdx.x % 32 == 0) top_s[threadIdx.x / 32] = top;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, top_s[w]);
-    const int d = 2 * (threadIdx.x % (D / 2)), group = threadIdx.x / (D / 2);
-    float3 s = make_float3(0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int c = c0 + group; c <= c1; c += kGroups) {
-        const float2 ml = stats(c);
-        const float2 o = *reinterpret_cast<const float2 *>(part(c) + r * D + d);
-        const float f = exp2f(ml.x - top);
-        s.x += o.x * f;
-        s.y += o.y * f;
-        s.z += ml.y * f;
+    float sum = 0.f;
+    for (int c = threadIdx.x; c < pieces; c += kJoinThreads) {
+        factor[c] = exp2f(factor[c] - top);
+        sum += factor[c] * stats(c0 + c).y;
     }
+    __syncthreads();
+    const int d = 2 * (threadIdx.x % (D / 2)), group = threadIdx.x / (D / 2);
+    float3 s = make_float3(0.f, 0.f, sum);
+#pragma unroll 8
+    for (int c = group; c < pieces; c += kGroups) {
+        const float2 o = __ldcg(reinterpret_cast<const float2 *>(part(c0 + c) + r * D + d));
+        s.x += o.x * factor[c];
+        s.y += o.y * factor[c];
+    }
+    // the row's sum over all threads, its values over the groups
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
     sums[threadIdx.x] = s;
     __syncthreads();
     if (group != 0) return;
@@ -897,8 +979,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(cons
         const float3 o = sums[threadIdx.x + k * (D / 2)];
         s.x += o.x;
         s.y += o.y;
-        s.z += o.z;
     }
+    s.z = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) s.z += sums[32 * w].z;
     store_pair<D>(p, b, pair / row_tiles, r0 + r, d, s.x, s.y, top, s.z);
 }
 
@@ -929,7 +1013,7 @@ int64_t main_ctas(const CacheAttnProblem &p, int tokens) {
         const int64_t w = (int64_t)p.window + p.sinks + p.Q + 2 * tokens;
         most = most < w ? most : w;
     }
-    const int64_t steps = pairs * ((most + tokens - 1) / tokens + 1), wave = 152 * (rows == 8 ? 3 : 2);
+    const int64_t steps = pairs * ((most + tokens - 1) / tokens + 1), wave = kMaxCtas;
     return steps < wave ? steps : wave;
 }
 
@@ -952,15 +1036,18 @@ cudaError_t launch_cache(const CacheAttnProblem &p, cudaStream_t stream) {
     // the join is launched while the main kernel runs and waits for its end on
     // the device, which hides its launch
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)pairs, C::kRows);
-    cfg.blockDim = dim3(kJoinThreads);
+    const bool many = main_ctas(p, C::kTokens) * kWarps >= pairs * kJoinMany;
+    const int live = (int)((int64_t)p.Q * p.G < C::kRows ? (int64_t)p.Q * p.G : C::kRows);
+    cfg.gridDim = dim3((unsigned)pairs, many ? live : 1);
+    cfg.blockDim = dim3(many ? kJoinThreads : 32 * C::kRows);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<D, C::kRows, C::kTokens>, p, row_tiles);
+    return many ? cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<D, C::kRows, C::kTokens>, p, row_tiles)
+                : cudaLaunchKernelEx(&cfg, cache_attention_join_few_kernel<D, C::kRows, C::kTokens>, p, row_tiles);
 }
 
 template <int D, bool E4M3>
@@ -969,7 +1056,8 @@ cudaError_t launch_cache_rows(const CacheAttnProblem &p, cudaStream_t stream) {
 }
 
 int step_tokens(const CacheAttnProblem &p, int cache_dtype) {
-    return 4096 / (p.cache.D * (cache_dtype == FLEX_DTYPE_E4M3 ? 1 : 2));
+    const int row = p.cache.D * (cache_dtype == FLEX_DTYPE_E4M3 ? 1 : 2);
+    return (tile_rows(p) == 8 && row >= 128 ? 8192 : 4096) / row;
 }
 
 }  // namespace

@@ -280,6 +280,19 @@ def test_attention_long(lens, G, Q, dtype):
     compare(q, cache, table, lens, 64, fa.FLEX_MASK_WINDOW_SINKS, 1000, 5, fa.FLEX_SCORE_ALIBI)
 
 
+@pytest.mark.parametrize("D,G,Q,dtype", [(128, 4, 1, E4M3), (128, 1, 1, BF16), (64, 8, 1, E4M3), (64, 2, 2, BF16),
+                                         (128, 4, 3, E4M3), (64, 16, 1, BF16)], ids=str)
+def test_attention_many_steps(D, G, Q, dtype):
+    """A ragged batch large enough that every warp of the launch walks over many steps, sequences and heads."""
+    gen = torch.Generator().manual_seed(D + G)
+    B, H, page = 40, 8, 64
+    lens = torch.randint(1, 9000, (B,), generator=gen).tolist()
+    lens[3], lens[4], lens[20] = 0, 1, 9000
+    cache, table = filled(gen, lens, H, page, D, dtype)
+    q = torch.randn((B, H * G, Q, D), generator=gen).bfloat16().cuda()
+    compare(q, cache, table, lens, page)
+
+
 @pytest.mark.parametrize("dtype", [E4M3, BF16], ids=["e4m3", "bf16"])
 def test_attention_shared_and_bad_pages(dtype):
     """Two sequences on the same pages; entries that name no page are masked; entries behind a window are not read."""
