@@ -7,9 +7,12 @@ missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -121,6 +124,8 @@ def library_path() -> str:
 def load_library():
     """Load libflexattn.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -139,7 +144,7 @@ def load_library():
             lib.flex_block_mask_create_qkv.argtypes = [i32, ctypes.POINTER(flex_mask_params), i32, i32, i32, i32,
                                                        i32, i32, ctypes.POINTER(flex_block_mask), vp]
             lib.flex_block_mask_create_qkv.restype = ctypes.c_int
-            tp = ctypes.POINTER(flex_tensor)
+            tp = vp  # const flex_tensor *: packed bytes (_tensor) or a reference to a flex_tensor
             lib.flex_attention_fwd.argtypes = [tp, tp, tp, ctypes.POINTER(flex_block_mask), i32, ctypes.c_float,
                                                ctypes.c_float, vp, vp, vp]
             lib.flex_attention_fwd.restype = ctypes.c_int
@@ -186,10 +191,24 @@ def load_library():
     return _lib
 
 
-def _stream_handle(stream, device) -> ctypes.c_void_p:
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(stream, device) -> int:
+    """The cudaStream_t of a stream (None: torch's current one on the device)."""
     if stream is None:
+        if _current_raw_stream is not None and device.index is not None:  # a tenth of the public call's time
+            return _current_raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _device_guard(device):
+    """A context in which `device` is the current CUDA device (nothing to enter when it already is)."""
+    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def flex_status_string(code: int) -> str:
@@ -262,7 +281,7 @@ def flex_block_mask_transpose(block_mask: BlockMask, stream=None) -> BlockMaskQ:
     bq = flex_block_mask_q()
     for key in BlockMaskQ.KEYS:
         setattr(bq, key, t[key].data_ptr())
-    with torch.cuda.device(device):
+    with _device_guard(device):
         rc = load_library().flex_block_mask_transpose(ctypes.byref(s), ctypes.byref(bq),
                                                       _stream_handle(stream, device))
     if rc != FLEX_OK:
@@ -300,7 +319,7 @@ def flex_block_mask_create(mask_kind: int, B: int, H: int, q_len: int, kv_len: i
     bm.kv_indices = t["kv_indices"].data_ptr()
     bm.full_kv_num_blocks = t["full_kv_num_blocks"].data_ptr()
     bm.full_kv_indices = t["full_kv_indices"].data_ptr()
-    with torch.cuda.device(device):
+    with _device_guard(device):
         if kv_block is None:
             rc = load_library().flex_block_mask_create(mask_kind, ctypes.byref(params), B, H, q_len, kv_len, block,
                                                        ctypes.byref(bm), _stream_handle(stream, device))
@@ -316,18 +335,19 @@ def flex_block_mask_create(mask_kind: int, B: int, H: int, q_len: int, kv_len: i
 _DTYPES = {torch.bfloat16: FLEX_DTYPE_BF16, torch.float32: FLEX_DTYPE_FP32}
 
 
-def _tensor(x: torch.Tensor) -> flex_tensor:
-    if x.dim() != 4:
+_pack_tensor = struct.Struct("=Qii8q").pack  # a flex_tensor's fields (a third of the time of filling the Structure)
+assert struct.calcsize("=Qii8q") == ctypes.sizeof(flex_tensor)
+
+
+def _tensor(x: torch.Tensor) -> bytes:
+    """The flex_tensor of a [B, H, S, D] tensor, as the bytes a call takes in its place."""
+    shape = x.shape
+    if len(shape) != 4:
         raise ValueError("expected a [B, H, S, D] tensor")
-    if x.dtype not in _DTYPES:
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
-    t = flex_tensor()
-    t.data = x.data_ptr()
-    t.dtype = _DTYPES[x.dtype]
-    for i in range(4):
-        t.shape[i] = x.shape[i]
-        t.stride[i] = x.stride(i)
-    return t
+    return _pack_tensor(x.data_ptr(), dtype, 0, *shape, *x.stride())
 
 
 def flex_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_mask: BlockMask,
@@ -345,11 +365,11 @@ def flex_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_
     if not out.is_contiguous() or not lse.is_contiguous() or lse.dtype != torch.float32:
         raise ValueError("out and lse must be contiguous; lse float32")
     tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
-    with torch.cuda.device(q.device):
-        rc = load_library().flex_attention_fwd(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
+    with _device_guard(q.device):
+        rc = load_library().flex_attention_fwd(tq, tk, tv,
                                                ctypes.byref(block_mask.struct), score_kind, float(score_param),
-                                               float(scale), ctypes.c_void_p(out.data_ptr()),
-                                               ctypes.c_void_p(lse.data_ptr()), _stream_handle(stream, q.device))
+                                               float(scale), out.data_ptr(),
+                                               lse.data_ptr(), _stream_handle(stream, q.device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_attention_fwd")
     return out, lse
@@ -383,12 +403,12 @@ def flex_attention_fwd_opts(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, b
     opts = flex_kernel_options(int(bool(prescale_qk)), int(bool(rows_guaranteed_safe)),
                                None if max_scores is None else max_scores.data_ptr())
     tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
-    with torch.cuda.device(q.device):
-        rc = load_library().flex_attention_fwd_opts(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
+    with _device_guard(q.device):
+        rc = load_library().flex_attention_fwd_opts(tq, tk, tv,
                                                     ctypes.byref(block_mask.struct), score_kind,
                                                     float(score_param), float(scale),
-                                                    ctypes.c_void_p(out.data_ptr()),
-                                                    ctypes.c_void_p(lse.data_ptr()), ctypes.byref(opts),
+                                                    out.data_ptr(),
+                                                    lse.data_ptr(), ctypes.byref(opts),
                                                     _stream_handle(stream, q.device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_attention_fwd_opts")
@@ -415,14 +435,14 @@ def flex_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: t
     if not lse.is_contiguous() or lse.dtype != torch.float32 or not delta.is_contiguous():
         raise ValueError("lse and delta must be contiguous float32")
     tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
-    with torch.cuda.device(q.device):
-        rc = load_library().flex_attention_bwd(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
-                                               ctypes.c_void_p(out.data_ptr()), ctypes.c_void_p(lse.data_ptr()),
-                                               ctypes.c_void_p(dout.data_ptr()), ctypes.byref(block_mask.struct),
+    with _device_guard(q.device):
+        rc = load_library().flex_attention_bwd(tq, tk, tv,
+                                               out.data_ptr(), lse.data_ptr(),
+                                               dout.data_ptr(), ctypes.byref(block_mask.struct),
                                                ctypes.byref(block_mask_q.struct), score_kind, float(score_param),
-                                               float(scale), ctypes.c_void_p(dq.data_ptr()),
-                                               ctypes.c_void_p(dk.data_ptr()), ctypes.c_void_p(dv.data_ptr()),
-                                               ctypes.c_void_p(delta.data_ptr()), _stream_handle(stream, q.device))
+                                               float(scale), dq.data_ptr(),
+                                               dk.data_ptr(), dv.data_ptr(),
+                                               delta.data_ptr(), _stream_handle(stream, q.device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_attention_bwd")
     return dq, dk, dv
@@ -440,12 +460,12 @@ def flex_attention_fwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
         scale = 1.0 / math.sqrt(q.shape[-1])
     tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
     status = ctypes.POINTER(ctypes.c_int)()
-    with torch.cuda.device(q.device):
-        rc = load_library().flex_attention_fwd_noalloc(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
+    with _device_guard(q.device):
+        rc = load_library().flex_attention_fwd_noalloc(tq, tk, tv,
                                                        ctypes.byref(block_mask.struct), score_kind,
                                                        float(score_param), float(scale),
-                                                       ctypes.c_void_p(out.data_ptr()),
-                                                       ctypes.c_void_p(lse.data_ptr()),
+                                                       out.data_ptr(),
+                                                       lse.data_ptr(),
                                                        _stream_handle(stream, q.device), ctypes.byref(status))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_attention_fwd_noalloc")
@@ -504,10 +524,10 @@ def flex_attention_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, b
     params = _mask_params(mask_kind, window, prefix, sinks, doc_ids)
     dev = buffers.struct()
     with torch.cuda.device(buffers.device):
-        rc = load_library().flex_attention_fwd_host(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), mask_kind,
+        rc = load_library().flex_attention_fwd_host(tq, tk, tv, mask_kind,
                                                     ctypes.byref(params), score_kind, float(score_param),
-                                                    float(scale), ctypes.c_void_p(out.data_ptr()),
-                                                    ctypes.c_void_p(lse.data_ptr()), ctypes.byref(dev), int(chunks),
+                                                    float(scale), out.data_ptr(),
+                                                    lse.data_ptr(), ctypes.byref(dev), int(chunks),
                                                     _stream_handle(stream, buffers.device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_attention_fwd_host")
@@ -529,7 +549,7 @@ def _device_array(x: torch.Tensor | None, name: str, dtype: torch.dtype, device,
     """The address of a contiguous tensor of this type, shape and device (None stays None)."""
     if x is None:
         return None
-    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or not x.is_contiguous() or x.device != device:
+    if x.dtype != dtype or x.shape != shape or not x.is_contiguous() or x.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
     return x.data_ptr()
 
@@ -553,10 +573,9 @@ def _rope(name: str, q, k, inv_freq, positions, layout, attention_scale, q_out, 
     params = _rope_params(inv_freq, layout, attention_scale, device)
     pos = _device_array(positions, "positions", torch.int32, device, (q.shape[0], q.shape[2]))
     tq, oq = _tensor(q), _tensor(q_out)
-    tk, ok = (None if k is None else ctypes.byref(_tensor(k))), (None if k is None else ctypes.byref(_tensor(k_out)))
-    with torch.cuda.device(device):
-        rc = getattr(load_library(), name)(ctypes.byref(tq), tk, ctypes.byref(params), pos, ctypes.byref(oq), ok,
-                                           _stream_handle(stream, device))
+    tk, ok = (None, None) if k is None else (_tensor(k), _tensor(k_out))
+    with _device_guard(device):
+        rc = getattr(load_library(), name)(tq, tk, ctypes.byref(params), pos, oq, ok, _stream_handle(stream, device))
     if rc != FLEX_OK:
         raise FlexError(rc, name)
     return q_out, k_out
@@ -636,8 +655,8 @@ def flex_kv_cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_
     new = _device_array(new_lens, "new_lens", torch.int32, device, (B,))
     params = None if inv_freq is None else ctypes.byref(_rope_params(inv_freq, layout, attention_scale, device))
     tk, tv = _tensor(k), _tensor(v)
-    with torch.cuda.device(device):
-        rc = load_library().flex_kv_cache_append(ctypes.byref(cache.struct), ctypes.byref(tk), ctypes.byref(tv), table,
+    with _device_guard(device):
+        rc = load_library().flex_kv_cache_append(ctypes.byref(cache.struct), tk, tv, table,
                                                  page_table.shape[1], lens, new, params,
                                                  _stream_handle(stream, device))
     if rc != FLEX_OK:
@@ -672,19 +691,22 @@ def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.T
     lens = _device_array(kv_lens, "kv_lens", torch.int32, device, (B,))
     out_at = _device_array(out, "out", q.dtype, device, q.shape)
     lse_at = _device_array(lse, "lse", torch.float32, device, (B, Hq, Q))
-    params = _mask_params(mask_kind, window, 0, sinks)
+    params = None if mask_kind == FLEX_MASK_CAUSAL and not sinks else \
+        ctypes.byref(_mask_params(mask_kind, window, 0, sinks))
     tq = _tensor(q)
     lib = load_library()
     if workspace is None:
-        size = _cache_workspace_bytes(lib, tq, cache, page_table.shape[1], mask_kind, params)
+        size = _cache_workspace_bytes(q.shape, cache.struct.H, cache.k.shape, cache.struct.dtype, page_table.shape[1],
+                                      mask_kind, window, sinks)
         workspace = torch.empty(size, dtype=torch.uint8, device=device)
-        if stream is not None:  # not the stream it was allocated on: keep it from being reused before that is done
+        if stream is not None and _stream_handle(stream, device) != _stream_handle(None, device):
+            # not the stream it was allocated on: keep it from being reused before that is done
             workspace.record_stream(stream if hasattr(stream, "cuda_stream") else
                                     torch.cuda.ExternalStream(int(stream), device))
     workspace_at = _device_array(workspace, "workspace", torch.uint8, device, workspace.shape)
-    with torch.cuda.device(device):
-        rc = lib.flex_kv_cache_attention(ctypes.byref(tq), ctypes.byref(cache.struct), table, page_table.shape[1], lens,
-                                         mask_kind, ctypes.byref(params), score_kind, float(score_param), float(scale),
+    with _device_guard(device):
+        rc = lib.flex_kv_cache_attention(tq, ctypes.byref(cache.struct), table, page_table.shape[1], lens,
+                                         mask_kind, params, score_kind, float(score_param), float(scale),
                                          out_at, lse_at, workspace_at, workspace.numel(),
                                          _stream_handle(stream, device))
     if rc != FLEX_OK:
@@ -692,10 +714,16 @@ def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.T
     return out, lse
 
 
-def _cache_workspace_bytes(lib, tq, cache: KVCache, max_pages: int, mask_kind: int, params) -> int:
-    size = ctypes.c_int64()
-    rc = lib.flex_kv_cache_attention_workspace(ctypes.byref(tq), ctypes.byref(cache.struct), max_pages, mask_kind,
-                                               ctypes.byref(params), ctypes.byref(size))
+@functools.lru_cache(maxsize=256)
+def _cache_workspace_bytes(q_shape, H: int, pool_shape, dtype: int, max_pages: int, mask_kind: int, window: int,
+                           sinks: int) -> int:
+    """The library's answer for these sizes (it depends on nothing else)."""
+    B, Hq, Q, D = q_shape
+    q = _pack_tensor(16, FLEX_DTYPE_BF16, 0, B, Hq, Q, D, Hq * Q * D, Q * D, D, 1)
+    cache = flex_kv_cache(pool_shape[0], H, pool_shape[2], pool_shape[3], dtype, 0, 16, 16, 16, 16)
+    params, size = _mask_params(mask_kind, window, 0, sinks), ctypes.c_int64()
+    rc = load_library().flex_kv_cache_attention_workspace(q, ctypes.byref(cache), max_pages, mask_kind,
+                                                          ctypes.byref(params), ctypes.byref(size))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_kv_cache_attention_workspace")
     return size.value
@@ -704,14 +732,16 @@ def _cache_workspace_bytes(lib, tq, cache: KVCache, max_pages: int, mask_kind: i
 def flex_kv_cache_attention_workspace(q: torch.Tensor, cache: KVCache, max_pages: int,
                                       mask_kind: int = FLEX_MASK_CAUSAL, window: int = 0, sinks: int = 0) -> int:
     """Bytes of workspace that flex_kv_cache_attention needs for these sizes."""
-    return _cache_workspace_bytes(load_library(), _tensor(q), cache, max_pages, mask_kind,
-                                  _mask_params(mask_kind, window, 0, sinks))
+    if q.dim() != 4:
+        raise ValueError("q must be a [B, Hq, Q, D] tensor")
+    return _cache_workspace_bytes(q.shape, cache.struct.H, cache.k.shape, cache.struct.dtype, max_pages, mask_kind,
+                                  window, sinks)
 
 
 def flex_selftest_wait_timeout(limit_ms: int = 50, stream=None, device=None) -> None:
     """Enqueue the bounded-wait failure check (see include/flexattn.h)."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with torch.cuda.device(device):
+    with _device_guard(device):
         rc = load_library().flex_selftest_wait_timeout(int(limit_ms), _stream_handle(stream, device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_selftest_wait_timeout")
