@@ -175,10 +175,10 @@ def load_library():
             lib.flex_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, ctypes.POINTER(f64)]
             lib.flex_rope_frequencies.restype = ctypes.c_int
             for f in (lib.flex_rope_fwd, lib.flex_rope_bwd):
-                f.argtypes = [tp, tp, ctypes.POINTER(flex_rope_params), vp, tp, tp, vp]
+                f.argtypes = [tp, tp, vp, vp, tp, tp, vp]  # the third: packed bytes (_rope_params) or a reference
                 f.restype = ctypes.c_int
             cp = ctypes.POINTER(flex_kv_cache)
-            lib.flex_kv_cache_append.argtypes = [cp, tp, tp, vp, i32, vp, vp, ctypes.POINTER(flex_rope_params), vp]
+            lib.flex_kv_cache_append.argtypes = [cp, tp, tp, vp, i32, vp, vp, vp, vp]
             lib.flex_kv_cache_append.restype = ctypes.c_int
             lib.flex_kv_cache_attention.argtypes = [tp, cp, vp, i32, vp, i32, ctypes.POINTER(flex_mask_params), i32,
                                                     ctypes.c_float, ctypes.c_float, vp, vp, vp, ctypes.c_int64, vp]
@@ -203,12 +203,20 @@ def _stream_handle(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-_NO_GUARD = contextlib.nullcontext()
-
-
 def _device_guard(device):
     """A context in which `device` is the current CUDA device (nothing to enter when it already is)."""
-    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(device, f, *args) -> int:
+    """f(*args) with `device` (of an existing CUDA tensor) as the current device."""
+    if _current_device() == device.index:
+        return f(*args)
+    with torch.cuda.device(device):
+        return f(*args)
 
 
 def flex_status_string(code: int) -> str:
@@ -364,12 +372,9 @@ def flex_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_
         lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
     if not out.is_contiguous() or not lse.is_contiguous() or lse.dtype != torch.float32:
         raise ValueError("out and lse must be contiguous; lse float32")
-    tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
-    with _device_guard(q.device):
-        rc = load_library().flex_attention_fwd(tq, tk, tv,
-                                               ctypes.byref(block_mask.struct), score_kind, float(score_param),
-                                               float(scale), out.data_ptr(),
-                                               lse.data_ptr(), _stream_handle(stream, q.device))
+    rc = _call(q.device, load_library().flex_attention_fwd, _tensor(q), _tensor(k), _tensor(v),
+               ctypes.byref(block_mask.struct), score_kind, float(score_param), float(scale), out.data_ptr(),
+               lse.data_ptr(), _stream_handle(stream, q.device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_attention_fwd")
     return out, lse
@@ -554,28 +559,40 @@ def _device_array(x: torch.Tensor | None, name: str, dtype: torch.dtype, device,
     return x.data_ptr()
 
 
-def _rope_params(inv_freq: torch.Tensor, layout: int, attention_scale: float, device) -> flex_rope_params:
+_pack_rope = struct.Struct("=Qiifi").pack
+assert struct.calcsize("=Qiifi") == ctypes.sizeof(flex_rope_params)
+
+
+def _rope_params(inv_freq: torch.Tensor, layout: int, attention_scale: float, device) -> bytes:
+    """A flex_rope_params as the bytes a call takes in its place."""
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a float64 [rotary_dim / 2] tensor")
-    return flex_rope_params(_device_array(inv_freq, "inv_freq", torch.float64, device, inv_freq.shape),
-                            2 * inv_freq.numel(), layout, attention_scale, 0)
+    n = inv_freq.shape[0]
+    return _pack_rope(_device_array(inv_freq, "inv_freq", torch.float64, device, (n,)), 2 * n, layout,
+                      attention_scale, 0)
 
 
 def _rope(name: str, q, k, inv_freq, positions, layout, attention_scale, q_out, k_out, stream):
     device = q.device
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
-    for x in (q, k, q_out, k_out):
-        if x is not None and x.device != device:
+    elif q_out.device != device:
+        raise ValueError("q, k and their outputs must be on one device")
+    tk = ok = None
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
+        if k.device != device or k_out.device != device:
             raise ValueError("q, k and their outputs must be on one device")
+        tk, ok = _tensor(k), _tensor(k_out)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    tq = _tensor(q)
     params = _rope_params(inv_freq, layout, attention_scale, device)
-    pos = _device_array(positions, "positions", torch.int32, device, (q.shape[0], q.shape[2]))
-    tq, oq = _tensor(q), _tensor(q_out)
-    tk, ok = (None, None) if k is None else (_tensor(k), _tensor(k_out))
-    with _device_guard(device):
-        rc = getattr(load_library(), name)(tq, tk, ctypes.byref(params), pos, oq, ok, _stream_handle(stream, device))
+    if positions is not None:
+        positions = _device_array(positions, "positions", torch.int32, device, (q.shape[0], q.shape[2]))
+    rc = _call(device, getattr(load_library(), name), tq, tk, params, positions, _tensor(q_out), ok,
+               _stream_handle(stream, device))
     if rc != FLEX_OK:
         raise FlexError(rc, name)
     return q_out, k_out
@@ -623,6 +640,7 @@ class KVCache:
                                     _device_array(v, "v", k.dtype, k.device, k.shape),
                                     _device_array(k_scale, "k_scale", torch.float32, k.device, (n, h)),
                                     _device_array(v_scale, "v_scale", torch.float32, k.device, (n, h)))
+        self._ref = ctypes.byref(self.struct)
 
 
 def flex_kv_cache_create(num_pages: int, H: int, D: int, page_size: int = 64,
@@ -645,20 +663,18 @@ def flex_kv_cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_
     rotated by its positions when inv_freq is given.
     """
     device = cache.k.device
-    B = k.shape[0]
     if k.device != device or v.device != device:
         raise ValueError("k and v must be on the cache's device")
     if page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
-    table = _device_array(page_table, "page_table", torch.int32, device, (B, page_table.shape[1]))
-    lens = _device_array(cache_lens, "cache_lens", torch.int32, device, (B,))
-    new = _device_array(new_lens, "new_lens", torch.int32, device, (B,))
-    params = None if inv_freq is None else ctypes.byref(_rope_params(inv_freq, layout, attention_scale, device))
     tk, tv = _tensor(k), _tensor(v)
-    with _device_guard(device):
-        rc = load_library().flex_kv_cache_append(ctypes.byref(cache.struct), tk, tv, table,
-                                                 page_table.shape[1], lens, new, params,
-                                                 _stream_handle(stream, device))
+    B, max_pages = k.shape[0], page_table.shape[1]
+    rc = _call(device, load_library().flex_kv_cache_append, cache._ref, tk, tv,
+               _device_array(page_table, "page_table", torch.int32, device, (B, max_pages)), max_pages,
+               _device_array(cache_lens, "cache_lens", torch.int32, device, (B,)),
+               _device_array(new_lens, "new_lens", torch.int32, device, (B,)),
+               None if inv_freq is None else _rope_params(inv_freq, layout, attention_scale, device),
+               _stream_handle(stream, device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_kv_cache_append")
 
@@ -675,52 +691,51 @@ def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.T
     bytes, not shared with calls that may run at the same time (allocated when
     none is given).  Asynchronous on `stream`.
     """
-    device = cache.k.device
-    if q.dim() != 4 or q.device != device:
+    device, shape = cache.k.device, q.shape
+    if len(shape) != 4 or q.device != device:
         raise ValueError("q must be a [B, Hq, Q, D] tensor on the cache's device")
-    B, Hq, Q, D = q.shape
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    if out is None:
-        out = torch.empty((B, Hq, Q, D), dtype=q.dtype, device=device)
-    if lse is None:
-        lse = torch.empty((B, Hq, Q), dtype=torch.float32, device=device)
+    B, Hq, Q, D = shape
     if page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
-    table = _device_array(page_table, "page_table", torch.int32, device, (B, page_table.shape[1]))
+    max_pages = page_table.shape[1]
+    table = _device_array(page_table, "page_table", torch.int32, device, (B, max_pages))
     lens = _device_array(kv_lens, "kv_lens", torch.int32, device, (B,))
-    out_at = _device_array(out, "out", q.dtype, device, q.shape)
-    lse_at = _device_array(lse, "lse", torch.float32, device, (B, Hq, Q))
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=device)
+    else:
+        _device_array(out, "out", q.dtype, device, shape)
+    if lse is None:
+        lse = torch.empty((B, Hq, Q), dtype=torch.float32, device=device)
+    else:
+        _device_array(lse, "lse", torch.float32, device, (B, Hq, Q))
     params = None if mask_kind == FLEX_MASK_CAUSAL and not sinks else \
         ctypes.byref(_mask_params(mask_kind, window, 0, sinks))
-    tq = _tensor(q)
-    lib = load_library()
+    handle = _stream_handle(stream, device)
     if workspace is None:
-        size = _cache_workspace_bytes(q.shape, cache.struct.H, cache.k.shape, cache.struct.dtype, page_table.shape[1],
-                                      mask_kind, window, sinks)
+        size = _cache_workspace_bytes(shape, cache.k.shape, cache.struct.dtype, max_pages, mask_kind, window, sinks)
         workspace = torch.empty(size, dtype=torch.uint8, device=device)
-        if stream is not None and _stream_handle(stream, device) != _stream_handle(None, device):
+        if stream is not None and handle != _stream_handle(None, device):
             # not the stream it was allocated on: keep it from being reused before that is done
             workspace.record_stream(stream if hasattr(stream, "cuda_stream") else
-                                    torch.cuda.ExternalStream(int(stream), device))
-    workspace_at = _device_array(workspace, "workspace", torch.uint8, device, workspace.shape)
-    with _device_guard(device):
-        rc = lib.flex_kv_cache_attention(tq, ctypes.byref(cache.struct), table, page_table.shape[1], lens,
-                                         mask_kind, params, score_kind, float(score_param), float(scale),
-                                         out_at, lse_at, workspace_at, workspace.numel(),
-                                         _stream_handle(stream, device))
+                                    torch.cuda.ExternalStream(handle, device))
+    else:
+        _device_array(workspace, "workspace", torch.uint8, device, workspace.shape)
+        size = workspace.numel()
+    rc = _call(device, load_library().flex_kv_cache_attention, _tensor(q), cache._ref, table, max_pages, lens,
+               mask_kind, params, score_kind, float(score_param), D**-0.5 if scale is None else float(scale),
+               out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, handle)
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_kv_cache_attention")
     return out, lse
 
 
 @functools.lru_cache(maxsize=256)
-def _cache_workspace_bytes(q_shape, H: int, pool_shape, dtype: int, max_pages: int, mask_kind: int, window: int,
+def _cache_workspace_bytes(q_shape, pool_shape, dtype: int, max_pages: int, mask_kind: int, window: int,
                            sinks: int) -> int:
     """The library's answer for these sizes (it depends on nothing else)."""
     B, Hq, Q, D = q_shape
     q = _pack_tensor(16, FLEX_DTYPE_BF16, 0, B, Hq, Q, D, Hq * Q * D, Q * D, D, 1)
-    cache = flex_kv_cache(pool_shape[0], H, pool_shape[2], pool_shape[3], dtype, 0, 16, 16, 16, 16)
+    cache = flex_kv_cache(*pool_shape, dtype, 0, 16, 16, 16, 16)
     params, size = _mask_params(mask_kind, window, 0, sinks), ctypes.c_int64()
     rc = load_library().flex_kv_cache_attention_workspace(q, ctypes.byref(cache), max_pages, mask_kind,
                                                           ctypes.byref(params), ctypes.byref(size))
@@ -734,8 +749,7 @@ def flex_kv_cache_attention_workspace(q: torch.Tensor, cache: KVCache, max_pages
     """Bytes of workspace that flex_kv_cache_attention needs for these sizes."""
     if q.dim() != 4:
         raise ValueError("q must be a [B, Hq, Q, D] tensor")
-    return _cache_workspace_bytes(q.shape, cache.struct.H, cache.k.shape, cache.struct.dtype, max_pages, mask_kind,
-                                  window, sinks)
+    return _cache_workspace_bytes(q.shape, cache.k.shape, cache.struct.dtype, max_pages, mask_kind, window, sinks)
 
 
 def flex_selftest_wait_timeout(limit_ms: int = 50, stream=None, device=None) -> None:
