@@ -331,15 +331,25 @@ __device__ __forceinline__ void apply_interval_mask(const MaskDesc &m, int q, in
 }
 
 // Window + sinks: columns up to sink_hi or in [lo, q] (mask_row_sinks), and
-// nothing at or past KV_LEN.
+// nothing at or past KV_LEN.  Most tiles meet one of the two intervals only,
+// and are masked like an interval mask's (both tests on every partial tile:
+// 9% slower at window 1024, 16 sinks, S 8192, D 128).
 __device__ __forceinline__ void apply_sinks_mask(const MaskDesc &m, int q, int kv0, uint64_t (&x2)[64]) {
     int sink_hi, lo;
     mask_row_sinks(m, q, sink_hi, lo);
     const int csink = min(sink_hi, m.kv_len - 1) - kv0, clo = lo - kv0, chi = min(q, m.kv_len - 1) - kv0;
+    const bool sink_here = csink >= 0, window_here = clo < kBlock && chi >= 0;
+    if (!__any_sync(0xffffffffu, sink_here && window_here)) {
+        const int a = sink_here ? 0 : clo, e = sink_here ? csink : chi;
 #pragma unroll
-    for (int j = 0; j < 64; ++j)
-        x2[j] = keep_pair(x2[j], 2 * j <= csink || (2 * j >= clo && 2 * j <= chi),
-                          2 * j + 1 <= csink || (2 * j + 1 >= clo && 2 * j + 1 <= chi));
+        for (int j = 0; j < 64; ++j)
+            x2[j] = keep_pair(x2[j], 2 * j >= a && 2 * j <= e, 2 * j + 1 >= a && 2 * j + 1 <= e);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            x2[j] = keep_pair(x2[j], 2 * j <= csink || (2 * j >= clo && 2 * j <= chi),
+                              2 * j + 1 <= csink || (2 * j + 1 >= clo && 2 * j + 1 <= chi));
+    }
 }
 
 // Document mask_mod: same document id (the tile's ids staged in shared

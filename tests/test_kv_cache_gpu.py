@@ -293,6 +293,17 @@ def test_attention_many_steps(D, G, Q, dtype):
     compare(q, cache, table, lens, page)
 
 
+@pytest.mark.parametrize("B,dtype", [(129, E4M3), (300, BF16), (1000, E4M3)], ids=str)
+def test_attention_many_sequences(B, dtype):
+    """More sequences than a CTA has threads: the list's prefix sums and the search in them."""
+    gen = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 90, (B,), generator=gen).tolist()
+    cache, table = filled(gen, lens, 2, 32, 64, dtype)
+    q = torch.randn((B, 4, 2, 64), generator=gen).bfloat16().cuda()
+    compare(q, cache, table, lens, 32)
+    compare(q, cache, table, lens, 32, fa.FLEX_MASK_WINDOW_SINKS, 10, 3)
+
+
 @pytest.mark.parametrize("dtype", [E4M3, BF16], ids=["e4m3", "bf16"])
 def test_attention_shared_and_bad_pages(dtype):
     """Two sequences on the same pages; entries that name no page are masked; entries behind a window are not read."""
