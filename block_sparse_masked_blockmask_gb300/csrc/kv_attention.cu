@@ -58,15 +58,15 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr int kJoinMany = 8;       // warps of the main launch per pair, from which a CTA joins one row
 constexpr int kMaxCtas = 152 * 2;  // of the main launch: two on every SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Entering and finishing a (sequence, head, row tile) costs a warp about as
 // much time as two steps: the list counts that many more for each.
-constexpr int kEnterCost = 2;
-constexpr int kMinShare = 2;  // fewest of the list's units a warp takes
+constexpr int kEnterCost = 3;
+constexpr int kMinShare = 1;  // fewest of the list's units a warp takes
 constexpr float kRaise = 8.f;  // raise the running max only beyond 2^8
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -89,6 +89,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+// cap tanh(s / cap) in base-2 units, as cap (1 - 2 / (1 + e^(2 s / cap))): within
+// 2^-21 cap absolutely (the softmax needs no more), at a tenth of tanhf's
+// instructions.  in = 2 log2(e) / cap, out = cap log2(e).
+__device__ __forceinline__ float softcap_log2(float s, float in, float out) {
+    return fmaf(-2.f * out, rcp_approx(1.f + ex2_approx(s * in)), out);
 }
 // 8 x 8 transpose of 16-bit values across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -632,13 +638,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[nt][j][e] *= qscale[nt][e & 1] * ks[0][j];
         if (p.score_kind == FLEX_SCORE_SOFTCAP) {
+            const float cap_in = 2.f * kLog2e / p.score_param, cap_out = p.score_param * kLog2e;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < SUB; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        x[nt][j][e] = p.score_param * tanhf(x[nt][j][e] / p.score_param) * kLog2e;
+                        x[nt][j][e] = softcap_log2(x[nt][j][e], cap_in, cap_out);
         } else if (p.score_kind == FLEX_SCORE_ALIBI) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -919,16 +926,16 @@ __global__ void __launch_bounds__(32 * ROWS) cache_attention_join_few_kernel(con
         store_pair<D>(p, b, pair / row_tiles, r0 + r, d + v, acc[v], acc[v + 1], top, sum);
 }
 
-// The same, one CTA a row: for pairs that many warps share.  The threads take
-// two head dims each, in groups that share out the pieces (76 pieces of 16
-// pairs: 5 us, against 13 with one warp a row).
+// The same for pairs that many warps share: one CTA for 32 head dims of a row,
+// two of them a thread, in groups that share out the pieces (16 pairs of 76
+// pieces: 4 us, against 13 with one warp a row).
 template <int D, int ROWS, int TOKENS>
 __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(const CacheAttnProblem p, int row_tiles) {
-    constexpr int kGroups = kJoinThreads / (D / 2);
-    __shared__ float top_s[kJoinThreads / 32], factor[kMaxCtas * kWarps];
-    __shared__ float3 sums[kJoinThreads];
+    constexpr int kColumns = 16, kGroups = kJoinThreads / kColumns, kJoinWarps = kJoinThreads / 32;
+    __shared__ float top_s[kJoinWarps], sum_s[kJoinWarps], factor[kMaxCtas * kWarps];
+    __shared__ float2 value_s[kJoinWarps][kColumns];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int pairs_per_seq = p.cache.H * row_tiles;
+    const int pairs_per_seq = p.cache.H * row_tiles, warp = threadIdx.x / 32;
     const int b = (int)(blockIdx.x / pairs_per_seq), pair = (int)(blockIdx.x % pairs_per_seq), r = (int)blockIdx.y;
     const int64_t *head = reinterpret_cast<const int64_t *>(p.workspace);
     const int64_t share = head[0];
@@ -940,7 +947,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(cons
     const float *parts =
         reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(p.workspace) + workspace_partials(p.B));
     auto part = [&](int c) { return parts + (2 * (int64_t)c + (c == c0)) * partial_floats(ROWS, D); };
-    auto stats = [&](int c) { return *reinterpret_cast<const float2 *>(part(c) + ROWS * D + 2 * r); };
+    auto stats = [&](int c) { return __ldcg(reinterpret_cast<const float2 *>(part(c) + ROWS * D + 2 * r)); };
     // the pieces' maxima, and what each is worth relative to the largest
     const int pieces = c1 - c0 + 1;
     float top = -FLT_MAX;
@@ -950,40 +957,43 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(cons
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (threadIdx.x % 32 == 0) top_s[threadIdx.x / 32] = top;
+    if (threadIdx.x % 32 == 0) top_s[warp] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, top_s[w]);
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, top_s[w]);
     float sum = 0.f;
     for (int c = threadIdx.x; c < pieces; c += kJoinThreads) {
         factor[c] = exp2f(factor[c] - top);
         sum += factor[c] * stats(c0 + c).y;
     }
     __syncthreads();
-    const int d = 2 * (threadIdx.x % (D / 2)), group = threadIdx.x / (D / 2);
-    float3 s = make_float3(0.f, 0.f, sum);
+    const int column = threadIdx.x % kColumns, group = threadIdx.x / kColumns;
+    const int d = (int)blockIdx.z * 2 * kColumns + 2 * column;
+    float2 s = make_float2(0.f, 0.f);
 #pragma unroll 8
     for (int c = group; c < pieces; c += kGroups) {
         const float2 o = __ldcg(reinterpret_cast<const float2 *>(part(c0 + c) + r * D + d));
         s.x += o.x * factor[c];
         s.y += o.y * factor[c];
     }
-    // the row's sum over all threads, its values over the groups
+    // over the threads: the row's sum, and each column's values
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
-    sums[threadIdx.x] = s;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    s.x += __shfl_xor_sync(0xffffffffu, s.x, kColumns);
+    s.y += __shfl_xor_sync(0xffffffffu, s.y, kColumns);
+    if (threadIdx.x % 32 == 0) sum_s[warp] = sum;
+    if (threadIdx.x % 32 < kColumns) value_s[warp][column] = s;
     __syncthreads();
-    if (group != 0) return;
+    if (threadIdx.x >= kColumns) return;
+    sum = 0.f;
+    s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int k = 1; k < kGroups; ++k) {
-        const float3 o = sums[threadIdx.x + k * (D / 2)];
-        s.x += o.x;
-        s.y += o.y;
+    for (int w = 0; w < kJoinWarps; ++w) {
+        sum += sum_s[w];
+        s.x += value_s[w][column].x;
+        s.y += value_s[w][column].y;
     }
-    s.z = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) s.z += sums[32 * w].z;
-    store_pair<D>(p, b, pair / row_tiles, r0 + r, d, s.x, s.y, top, s.z);
+    store_pair<D>(p, b, pair / row_tiles, r0 + r, d, s.x, s.y, top, sum);
 }
 
 // The cache's keys or values as [pages * heads][page][D]: boxes of box_rows
@@ -1038,7 +1048,7 @@ cudaError_t launch_cache(const CacheAttnProblem &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     const bool many = main_ctas(p, C::kTokens) * kWarps >= pairs * kJoinMany;
     const int live = (int)((int64_t)p.Q * p.G < C::kRows ? (int64_t)p.Q * p.G : C::kRows);
-    cfg.gridDim = dim3((unsigned)pairs, many ? live : 1);
+    cfg.gridDim = dim3((unsigned)pairs, many ? live : 1, many ? D / 32 : 1);
     cfg.blockDim = dim3(many ? kJoinThreads : 32 * C::kRows);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
