@@ -6,44 +6,61 @@
 // share a key head reading it together.
 //
 // Bound by memory: the visible tokens' keys and values are read once (1 or 2
-// bytes a value) for 4 G Q flops per pair of them.  The products run on
-// mma.sync m16n8k16: one such tile has 16 keys against 8 query rows, which is
-// what a step of decoding has; a tcgen05 tile has 128 rows, and its operands
-// would have to pass through shared memory as 16-bit values first, which costs
-// more than the product.  At 6.8 TB/s an SM receives 23 e4m3 values a clock; 8
-// rows of products on them are 375 flops a clock.
+// bytes a value) for 4 G Q flops per pair of them.  Measured against the 6.77
+// TB/s of a copy (32 sequences x 8 heads x 8192 tokens, D 128, e4m3, G 4): 95 us,
+// 83%; bf16 of half the length 89 us, 89%; G 8: 80%; G 16, two row tiles: 68%.
+// Above 16 rows per head the products bind (170 TFLOP/s at G 8, Q 64).
 //
-//  * Keys go from global memory straight into the A operand of S^T = K Q^T:
-//    thread (g, t) of a warp (lane = 4 g + t) loads 16-byte pieces of keys g and
-//    g + 8, in a fixed permutation of the head dim that Q's operand follows.
-//    Values are the A operand of O^T = V^T P^T: the thread loads the pieces at
-//    its own head dims of the tokens 2t, 2t+1, 2t+8, 2t+9 and pairs them with
-//    byte permutes.  Neither passes through shared memory.
-//  * e4m3 codes convert to fp16 exactly, two per instruction.  Q rows are
-//    divided by a power of two first so that they fit fp16 (bf16 values keep
-//    all their bits down to 2^-14 of the row's largest).  The page's scale of K
-//    multiplies the scores, the one of V the weights: P is kept relative to the
-//    largest V scale met, which rescales the accumulators when it grows.
-//    A bf16 cache runs the same in bf16.
+// The products run on mma.sync m16n8k16: one such tile has 16 keys against 8
+// query rows, which is what a step of decoding has.  A tcgen05 tile has 128
+// rows, and e4m3 keys would have to be written back to shared memory as 16-bit
+// values to meet a bf16 query there, which costs more than the product.  At 6.8
+// TB/s an SM receives 23 e4m3 values a clock; 8 rows of products on them are 375
+// flops a clock.  What binds beside the memory is the work on the values:
+// converting them (two codes in 2 cycles of a sub-partition, or 4 where they
+// lie in a word's upper half), pairing them, and the latency of it all with
+// two warps on a sub-partition.
+//
+//  * A step of a warp is 64 tokens of one head (32 of bf16 at D 128): keys and
+//    values come by TMA (128-byte swizzle, so that the reads below are free of
+//    bank conflicts) into the warp's own ring and go from there into registers
+//    at once, which frees the slot for the next step while this one computes:
+//    one slot in flight and one in registers.  With the slot freed only after
+//    the products the same took 112 us instead of 98 (64 sequences, ragged to
+//    8192), and with three CTAs of fewer registers on an SM spilling cost more
+//    than the added warps hid.
+//  * Keys are the A operand of S^T = K Q^T: thread (g, t) of a warp (lane =
+//    4 g + t) reads 16-byte pieces of keys g and g + 8, in a fixed permutation of
+//    the head dim that Q's operand follows.  Values are the A operand of
+//    O^T = V^T P^T: the thread reads the pieces at its own head dims of the
+//    tokens 2t, 2t+1, 2t+8, 2t+9 and pairs them with byte permutes.
+//  * e4m3 codes convert to fp16 exactly.  Q rows are divided by a power of two
+//    first so that they fit fp16 (bf16 values keep all their bits down to 2^-14
+//    of the row's largest).  The page's scale of K multiplies the scores, the
+//    one of V the weights: P is kept relative to the largest V scale met, which
+//    rescales the accumulators when it grows.  P is rounded to fp16 (11 bits),
+//    beside a bf16 cache to bf16 (8 bits) like the operands it meets.
 //  * S^T's accumulators hold keys along lanes' g and rows along t: after
-//    exp, one 8 x 8 transpose (movmatrix) per half tile makes them the B
-//    operand P^T.  Statistics, sums and accumulators are float32.
+//    exp, one 8 x 8 transpose (movmatrix) per 8 keys makes them the B operand
+//    P^T.  Statistics, sums and accumulators are float32, and the sum takes the
+//    unrounded weights.
 //  * The maximum is only raised when a score exceeds it by 2^8 (votes instead of
 //    reductions on most steps); weights then stay below 2^8.
-//  * The steps (4 KB of keys and 4 KB of values) of all sequences, heads and
-//    row tiles form one list, which the warps of one wave of CTAs share out
-//    evenly, so that ragged batches and a few long sequences fill the SMs
-//    alike.  A warp works alone: its TMA-filled ring runs on from one (sequence,
-//    head, row tile) to the next, and no barrier joins it to other warps.
-//    Where it covers all steps of one it writes the rows; where a cut falls
-//    inside one, the pieces' statistics and accumulators go to the workspace
-//    and a second, dependent launch joins them.  Nothing is joined by atomics:
-//    results do not depend on the order in which warps run.
-//  * Only tiles at an edge (the last tokens, a window's ends, a bad page)
+//  * The steps of all sequences, heads and row tiles form one list, which the
+//    warps of one wave of CTAs share out evenly, so that ragged batches and a
+//    few long sequences fill the SMs alike (clusters of CTAs, one for each
+//    sequence and head, took 108 and 116 us for what takes 98 and 96 now).  A
+//    warp works alone: its ring runs on from one (sequence, head, row tile) to
+//    the next, and no barrier joins it to other warps.  Where it covers all
+//    steps of one it writes the rows; where a cut falls inside one, the pieces'
+//    statistics and accumulators go to the workspace and a second, dependent
+//    launch joins them.  Nothing is joined by atomics: results do not depend on
+//    the order in which warps run.
+//  * Only steps at an edge (the last tokens, a window's ends, a bad page)
 //    evaluate the mask; there the values of tokens that no row keeps are
 //    zeroed, so that whatever lies in those slots has no effect, and where
 //    rows of the call differ in what they keep and such a token's value is not
-//    finite, the tile's product is done once per query token.
+//    finite, the step's product is done once per query token.
 #include <cfloat>
 #include <climits>
 
@@ -59,14 +76,17 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kJoinThreads = 512;
-constexpr int kJoinMany = 8;       // warps of the main launch per pair, from which a CTA joins one row
+constexpr int kJoinMany = 8;       // warps of the main launch per pair, from which CTAs join a row
 constexpr int kMaxCtas = 152 * 2;  // of the main launch: two on every SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Entering and finishing a (sequence, head, row tile) costs a warp about as
-// much time as two steps: the list counts that many more for each.
+// Entering and finishing a (sequence, head, row tile) costs a warp the time of
+// some steps: the list counts that many units more for each (0 of 512 pairs:
+// 112 us, 1: 104, 2 to 6: 98).  A warp takes one unit at least: few steps are
+// over sooner with more of them in flight (513 tokens of 8 heads: 12.5 us, and
+// 14.5 with two, 17.6 with four).
 constexpr int kEnterCost = 3;
-constexpr int kMinShare = 1;  // fewest of the list's units a warp takes
+constexpr int kMinShare = 1;
 constexpr float kRaise = 8.f;  // raise the running max only beyond 2^8
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

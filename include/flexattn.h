@@ -504,8 +504,9 @@ typedef struct {
  * when an append raises it, the page's earlier codes are rounded to it.  NaN
  * and infinities are stored as NaN and do not raise the scale.  Tokens whose
  * position has no page (past max_pages, or a bad entry) are dropped; slots
- * that get no token keep their contents.  A page must not be appended to by
- * two sequences of one call, or by two calls that may run at the same time.
+ * that get no token keep their contents.  A page must not be appended to from
+ * two places of the page table in one call, or by two calls that may run at
+ * the same time (sequences may share pages that they only read).
  * Errors: FLEX_ERR_INVALID_ARG, FLEX_ERR_SHAPE, FLEX_ERR_ALIGNMENT,
  * FLEX_ERR_UNSUPPORTED (page size, head dim, more than 2^30 positions per
  * sequence, sizes as for flex_rope_fwd), FLEX_ERR_CUDA.  Asynchronous on
@@ -531,10 +532,11 @@ FLEX_API int flex_kv_cache_append(const flex_kv_cache *cache, const flex_tensor 
  *   out, lse  : device, contiguous [B, Hq, Q, D] bf16 and [B, Hq, Q] float32.
  * Rows that keep nothing get out = 0, lse = -inf; tokens on a bad page count
  * as masked.  What lies in slots that a row does not keep has no effect on
- * it, NaN included.  Made for few query tokens (a decoding step, a handful of
- * tokens to check); any Q is computed, at the rate of a step of 16 rows per
- * key head.  Errors: as flex_kv_cache_append, and FLEX_ERR_UNSUPPORTED for
- * fp32 q and for the prefix and document masks.
+ * it, NaN included.  Scales are taken as positive numbers of any value; the
+ * append writes powers of two.  Made for few query tokens (a decoding step, a
+ * handful of tokens to check); any Q is computed, at up to 170 TFLOP/s (whole
+ * prompts belong to flex_attention_fwd).  Errors: as flex_kv_cache_append, and
+ * FLEX_ERR_UNSUPPORTED for fp32 q and for the prefix and document masks.
  *   workspace : device, 16-byte aligned, at least as many bytes as
  *               flex_kv_cache_attention_workspace gives (else FLEX_ERR_SHAPE);
  *               any contents.  Calls that may run at the same time (other
