@@ -18,7 +18,12 @@
 // codes.  The sines and cosines, which depend on (token, pair) only, are
 // computed once per CTA into shared memory, with sincospi: the fast sine and
 // cosine moved 4e-5 of the codes of a prompt (2-norm) to a neighbour.  The
-// rotated key is quantised from float32, not from a bf16 rounding of it.
+// rotated key is quantised from float32, not from a bf16 rounding of it.  Four
+// prompts of up to 4095 tokens (8 heads, D 128, e4m3) take 18 us, 3.0 TB/s: a
+// head's chain of loads, reduction over the CTA and stores binds there (43% of
+// the warps an SM can hold, half the issue slots; loading the next head ahead
+// needs the registers of a CTA and gained 8%); a step of 32 sequences takes
+// 3.7 us, most of it the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

@@ -25,10 +25,9 @@
 //    values come by TMA (128-byte swizzle, so that the reads below are free of
 //    bank conflicts) into the warp's own ring and go from there into registers
 //    at once, which frees the slot for the next step while this one computes:
-//    one slot in flight and one in registers.  With the slot freed only after
-//    the products the same took 112 us instead of 98 (64 sequences, ragged to
-//    8192), and with three CTAs of fewer registers on an SM spilling cost more
-//    than the added warps hid.
+//    one slot in flight and one in registers (two slots of half the size: 101
+//    us for 98, 64 sequences ragged to 8192).  Eight warps an SM, since twelve
+//    leave 168 registers each, too few for this without spilling.
 //  * Keys are the A operand of S^T = K Q^T: thread (g, t) of a warp (lane =
 //    4 g + t) reads 16-byte pieces of keys g and g + 8, in a fixed permutation of
 //    the head dim that Q's operand follows.  Values are the A operand of
@@ -48,9 +47,9 @@
 //    reductions on most steps); weights then stay below 2^8.
 //  * The steps of all sequences, heads and row tiles form one list, which the
 //    warps of one wave of CTAs share out evenly, so that ragged batches and a
-//    few long sequences fill the SMs alike (clusters of CTAs, one for each
-//    sequence and head, took 108 and 116 us for what takes 98 and 96 now).  A
-//    warp works alone: its ring runs on from one (sequence, head, row tile) to
+//    few long sequences fill the SMs alike (an earlier form with a cluster of
+//    CTAs for each took 108 and 116 us for what takes 98 and 96 now).  A warp
+//    works alone: its ring runs on from one (sequence, head, row tile) to
 //    the next, and no barrier joins it to other warps.  Where it covers all
 //    steps of one it writes the rows; where a cut falls inside one, the pieces'
 //    statistics and accumulators go to the workspace and a second, dependent
@@ -81,10 +80,10 @@ constexpr int kMaxCtas = 152 * 2;  // of the main launch: two on every SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Entering and finishing a (sequence, head, row tile) costs a warp the time of
-// some steps: the list counts that many units more for each (0 of 512 pairs:
-// 112 us, 1: 104, 2 to 6: 98).  A warp takes one unit at least: few steps are
-// over sooner with more of them in flight (513 tokens of 8 heads: 12.5 us, and
-// 14.5 with two, 17.6 with four).
+// some steps: the list counts that many units more for each (512 pairs, ragged
+// to 8192 tokens: none 134 us, 1: 114, 2 to 6: 98).  A warp takes one unit at
+// least: few steps are over sooner with more of them in flight (513 tokens of 8
+// heads: 12.5 us, and 14.6 with two, 18.1 with four).
 constexpr int kEnterCost = 3;
 constexpr int kMinShare = 1;
 constexpr float kRaise = 8.f;  // raise the running max only beyond 2^8
@@ -884,8 +883,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins the pieces of one (sequence, head, row tile), one warp a row; nothing
-// to do for one that a single warp covered.  For lists that a pair is a few
-// warps' share of: a CTA for each row as below costs 10 us more at 512 pairs.
+// to do for one that a single warp covered.  For lists in which a pair is a few
+// warps' share (512 pairs: 98 us in all, 137 with the kernel below).
 template <int D, int ROWS, int TOKENS>
 __global__ void __launch_bounds__(32 * ROWS) cache_attention_join_few_kernel(const CacheAttnProblem p, int row_tiles) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -948,7 +947,7 @@ __global__ void __launch_bounds__(32 * ROWS) cache_attention_join_few_kernel(con
 
 // The same for pairs that many warps share: one CTA for 32 head dims of a row,
 // two of them a thread, in groups that share out the pieces (16 pairs of 76
-// pieces: 4 us, against 13 with one warp a row).
+// pieces: 96 us in all, 109 with the kernel above).
 template <int D, int ROWS, int TOKENS>
 __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(const CacheAttnProblem p, int row_tiles) {
     constexpr int kColumns = 16, kGroups = kJoinThreads / kColumns, kJoinWarps = kJoinThreads / 32;

@@ -9,7 +9,10 @@
 // registers for one item (two 16-byte vectors: the two halves of eight pairs,
 // or four in fp32) of one token and walks the heads of both tensors with them.
 // Rotating a bf16 head costs two loads, two stores and ~60 other instructions
-// per thread; one sincospi costs ~40, which eight heads per thread hide.
+// per thread; one sincospi costs ~40, which four heads or more per thread hide.
+// q and k of B2 H32 S16384 D128 in bf16 take 163 us, 6.6 TB/s: 97% of the rate
+// of a copy.  A step of 16 sequences (40 heads each) takes 3.1 us, of which the
+// launch is most.
 // Frequencies are converted to fixed-point turns once per CTA: the conversion
 // is double precision, of which an SM does about two operations a clock.
 #include <cuda_bf16.h>
@@ -139,7 +142,7 @@ cudaError_t launch_rope_typed(const RopeProblem &p, cudaStream_t stream) {
     const int64_t ctas = (threads + kRopeThreads - 1) / kRopeThreads;
     const int total = p.heads[0] + p.heads[1];
     // Heads per CTA: 16, so that the angles are shared, unless that leaves
-    // SMs without work
+    // fewer than four CTAs for every SM; four are loaded at a time
     int per = 16;
     while (per > 4 && ctas * ((total + per - 1) / per) < 4 * 152) per /= 2;
     const dim3 grid((unsigned)ctas, (unsigned)((total + per - 1) / per));

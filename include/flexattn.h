@@ -1,7 +1,7 @@
 /*
- * flexattn.h -- C-ABI of the GB300 (sm_103a) block-sparse FlexAttention forward.
+ * flexattn.h -- C-ABI of the GB300 (sm_103a) block-sparse FlexAttention.
  *
- * Two calls do the work:
+ * These calls do the work:
  *   flex_block_mask_create  builds a BlockMask from an enumerated mask_mod;
  *   flex_attention_fwd      runs softmax(mask(score_mod(Q K^T * scale))) V
  *                           block-sparsely from that BlockMask and returns the
