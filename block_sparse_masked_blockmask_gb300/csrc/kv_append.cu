@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int he
             const uint64_t t0 = turns[pair], t1 = turns[pair + 1];
             for (int tok = threadIdx.x / kPer; tok < n; tok += blockDim.x / kPer) {
                 float4 w;
-                sincospif(half_turns(t0, (int32_t)(lo + tok)), &w.y, &w.x);
-                sincospif(half_turns(t1, (int32_t)(lo + tok)), &w.w, &w.z);
+                sincos_at(t0, (int32_t)(lo + tok), &w.y, &w.x);
+                sincos_at(t1, (int32_t)(lo + tok), &w.w, &w.z);
                 w.x *= p.attention_scale;
                 w.y *= p.attention_scale;
                 w.z *= p.attention_scale;

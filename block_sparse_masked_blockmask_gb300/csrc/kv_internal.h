@@ -70,10 +70,18 @@ __device__ __forceinline__ uint64_t turns_per_position(double inv_freq) {
     const double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
     return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
 }
-// The angle of a position in half turns, in [-1, 1).
-__device__ __forceinline__ float half_turns(uint64_t turns, int32_t position) {
-    const int32_t hi = (int32_t)((turns * (uint64_t)(int64_t)position) >> 32);
-    return (float)hi * 4.656612873077393e-10f;  // 2^-31
+// Sine and cosine of a position's angle.  What is left of it beside whole
+// quarter turns goes to float32, at most 1/4 half turn: rounding it moves the
+// angle by 2^-28 of a turn at most (a rounding of all of it: 2^-26).
+__device__ __forceinline__ void sincos_at(uint64_t turns, int32_t position, float *sine, float *cosine) {
+    const uint64_t angle = turns * (uint64_t)(int64_t)position;
+    const uint32_t quarters = ((uint32_t)(angle >> 32) + 0x20000000u) >> 30;
+    const int64_t rest = (int64_t)(angle - ((uint64_t)quarters << 62));
+    float s, c;
+    sincospif((float)(int32_t)(rest >> 30) * 1.1641532182693481e-10f, &s, &c);  // 2^-33
+    const float a = quarters & 1u ? c : s, z = quarters & 1u ? s : c;
+    *sine = quarters & 2u ? -a : a;
+    *cosine = (quarters + 1u) & 2u ? -z : z;
 }
 
 }  // namespace flex

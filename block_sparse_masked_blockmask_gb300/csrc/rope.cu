@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeProblem p, int h
         const int pos = p.positions ? p.positions[token] : s;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            sincospif(half_turns(turns[item * V + j], pos), &n[j], &c[j]);
+            sincos_at(turns[item * V + j], pos, &n[j], &c[j]);
             c[j] *= p.attention_scale;
             n[j] *= p.attention_scale * p.direction;
         }

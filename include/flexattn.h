@@ -456,7 +456,7 @@ FLEX_API int flex_rope_frequencies(int32_t rotary_dim, double base, int32_t scal
  *   q_out, k_out : tensors of the inputs' shapes with their own strides;
  *               they may be the inputs themselves (same data and strides) and
  *               must not overlap them otherwise.
- * Angles are exact to 2^-33 of a turn for every position; sine, cosine and the
+ * Angles are within 2^-28 of a turn at every position; sine, cosine and the
  * rotation are float32, the result is rounded once.
  * Errors: FLEX_ERR_INVALID_ARG, FLEX_ERR_SHAPE, FLEX_ERR_ALIGNMENT,
  * FLEX_ERR_UNSUPPORTED (head dim, rotary_dim not a multiple of 16, B > 65535,
@@ -553,7 +553,7 @@ FLEX_API int flex_kv_cache_attention(const flex_tensor *q, const flex_kv_cache *
 
 /*
  * Bytes of workspace of flex_kv_cache_attention for these sizes (pointers in
- * q are checked, not read).  At most 6 MB and 8 bytes per sequence.  Errors: as
+ * q are checked, not read).  At most 20 MiB and 8 bytes per sequence.  Errors: as
  * flex_kv_cache_attention.
  */
 FLEX_API int flex_kv_cache_attention_workspace(const flex_tensor *q, const flex_kv_cache *cache, int32_t max_pages,
