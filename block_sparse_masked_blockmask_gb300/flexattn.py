@@ -203,6 +203,17 @@ def _stream_handle(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream`, from that stream's pool: what the pool last lent it for lies before the
+    call in the stream's order (None: torch's current stream)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_handle(stream, device), device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _device_guard(device):
     """A context in which `device` is the current CUDA device (nothing to enter when it already is)."""
     return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
@@ -575,13 +586,13 @@ def _rope_params(inv_freq: torch.Tensor, layout: int, attention_scale: float, de
 def _rope(name: str, q, k, inv_freq, positions, layout, attention_scale, q_out, k_out, stream):
     device = q.device
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        q_out = _empty(q.shape, q.dtype, device, stream)
     elif q_out.device != device:
         raise ValueError("q, k and their outputs must be on one device")
     tk = ok = None
     if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
+            k_out = _empty(k.shape, k.dtype, device, stream)
         if k.device != device or k_out.device != device:
             raise ValueError("q, k and their outputs must be on one device")
         tk, ok = _tensor(k), _tensor(k_out)
@@ -604,7 +615,8 @@ def flex_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, inv_freq: torch.Tenso
     """q [B, Hq, S, D] and k [B, Hk, S, D] (or None) turned by their positions; returns (q_out, k_out).
 
     positions: int32 [B, S] (default 0 .. S - 1).  The outputs may be the
-    inputs.  Asynchronous on `stream`.
+    inputs; those not given are allocated from `stream`'s pool.  Asynchronous
+    on `stream`.
     """
     return _rope("flex_rope_fwd", q, k, inv_freq, positions, layout, attention_scale, q_out, k_out, stream)
 
@@ -688,8 +700,9 @@ def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.T
 
     kv_lens int32 [B] counts the tokens in the cache, the query tokens among
     them.  workspace: a uint8 tensor of flex_kv_cache_attention_workspace()
-    bytes, not shared with calls that may run at the same time (allocated when
-    none is given).  Asynchronous on `stream`.
+    bytes, not shared with calls that may run at the same time.  It and the
+    outputs are allocated from `stream`'s pool when not given.  Asynchronous on
+    `stream`.
     """
     device, shape = cache.k.device, q.shape
     if len(shape) != 4 or q.device != device:
@@ -701,29 +714,24 @@ def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.T
     table = _device_array(page_table, "page_table", torch.int32, device, (B, max_pages))
     lens = _device_array(kv_lens, "kv_lens", torch.int32, device, (B,))
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=device)
+        out = _empty(shape, q.dtype, device, stream)
     else:
         _device_array(out, "out", q.dtype, device, shape)
     if lse is None:
-        lse = torch.empty((B, Hq, Q), dtype=torch.float32, device=device)
+        lse = _empty((B, Hq, Q), torch.float32, device, stream)
     else:
         _device_array(lse, "lse", torch.float32, device, (B, Hq, Q))
     params = None if mask_kind == FLEX_MASK_CAUSAL and not sinks else \
         ctypes.byref(_mask_params(mask_kind, window, 0, sinks))
-    handle = _stream_handle(stream, device)
     if workspace is None:
         size = _cache_workspace_bytes(shape, cache.k.shape, cache.struct.dtype, max_pages, mask_kind, window, sinks)
-        workspace = torch.empty(size, dtype=torch.uint8, device=device)
-        if stream is not None and handle != _stream_handle(None, device):
-            # not the stream it was allocated on: keep it from being reused before that is done
-            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else
-                                    torch.cuda.ExternalStream(handle, device))
+        workspace = _empty((size,), torch.uint8, device, stream)
     else:
         _device_array(workspace, "workspace", torch.uint8, device, workspace.shape)
         size = workspace.numel()
     rc = _call(device, load_library().flex_kv_cache_attention, _tensor(q), cache._ref, table, max_pages, lens,
                mask_kind, params, score_kind, float(score_param), D**-0.5 if scale is None else float(scale),
-               out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, handle)
+               out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, _stream_handle(stream, device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_kv_cache_attention")
     return out, lse

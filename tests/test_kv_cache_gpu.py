@@ -420,3 +420,64 @@ def test_other_stream_and_results_repeat():
     torch.cuda.synchronize()
     for o, l_ in got:
         assert torch.equal(o, a[0]) and torch.equal(l_, a[1])
+
+
+def test_calls_at_the_same_time():
+    """Calls on several streams at once, with the memory that they allocate themselves, and as two graphs."""
+    gen = torch.Generator().manual_seed(23)
+    lens = torch.randint(2000, 4000, (24,), generator=gen).tolist()
+    cache, table = filled(gen, lens, 4, 64, 128, E4M3)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    qs = [torch.randn((24, 16, 1, 128), generator=gen).bfloat16().cuda() for _ in range(3)]
+    want = [fa.flex_kv_cache_attention(q, cache, table, n) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [fa.flex_kv_cache_attention(qs[0], cache, table, n),
+               fa.flex_kv_cache_attention(qs[1], cache, table, n, stream=streams[0]),
+               fa.flex_kv_cache_attention(qs[2], cache, table, n, stream=streams[1].cuda_stream)]
+        torch.cuda.synchronize()
+        for (o, l_), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(l_, wl)
+    graphs, outs = [], []
+    for s, q in zip(streams, qs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append([fa.flex_kv_cache_attention(q, cache, table, n) for _ in range(4)])
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for g, s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    for results, (wo, wl) in zip(outs, want):
+        for o, l_ in results:
+            assert torch.equal(o, wo) and torch.equal(l_, wl)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, BF16], ids=["e4m3", "bf16"])
+def test_pages_and_strides_past_32_bits(dtype):
+    """Pages behind 2^32 elements of the pool, and new tokens whose strides pass 2^31 elements: as near ones."""
+    H, D, page = 4, 128, 256
+    pages = 2**32 // (H * page * D) + 6
+    gen = torch.Generator().manual_seed(29)
+    far, near = fa.flex_kv_cache_create(pages, H, D, page, dtype), new_cache(6, H, page, D, dtype)
+    far_table = torch.tensor([[pages - 1, 3], [pages - 4, pages - 2]], dtype=torch.int32, device="cuda")
+    near_table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+    wide = torch.empty(2**31 + 2**20, dtype=BF16, device="cuda")
+    k = wide.as_strided((2, H, 300, D), (2**31, 300 * D, D, 1))
+    k.copy_(torch.randn(k.shape, generator=gen).cuda())
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    inv = fa.flex_rope_frequencies(D)
+    for cache, table in ((far, far_table), (near, near_table)):
+        fa.flex_kv_cache_append(cache, k, k, table, lens, inv_freq=inv)
+    for ids, other in zip(far_table.tolist(), near_table.tolist()):
+        for i, j, used in zip(ids, other, (page, 300 - page)):
+            for x, y in ((far.k, near.k), (far.v, near.v)):
+                assert torch.equal(x[i, :, :used].view(torch.uint8), y[j, :, :used].view(torch.uint8))
+    q = wide.as_strided((2, 2 * H, 1, D), (2**31, D, D, 1))
+    turned = [fa.flex_rope_fwd(x, None, inv)[0] for x in (q, q.contiguous())]
+    assert torch.equal(*turned)
+    n = torch.tensor([300, 290], dtype=torch.int32, device="cuda")
+    a, b = (fa.flex_kv_cache_attention(x, c, t, n) for x, c, t in ((q, far, far_table), (q.contiguous(), near, near_table)))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
