@@ -146,8 +146,22 @@ int *device_status_word(int *err) {
     }
     std::lock_guard<std::mutex> lock(g_ws_mutex);
     if (!g_status[dev]) {
+        // The first call on a device may be one that a stream captures: the
+        // memory is made and cleared outside of the capture, on a stream of
+        // its own.
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        cudaStream_t own = nullptr;
         int *p = nullptr;
-        if (cudaMalloc(&p, 256) != cudaSuccess || cudaMemset(p, 0, 256) != cudaSuccess) {
+        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) {
+            *err = FLEX_ERR_CUDA;
+            return nullptr;
+        }
+        const bool ok = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) == cudaSuccess &&
+                        cudaMalloc(&p, 256) == cudaSuccess && cudaMemsetAsync(p, 0, 256, own) == cudaSuccess &&
+                        cudaStreamSynchronize(own) == cudaSuccess;
+        if (own) cudaStreamDestroy(own);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (!ok) {
             *err = FLEX_ERR_CUDA;
             return nullptr;
         }

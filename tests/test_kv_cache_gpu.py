@@ -13,6 +13,9 @@ largest weight (at least 2^-8 of 1 in the kernel's units) times the largest V
 scale; out is rounded once, 2^-8.
 """
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -481,3 +484,28 @@ def test_pages_and_strides_past_32_bits(dtype):
     n = torch.tensor([300, 290], dtype=torch.int32, device="cuda")
     a, b = (fa.flex_kv_cache_attention(x, c, t, n) for x, c, t in ((q, far, far_table), (q.contiguous(), near, near_table)))
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+FIRST_CALL = """
+import torch
+from block_sparse_masked_blockmask_gb300 import flexattn as fa
+c = fa.flex_kv_cache_create(3, 2, 64, 16, torch.bfloat16)
+c.k.normal_(), c.v.normal_()
+t = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+n = torch.tensor([40], dtype=torch.int32, device="cuda")
+q = torch.randn((1, 4, 1, 64), device="cuda").bfloat16()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = fa.flex_kv_cache_attention(q, c, t, n)
+g.replay()
+want = fa.flex_kv_cache_attention(q, c, t, n)
+assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+assert fa.flex_device_status() == fa.FLEX_OK
+print("captured")
+"""
+
+
+def test_first_call_of_a_process_is_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
