@@ -159,3 +159,83 @@ def test_host_entry_point_and_options():
     x = (q.double() @ k.double().transpose(2, 3)) / math.sqrt(D)
     x = x.masked_fill(~dense_mask(S, S, 50, 7), -math.inf)
     assert (m.cpu().double() - x.amax(-1)).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("score", [fa.FLEX_SCORE_IDENTITY, fa.FLEX_SCORE_SOFTCAP, fa.FLEX_SCORE_ALIBI])
+def test_as_the_older_kinds(score, D, dtype):
+    """Every score_mod, without sinks against the sliding window and with a window of all tokens against causal:
+    the same products, summed in float32 in another order at most.  The older bf16 forward sums rounded weights
+    (2^-8 of lse, and of out beside its own rounding and the weights').  The gradients of equal inputs differ by a
+    last rounding and by float32 sums: 2^-12 of the largest covers those of 500 terms."""
+    S, dt = 500, torch.bfloat16 if dtype == "bf16" else torch.float32
+    gen = torch.Generator().manual_seed(score * 10 + D)
+    q, k, v, g = (torch.randn((2, 3, S, D), generator=gen).to(dt).cuda() for _ in range(4))
+    r = 2.0**-8 if dtype == "bf16" else 2.0**-16
+    for new, old in ((dict(window=150), dict(mask_kind=fa.FLEX_MASK_SLIDING_WINDOW, window=150)),
+                     (dict(window=S, sinks=9), dict(mask_kind=fa.FLEX_MASK_CAUSAL))):
+        a = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, 2, 3, S, S, **new)
+        b = fa.flex_block_mask_create(B=2, H=3, q_len=S, kv_len=S, **old)
+        (oa, la), (ob, lb) = (fa.flex_attention_fwd(q, k, v, m, score, 7.0) for m in (a, b))
+        assert (oa.float() - ob.float()).abs().max() <= 4 * r * v.float().abs().max()
+        assert ((la - lb).abs() <= 1.01 * r * (1 + lb.abs() * (0 if dtype == "bf16" else 1))).all()
+        ga, gb = (fa.flex_attention_bwd(q, k, v, ob, lb, g, m, fa.flex_block_mask_transpose(m), score, 7.0)
+                  for m in (a, b))
+        for x, y in zip(ga, gb):
+            x, y = x.float(), y.float()
+            assert ((x - y).abs() <= 2 * r * y.abs() + 2.0**-12 * y.abs().max()).all()
+
+
+def test_training_step_with_rotary_positions():
+    """Rotation, attention, its gradients and the rotation back, in float32, against the formula of all of it in
+    float64; the formula against differences.  Beside the attention's own bounds: a rotated value is off by 2^-21
+    of its pair, which moves scores by less than the bound of their own rounding and gradients by 2^-20 of the sum
+    of their terms' sizes; turning back adds up the bounds of a pair."""
+    B, H, S, D, rotary, window, sinks = 2, 3, 300, 64, 32, 70, 5
+    scale = 1.0 / math.sqrt(D)
+    gen = torch.Generator().manual_seed(5)
+    q, k, v, g = (torch.randn((B, H, S, D), generator=gen).cuda() for _ in range(4))
+    keep = dense_mask(S, S, window, sinks).cuda()
+    inv = fa.flex_rope_frequencies(rotary)
+    at = torch.arange(1000, 1000 + S, dtype=torch.int32, device="cuda").expand(B, S).contiguous()
+    bm = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, B, H, S, S, window=window, sinks=sinks)
+    qr, kr = fa.flex_rope_fwd(q, k, inv, at)
+    out, lse = fa.flex_attention_fwd(qr, kr, v, bm)
+    dqr, dkr, dv = fa.flex_attention_bwd(qr, kr, v, out, lse, g, bm, fa.flex_block_mask_transpose(bm))
+    dq, dk = fa.flex_rope_bwd(dqr, dkr, inv, at)
+
+    def turn(x, sign):
+        y, h = x.double().clone(), rotary // 2
+        angle = sign * at.double()[:, None, :, None] * inv
+        z = torch.complex(y[..., :h], y[..., h:rotary]) * torch.polar(torch.ones_like(angle), angle)
+        y[..., :h], y[..., h:rotary] = z.real, z.imag
+        return y
+
+    def pairs(x):
+        y, h = x.clone(), rotary // 2
+        y[..., :h] = y[..., h:rotary] = x[..., :h] + x[..., h:rotary]
+        return y
+
+    ref, absolute, product, e_s = reference(turn(q, 1), turn(k, 1), v, g, keep, fa.FLEX_SCORE_IDENTITY, 0.0, scale)
+    e_p = 4 * float(e_s.max()) + 2.0**-18
+    bound = {n: 2.0**-18 * (ref[n].abs() + 2 * absolute[n]) + 2.0**-20 * absolute[n] + (e_p + 2.0**-18) * product[n]
+             for n in ("out", "dq", "dk", "dv")}
+    want = dict(out=ref["out"], dv=ref["dv"], dq=turn(ref["dq"], -1), dk=turn(ref["dk"], -1))
+    for n in ("dq", "dk"):
+        bound[n] = pairs(bound[n]) + 2.0**-21 * pairs(ref[n].abs())
+    for n, x in dict(out=out, dq=dq, dk=dk, dv=dv).items():
+        diff = (x.double() - want[n]).abs()
+        assert (diff <= bound[n]).all(), (n, float((diff - bound[n]).max()))
+
+    def loss(q, k, v):
+        s = (scale * (turn(q, 1) @ turn(k, 1).transpose(2, 3))).masked_fill(~keep, -math.inf)
+        return float((torch.softmax(s, -1) @ v.double() * g.double()).sum())
+
+    x = [t.double() for t in (q, k, v)]
+    step = [torch.randn(t.shape, generator=gen, dtype=torch.float64).cuda() for t in x]
+    eps = 1e-5  # the difference is off by about eps^2 times a third derivative, and 1e-16 / eps of the loss
+    up, down = (loss(*(t + s * eps * d for t, d in zip(x, step))) for s in (1, -1))
+    slope = sum(float((want[n] * d).sum()) for n, d in zip(("dq", "dk", "dv"), step))
+    size = sum(float((want[n] * d).abs().sum()) for n, d in zip(("dq", "dk", "dv"), step))
+    assert abs((up - down) / (2 * eps) - slope) <= 1e-6 * size
