@@ -13,17 +13,17 @@
 // Bound by memory (read 2 or 4 bytes and write 1 or 2 per value).  One CTA
 // owns a page of one of the two tensors for a run of heads, so the scales need
 // no exchange between CTAs and no atomics in global memory: head by head it
-// reads the tokens that fall on its page into registers (two items of 16 values
-// a thread), rotates them in float32, reduces the largest magnitude, and writes
-// codes.  The sines and cosines, which depend on (token, pair) only, are
-// computed once per CTA into shared memory, with sincospi: the fast sine and
-// cosine moved 4e-5 of the codes of a prompt (2-norm) to a neighbour.  The
-// rotated key is quantised from float32, not from a bf16 rounding of it.  Four
-// prompts of up to 4095 tokens (8 heads, D 128, e4m3) take 18 us, 3.0 TB/s: a
-// head's chain of loads, reduction over the CTA and stores binds there (43% of
-// the warps an SM can hold, half the issue slots; loading the next head ahead
-// needs the registers of a CTA and gained 8%); a step of 32 sequences takes
-// 3.7 us, most of it the launch.
+// reads the tokens that fall on its page into registers (an item of 16 values a
+// thread, or two), rotates them in float32, reduces the largest magnitude, and
+// writes codes, while the next head's values are on the way.  The sines and
+// cosines, which depend on (token, pair) only, are computed once per CTA into
+// shared memory, to float32's accuracy: the fast sine and cosine moved 4e-5 of
+// the codes of a prompt (2-norm) to a neighbour.  The rotated key is quantised
+// from float32, not from a bf16 rounding of it.  Four prompts of up to 4095
+// tokens (8 heads, D 128, e4m3) take 14 us, 3.8 TB/s: about two thirds of it
+// are the instructions (a quarter of them the sines and cosines) and what the
+// last CTAs leave idle.  A step of 32 sequences takes 3.2 us, most of it the
+// launch.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -33,7 +33,6 @@
 namespace flex {
 namespace {
 
-constexpr int kItems = 2;   // items (of 16 values) per thread
 constexpr int kMinExp = -126;  // scales are normal float32 powers of two
 
 // Four floats to e4m3 (round to nearest even), the first in the lowest byte.
@@ -70,31 +69,47 @@ __device__ __forceinline__ float power_scale(uint32_t amax_bits) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ void load8(const uint16_t *src, float (&x)[8]) {
-    const uint4 r = *reinterpret_cast<const uint4 *>(src);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight values as they lie in memory, and as floats.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+    uint4 r;
+    __device__ __forceinline__ void load(const uint16_t *src) { r = *reinterpret_cast<const uint4 *>(src); }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(w[j] << 16);
+            x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
     }
-}
-__device__ __forceinline__ void load8(const float *src, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *src) {
+        a = *reinterpret_cast<const float4 *>(src);
+        b = *reinterpret_cast<const float4 *>(src + 4);
+    }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
 
-// T: source type; E4M3: the cache's codes (else bf16).
-template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int heads_per_cta) {
+// T: source type; E4M3: the cache's codes (else bf16); kItems: items (of 16
+// values) per thread.
+template <typename T, bool E4M3, int D, int kItems>
+__global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int heads_per_cta, int groups) {
     // cosines and sines of two pairs each: [token][quarter of an item][item],
     // so that neighbouring threads read neighbouring 16 bytes
     extern __shared__ __align__(16) float4 table[];
     __shared__ uint64_t turns[64];
     __shared__ uint32_t amax_smem[2];
     constexpr int IT = D / 16;  // items per token
-    const int is_v = blockIdx.y & 1, h_first = (int)(blockIdx.y >> 1) * heads_per_cta, b = blockIdx.z;
+    const int is_v = (int)blockIdx.z >= groups, h_first = ((int)blockIdx.z - (is_v ? groups : 0)) * heads_per_cta;
+    const int b = blockIdx.y;
     const int h_last = min(h_first + heads_per_cta, p.cache.H);
     const int page = p.cache.page;
     const bool rotate = !is_v && p.inv_freq;
@@ -108,6 +123,34 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int he
     const int id = p.page_table[(int64_t)b * p.max_pages + slot];
     const int old_n = (int)(lo - page0);                     // tokens the page already holds
     const int n = (int)(hi - lo), total = n * IT;
+    // this thread's items: where their first vectors lie, in the source (of the
+    // first head) and within the page, and how far behind the second ones are
+    const int64_t *st = is_v ? p.v_stride : p.k_stride;
+    const T *src[kItems];
+    int at[kItems], second[kItems];
+    bool turned[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int i = k * (int)blockDim.x + (int)threadIdx.x, tok = i / IT, item = i % IT;
+        turned[k] = rotate && item < p.rotary / 16;
+        const bool half = turned[k] && p.layout == FLEX_ROPE_HALF;
+        const int e = half ? item * 8 : item * 16;
+        second[k] = half ? p.rotary / 2 : 8;
+        src[k] = static_cast<const T *>(is_v ? p.v : p.k) + b * st[0] + h_first * st[1] + (lo + tok - first) * st[2] + e;
+        at[k] = i < total ? (old_n + tok) * D + e : -1;
+    }
+    // a head's values, loaded one head ahead
+    Raw8<T> raw[kItems][2];
+    auto load = [&]() {
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            if (at[k] < 0) continue;
+            raw[k][0].load(src[k]);
+            raw[k][1].load(src[k] + second[k]);
+            src[k] += st[1];
+        }
+    };
+    load();
     if (rotate) {
         for (int i = threadIdx.x; i < p.rotary / 2; i += blockDim.x) turns[i] = turns_per_position(p.inv_freq[i]);
         __syncthreads();
@@ -132,22 +175,6 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int he
     __syncthreads();
     if (id < 0 || id >= p.cache.num_pages) return;           // a bad page: its tokens are dropped
 
-    // this thread's items: where their first vectors lie, in the source (of the
-    // first head) and within the page, and how far behind the second ones are
-    const int64_t *st = is_v ? p.v_stride : p.k_stride;
-    const T *src[kItems];
-    int at[kItems], second[kItems];
-    bool turned[kItems];
-#pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        const int i = k * (int)blockDim.x + (int)threadIdx.x, tok = i / IT, item = i % IT;
-        turned[k] = rotate && item < p.rotary / 16;
-        const bool half = turned[k] && p.layout == FLEX_ROPE_HALF;
-        const int e = half ? item * 8 : item * 16;
-        second[k] = half ? p.rotary / 2 : 8;
-        src[k] = static_cast<const T *>(is_v ? p.v : p.k) + b * st[0] + h_first * st[1] + (lo + tok - first) * st[2] + e;
-        at[k] = i < total ? (old_n + tok) * D + e : -1;
-    }
     float *scale_at = (is_v ? p.cache.v_scale : p.cache.k_scale) + (int64_t)id * p.cache.H;
     uint8_t *dst = (is_v ? p.cache.v : p.cache.k) + ((int64_t)id * p.cache.H + h_first) * page * D * (E4M3 ? 1 : 2);
     for (int h = h_first; h < h_last; ++h, dst += (int64_t)page * D * (E4M3 ? 1 : 2)) {
@@ -155,11 +182,10 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int he
         float x[kItems][2][8];
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            if (at[k] < 0) continue;
-            load8(src[k], x[k][0]);
-            load8(src[k] + second[k], x[k][1]);
-            src[k] += st[1];
+            raw[k][0].unpack(x[k][0]);
+            raw[k][1].unpack(x[k][1]);
         }
+        if (h + 1 < h_last) load();
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
@@ -243,7 +269,7 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int he
                     codes[i] = w;
                 }
             }
-            inv = 1.f / now;
+            inv = __uint_as_float((254u << 23) - __float_as_uint(now));  // 1 / now, a power of two
             if (h + 1 < h_last) __syncthreads();  // the cleared word, before the next head's maxima
         }
 #pragma unroll
@@ -266,10 +292,10 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int he
     }
 }
 
-template <typename T, bool E4M3, int D>
+template <typename T, bool E4M3, int D, int kItems>
 cudaError_t launch_append(const AppendProblem &p, cudaStream_t stream) {
     const int page = p.cache.page;
-    // threads for the tokens that can fall on one page, two items each
+    // threads for the tokens that can fall on one page
     const int most = (p.S < page ? p.S : page) * (D / 16);
     int threads = (most + kItems - 1) / kItems;
     threads = (threads + 31) / 32 * 32;
@@ -278,23 +304,32 @@ cudaError_t launch_append(const AppendProblem &p, cudaStream_t stream) {
     const int64_t slots = pages < p.max_pages ? pages : p.max_pages;
     // heads per CTA: up to 8 share the sines and cosines, as long as that
     // leaves six CTAs for every SM (2 heads instead of 4 at 528 pages of 8 heads
-    // and two tensors: 20.4 us for 18.0; 4 instead of 2 at 204 of 16: 5.8 for 5.2)
+    // and two tensors: 16.2 us for 14.0; 4 instead of 2 at 204 of 16: 5.0 for 4.6)
     int heads = 8;
     while (heads > 1 && slots * p.B * 2 * ((p.cache.H + heads - 1) / heads) < 6 * 152) heads /= 2;
-    const dim3 grid((unsigned)slots, 2u * ((p.cache.H + heads - 1) / heads), p.B);
+    // the CTAs of the keys, which have the sines and cosines to do, come first,
+    // and those of the values fill in behind them (alternating: 16.0 us for 13.9)
+    const int groups = (p.cache.H + heads - 1) / heads;
+    const dim3 grid((unsigned)slots, p.B, 2u * groups);
     const int smem = p.inv_freq ? (p.S < page ? p.S : page) * D * 4 : 0;  // one (cosine, sine) per pair of a head
-    auto kernel = kv_append_kernel<T, E4M3, D>;
+    auto kernel = kv_append_kernel<T, E4M3, D, kItems>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<grid, threads, smem, stream>>>(p, heads);
+    kernel<<<grid, threads, smem, stream>>>(p, heads, groups);
     return cudaGetLastError();
 }
 
 template <typename T, bool E4M3>
 cudaError_t launch_append_d(const AppendProblem &p, cudaStream_t stream) {
-    return p.cache.D == 64 ? launch_append<T, E4M3, 64>(p, stream) : launch_append<T, E4M3, 128>(p, stream);
+    // one item a thread while that makes at most 256 threads: two halve what a
+    // head costs beside its values, which pays where there are warps enough
+    // (pages of 512 items: 14.0 us for 18.0 with one; of 64: 6.9 for 4.6)
+    const int items = (p.S < p.cache.page ? p.S : p.cache.page) * (p.cache.D / 16);
+    if (p.cache.D == 64)
+        return items <= 256 ? launch_append<T, E4M3, 64, 1>(p, stream) : launch_append<T, E4M3, 64, 2>(p, stream);
+    return items <= 256 ? launch_append<T, E4M3, 128, 1>(p, stream) : launch_append<T, E4M3, 128, 2>(p, stream);
 }
 
 }  // namespace

@@ -71,14 +71,30 @@ __device__ __forceinline__ uint64_t turns_per_position(double inv_freq) {
     return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
 }
 // Sine and cosine of a position's angle.  What is left of it beside whole
-// quarter turns goes to float32, at most 1/4 half turn: rounding it moves the
-// angle by 2^-28 of a turn at most (a rounding of all of it: 2^-26).
+// quarter turns goes to float32, x in [-1/4, 1/4] half turns: rounding it moves
+// the angle by 2^-28 of a turn at most (a rounding of all of it: 2^-26).  There
+// the Taylor series of sin(pi x) to x^9 and of cos(pi x) to x^10 leave out less
+// than 2^-28 of the result; pi as a sum of two floats keeps the sine's first
+// term from losing a bit.  Half the instructions of sincospi, of which a prompt
+// appended to a cache needs one per token, pair and run of heads.
 __device__ __forceinline__ void sincos_at(uint64_t turns, int32_t position, float *sine, float *cosine) {
     const uint64_t angle = turns * (uint64_t)(int64_t)position;
     const uint32_t quarters = ((uint32_t)(angle >> 32) + 0x20000000u) >> 30;
     const int64_t rest = (int64_t)(angle - ((uint64_t)quarters << 62));
-    float s, c;
-    sincospif((float)(int32_t)(rest >> 30) * 1.1641532182693481e-10f, &s, &c);  // 2^-33
+    const float x = (float)(int32_t)(rest >> 30) * 1.1641532182693481e-10f;  // 2^-33
+    constexpr double pi = 3.14159265358979323846, p2 = pi * pi;
+    constexpr float pi_hi = (float)pi, pi_lo = (float)(pi - (double)(float)pi);
+    const float t = x * x;
+    float s = fmaf(t, (float)(p2 * p2 * p2 * p2 * pi / 362880), (float)(-p2 * p2 * p2 * pi / 5040));
+    s = fmaf(t, s, (float)(p2 * p2 * pi / 120));
+    s = fmaf(t, s, (float)(-p2 * pi / 6));
+    s = fmaf(t, s, pi_lo);
+    s = fmaf(x, pi_hi, x * s);
+    float c = fmaf(t, (float)(-p2 * p2 * p2 * p2 * p2 / 3628800), (float)(p2 * p2 * p2 * p2 / 40320));
+    c = fmaf(t, c, (float)(-p2 * p2 * p2 / 720));
+    c = fmaf(t, c, (float)(p2 * p2 / 24));
+    c = fmaf(t, c, (float)(-p2 / 2));
+    c = fmaf(t, c, 1.f);
     const float a = quarters & 1u ? c : s, z = quarters & 1u ? s : c;
     *sine = quarters & 2u ? -a : a;
     *cosine = (quarters + 1u) & 2u ? -z : z;

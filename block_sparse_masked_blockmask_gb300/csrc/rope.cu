@@ -9,7 +9,7 @@
 // registers for one item (two 16-byte vectors: the two halves of eight pairs,
 // or four in fp32) of one token and walks the heads of both tensors with them.
 // Rotating a bf16 head costs two loads, two stores and ~60 other instructions
-// per thread; one sincospi costs ~40, which four heads or more per thread hide.
+// per thread; a sine and cosine cost ~40, which four heads or more per thread hide.
 // q and k of B2 H32 S16384 D128 in bf16 take 163 us, 6.6 TB/s: 97% of the rate
 // of a copy.  A step of 16 sequences (40 heads each) takes 3.1 us, of which the
 // launch is most.
