@@ -585,23 +585,23 @@ def _rope_params(inv_freq: torch.Tensor, layout: int, attention_scale: float, de
 
 def _rope(name: str, q, k, inv_freq, positions, layout, attention_scale, q_out, k_out, stream):
     device = q.device
-    if q_out is None:
-        q_out = _empty(q.shape, q.dtype, device, stream)
-    elif q_out.device != device:
-        raise ValueError("q, k and their outputs must be on one device")
-    tk = ok = None
+    tq, tk, ok = _tensor(q), None, None
     if k is not None:
-        if k_out is None:
-            k_out = _empty(k.shape, k.dtype, device, stream)
-        if k.device != device or k_out.device != device:
-            raise ValueError("q, k and their outputs must be on one device")
-        tk, ok = _tensor(k), _tensor(k_out)
+        tk = _tensor(k)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    tq = _tensor(q)
+    for x in (k, q_out, k_out):
+        if x is not None and x.device != device:
+            raise ValueError("q, k and their outputs must be on one device")
     params = _rope_params(inv_freq, layout, attention_scale, device)
     if positions is not None:
         positions = _device_array(positions, "positions", torch.int32, device, (q.shape[0], q.shape[2]))
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, device, stream)
+    if k is not None:
+        if k_out is None:
+            k_out = _empty(k.shape, k.dtype, device, stream)
+        ok = _tensor(k_out)
     rc = _call(device, getattr(load_library(), name), tq, tk, params, positions, _tensor(q_out), ok,
                _stream_handle(stream, device))
     if rc != FLEX_OK:
