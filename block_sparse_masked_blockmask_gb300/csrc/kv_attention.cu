@@ -43,8 +43,11 @@
 //    exp, one 8 x 8 transpose (movmatrix) per 8 keys makes them the B operand
 //    P^T.  Statistics, sums and accumulators are float32, and the sum takes the
 //    unrounded weights.
-//  * The maximum is only raised when a score exceeds it by 2^8 (votes instead of
-//    reductions on most steps); weights then stay below 2^8.
+//  * Weights are relative to 2^-7 of the largest when that was last raised, and it
+//    is only raised when a score exceeds it by 2^8 (votes instead of reductions on
+//    most steps): they stay below 2^15, and fp16's smallest step is 2^-31 of the
+//    largest or less.  Small weights and pages with a small V scale beside
+//    one with a large scale need the room below.
 //  * The steps of all sequences, heads and row tiles form one list, which the
 //    warps of one wave of CTAs share out evenly, so that ragged batches and a
 //    few long sequences fill the SMs alike (an earlier form with a cluster of
@@ -86,7 +89,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // heads: 12.5 us, and 14.6 with two, 18.1 with four).
 constexpr int kEnterCost = 3;
 constexpr int kMinShare = 1;
-constexpr float kRaise = 8.f;  // raise the running max only beyond 2^8
+constexpr float kTop = 7.f;     // raising the reference leaves the largest weight at 2^7
+constexpr float kRaise = 15.f;  // and is due when one would pass 2^15
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
@@ -715,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float w = top[nt][u];
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
-                    const float now = w > m[nt][u] + kRaise ? w : m[nt][u];
+                    const float now = w > m[nt][u] + kRaise ? w - kTop : m[nt][u];
                     alpha[u] = exp2f(m[nt][u] - now);
                     m[nt][u] = now;
                     l[nt][u] *= alpha[u];

@@ -364,6 +364,37 @@ def test_attention_large_and_small_queries():
     compare(q, cache, table, lens, 16)
 
 
+def test_attention_beside_a_page_of_large_values():
+    """A page whose values (and V scale) are 2^10 times the others', which no query looks at: its share of the
+    result is small, and the others keep their bits.  A weight is off by fp16's 2^-11, or by half its smallest step:
+    2^-25 in units where the row's largest is 2^7 at least, times the largest V scale and 448."""
+    gen = torch.Generator().manual_seed(37)
+    lens, page, D, G = [200], 16, 64, 4
+    cache, table = filled(gen, lens, 1, page, D, E4M3)
+    for i in range(13):
+        pid, used = int(table[0, i]), min(page, lens[0] - i * page)
+        big = i == 5
+        cache.k_scale[pid], cache.v_scale[pid] = 2.0**-6, 2.0**2 if big else 2.0**-8
+        k, v = (torch.randn((used, D), generator=gen).cuda() for _ in range(2))
+        k[:, 0] = -6.0 if big else 1.0
+        for x, y in ((cache.k, k * 64), (cache.v, v * 100)):
+            x[pid, 0, :used] = y.clamp(-448, 448).to(E4M3)
+    q = torch.randn((1, G, 1, D), generator=gen)
+    q[..., 0] = 40.0
+    q = q.bfloat16().cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, _ = fa.flex_kv_cache_attention(q, cache, table, n)
+    ids = table[0].long()[torch.arange(200, device="cuda") // page]
+    k, v = (values(cache, w)[ids, 0, torch.arange(200, device="cuda") % page] for w in "kv")
+    s = (q[0, :, 0].double() @ k.T) * D**-0.5
+    e_s = 2.0**-24 * (D + 8) * (q[0, :, 0].double().abs() @ k.abs().T).amax(-1, keepdim=True) * D**-0.5
+    p = torch.softmax(s, -1)
+    total = (s - s.amax(-1, keepdim=True)).exp().sum(-1, keepdim=True)
+    want = p @ v
+    bound = (2.0**-11 + 2 * e_s + 2.0**-18) * (p @ v.abs()) + 2.0**-32 * 200 * 448 * 4.0 / total + 2.0**-8 * want.abs()
+    assert ((out[0, :, 0].double() - want).abs() <= bound).all()
+
+
 def test_decoding_loop_in_a_graph():
     """Prompt, then steps of rotation + append + attention replayed from one CUDA graph on another stream,
     against attention over the whole sequence with the cache's own rounded values."""
