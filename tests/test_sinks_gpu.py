@@ -239,3 +239,27 @@ def test_training_step_with_rotary_positions():
     slope = sum(float((want[n] * d).sum()) for n, d in zip(("dq", "dk", "dv"), step))
     size = sum(float((want[n] * d).abs().sum()) for n, d in zip(("dq", "dk", "dv"), step))
     assert abs((up - down) / (2 * eps) - slope) <= 1e-6 * size
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_query_side_in_fp32(D):
+    """dk and dv of more than 2048 query tiles, which the CUDA cores compute.  Beside the bounds of the short ones a
+    column's float32 sum of n terms of no common sign is off by 2^-24 of its partial sums, 8 sqrt(n) of its terms'
+    mean size: 2^-21 sqrt(n) of the sum of their sizes, n times over at most, in the mean over n."""
+    q_len, kv_len, window, sinks = 2048 * 128 + 130, 200, 70, 3
+    gen = torch.Generator().manual_seed(D)
+    q, k, v, g = (torch.randn((1, 1, n, D), generator=gen).cuda() for n in (q_len, kv_len, kv_len, q_len))
+    keep = dense_mask(q_len, kv_len, window, sinks).cuda()
+    bm = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, 1, 1, q_len, kv_len, window=window, sinks=sinks)
+    out, lse = fa.flex_attention_fwd(q, k, v, bm)
+    got = dict(zip(("dq", "dk", "dv"), fa.flex_attention_bwd(q, k, v, out, lse, g, bm, fa.flex_block_mask_transpose(bm))))
+    got["out"] = out
+    ref, absolute, product, e_s = reference(q, k, v, g, keep, fa.FLEX_SCORE_IDENTITY, 0.0, 1.0 / math.sqrt(D))
+    e_p = 2 * float(e_s.max()) + 2.0**-18
+    terms = keep.sum(0).double().sqrt()[:, None]
+    for name, x in got.items():
+        diff = (x.double() - ref[name]).abs()
+        bound = 2.0**-18 * (ref[name].abs() + 2 * absolute[name]) + (e_p + 2.0**-18) * product[name]
+        if name in ("dk", "dv"):
+            bound += 2.0**-21 * terms * absolute[name]
+        assert (diff <= bound + 1e-30).all(), (name, float((diff - bound).max()))
