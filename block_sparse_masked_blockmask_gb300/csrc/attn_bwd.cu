@@ -590,20 +590,36 @@ cudaError_t launch_bwd_bf16_tc(const AttnProblem &p, const BwdArgs &a, cudaStrea
     kp.delta = a.delta;
     kp.status = p.status;
     // dK, dV: own the kv tiles, walk the q side of the BlockMask
+    kp.own_begin = 0;
     kp.nblocks = p.nkvt;
     kp.lists = TileLists{a.q_num, a.q_idx, a.fq_num, a.fq_idx, p.nkvb, p.nqb, p.kv_block, p.q_block, p.nqt};
     kp.out0 = static_cast<uint16_t *>(a.dv);
     kp.out1 = static_cast<uint16_t *>(a.dk);
     const CUtensorMap kv_maps[4] = {mk, mv, mq, mdo};
     // dQ: own the q tiles, walk the kv side
-    BwdTcParams qp = kp;
+    BwdTcParams qp = kp;  // own_begin 0: all of them
     qp.nblocks = p.nqt;
     qp.lists = TileLists{p.kv_num, p.kv_idx, p.full_num, p.full_idx, p.nqb, p.nkvb, p.q_block, p.kv_block, p.nkvt};
     qp.out0 = static_cast<uint16_t *>(a.dq);
     qp.out1 = nullptr;
     const CUtensorMap q_maps[4] = {mq, mdo, mk, mv};
+    // tiles with sinks that would keep one CTA walking: first and apart, with dq
+    // (not written yet) as the place of their parts' sums
+    BwdTcParams parts = kp;
+    const int apart = bwd_tc_parts(kp, p.nqt, parts.chunks, parts.chunk_tiles);
+    if (apart > 0) {
+        parts.nblocks = apart;
+        parts.part = static_cast<float *>(a.dq);
+        parts.part_stride = (int64_t)p.q_len * p.D / 2;
+        if ((e = launch_bwd_tc_dkdv_parts(kv_maps, parts, p.D, p.score_kind, stream)) != cudaSuccess) return e;
+        kp.own_begin = apart;
+        kp.nblocks -= apart;
+    }
     return launch_dkdv_dq(
-        stream, [&](cudaStream_t s) { return launch_bwd_tc_dkdv(kv_maps, kp, p.D, p.score_kind, s); },
+        stream,
+        [&](cudaStream_t s) {
+            return kp.nblocks == 0 ? cudaSuccess : launch_bwd_tc_dkdv(kv_maps, kp, p.D, p.score_kind, s);
+        },
         [&](cudaStream_t s) { return launch_bwd_tc_dq(q_maps, qp, p.D, p.score_kind, s); });
 }
 

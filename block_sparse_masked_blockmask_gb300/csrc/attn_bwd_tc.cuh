@@ -61,7 +61,7 @@ constexpr float kBwdLog2e = 1.4426950408889634f;
 
 struct BwdTcParams {
     int B, H, q_len, kv_len;
-    int nblocks;                  // 128-tiles of the owned dimension (kv when KV_MAJOR, else q)
+    int own_begin, nblocks;       // first and number of the owned 128-tiles (kv when KV_MAJOR, else q)
     int bh_begin, nbh;
     TileLists lists;              // the BlockMask side that lists the walked dimension, read as 128-tiles
     MaskDesc mask;
@@ -69,6 +69,9 @@ struct BwdTcParams {
     const float *lse, *delta;     // [B, H, q_len]
     uint16_t *out0, *out1;        // KV_MAJOR: dv, dk; else dq (out1 unused); bf16, contiguous
     int *status;
+    int chunks, chunk_tiles;      // parts of kv tiles (below): per tile, and walked tiles of one
+    float *part;                  // their sums: per (b, h) part_stride floats, [tile][chunk][dv, dk][128][D]
+    int64_t part_stride;
 };
 
 // One work item (a 128-row block of one (batch, head)) as the scheduler
@@ -77,7 +80,7 @@ struct BwdSlot {
     int n;      // list steps; -1: no more work for this CTA
     int own;    // owned block
     int bh;     // b * H + h
-    int pad;
+    int chunk;  // of a kv tile computed in parts
     alignas(16) uint32_t list[kBwdMaxList];  // walked tile | full << 16, ascending
 };
 
@@ -241,18 +244,25 @@ __device__ __forceinline__ void bwd_decode_item(const BwdTcParams &p, bool kv_ma
     const int g0 = (item / group_items) * kBwdHeadGroup;
     const int gsize = min(kBwdHeadGroup, p.nbh - g0);
     const int r = item - (item / group_items) * group_items;
-    own = kv_major ? r / gsize : p.nblocks - 1 - r / gsize;
+    own = kv_major ? p.own_begin + r / gsize : p.nblocks - 1 - r / gsize;
     bh = p.bh_begin + g0 + r % gsize;
 }
 
 // The walked tiles of an item's block, with the 32 lanes of one warp: the
 // BlockMask's lists (any block sizes) read as 128-tiles, in ascending order;
 // counts are clamped and malformed entries dropped, so nothing is written or
-// loaded out of bounds.
+// loaded out of bounds.  PARTS: an item is one chunk of a tile's walked tiles.
+template <bool PARTS>
 __device__ __forceinline__ void bwd_build_list(const BwdTcParams &p, bool kv_major, BwdMisc &ms, BwdSlot &sl, int item,
                                                int lane) {
-    int own, bh;
-    bwd_decode_item(p, kv_major, item, own, bh);
+    int own, bh, chunk = 0;
+    if constexpr (PARTS) {
+        chunk = item % p.chunks;
+        own = item / p.chunks % p.nblocks;
+        bh = p.bh_begin + item / p.chunks / p.nblocks;
+    } else {
+        bwd_decode_item(p, kv_major, item, own, bh);
+    }
     const int nt = min(p.lists.walk_nt, kBwdMaxList);
     for (int i = lane; i < nt; i += 32) ms.words[i] = 0u;
     __syncwarp();
@@ -264,7 +274,7 @@ __device__ __forceinline__ void bwd_build_list(const BwdTcParams &p, bool kv_maj
     for (int base = 0; base < nt; base += 32) {
         const int i = base + lane;
         const uint32_t w = i < nt ? ms.words[i] : 0u;
-        const bool ok = tl_listed(w, 0);
+        const bool ok = tl_listed(w, 0) && (!PARTS || i / p.chunk_tiles == chunk);
         const unsigned bal = __ballot_sync(0xffffffffu, ok);
         if (ok) sl.list[cnt + __popc(bal & lt)] = (uint32_t)i | (tl_full(expect, w, 0) ? (1u << 16) : 0u);
         cnt += __popc(bal);
@@ -273,6 +283,7 @@ __device__ __forceinline__ void bwd_build_list(const BwdTcParams &p, bool kv_maj
         sl.n = cnt;
         sl.own = own;
         sl.bh = bh;
+        sl.chunk = chunk;
     }
 }
 
@@ -290,7 +301,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     using C = BwdTcCfg<D, KV_MAJOR>;
     constexpr int NA = C::kNA, NB = C::kNB;
     constexpr bool DOC = MASKC == kMaskDocument, SINKS = MASKC == kMaskSinks;
-    static_assert(!(SINKS && KV_MAJOR), "a column of a window + sinks mask is one interval");
+    // A column of a window + sinks mask is one interval, so that its dK and dV
+    // run as interval masks; this combination computes the tiles that hold sinks,
+    // whose columns every later row keeps, in parts.
+    constexpr bool PARTS = SINKS && KV_MAJOR;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     BwdMisc &ms = *reinterpret_cast<BwdMisc *>(smem + C::kMiscOff);
@@ -361,7 +375,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 break;
             }
             if (item >= 0) {
-                bwd_build_list(p, KV_MAJOR, ms, sl, item, lane);
+                bwd_build_list<PARTS>(p, KV_MAJOR, ms, sl, item, lane);
             } else if (lane == 0) {
                 sl.n = -1;
             }
@@ -828,6 +842,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                   const float mul = (KV_MAJOR && which == 0) ? 1.f : p.scale;
                   uint16_t *dst = (which == 0 ? p.out0 : p.out1) + orow * D + half * (D / 2);
                   const uint32_t col = (which == 0 ? C::kAcc0 : C::kAcc1) + half * (D / 2);
+                  float *sums = nullptr;
+                  if constexpr (PARTS)
+                      sums = p.part + bh * p.part_stride +
+                             ((((int64_t)own * p.chunks + sl.chunk) * 2 + which) * 128 + t) * D + half * (D / 2);
   #pragma unroll 1
                   for (int c0 = 0; c0 < D / 2; c0 += 32) {
                       uint32_t o[32];
@@ -836,6 +854,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                       } else {
   #pragma unroll
                           for (int j = 0; j < 32; ++j) o[j] = 0u;
+                      }
+                      if constexpr (PARTS) {
+  #pragma unroll
+                          for (int j = 0; j < 32; j += 4)
+                              *reinterpret_cast<float4 *>(sums + c0 + j) =
+                                  make_float4(__uint_as_float(o[j]) * mul, __uint_as_float(o[j + 1]) * mul,
+                                              __uint_as_float(o[j + 2]) * mul, __uint_as_float(o[j + 3]) * mul);
+                          continue;
                       }
                       uint32_t pk[16];
   #pragma unroll

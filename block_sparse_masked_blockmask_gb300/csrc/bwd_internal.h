@@ -19,6 +19,10 @@ cudaError_t launch_bwd_tc_dq(const CUtensorMap (&maps)[4], const BwdTcParams &kp
                              cudaStream_t stream);
 cudaError_t launch_bwd_tc_dq_sinks(const CUtensorMap (&maps)[4], const BwdTcParams &kp, int D, int score_kind,
                                    cudaStream_t stream);
+// dK and dV of kv tiles that hold sinks, in parts (attn_bwd_tc_kv_sinks.cu)
+int bwd_tc_parts(const BwdTcParams &kp, int nqt, int &chunks, int &chunk_tiles);
+cudaError_t launch_bwd_tc_dkdv_parts(const CUtensorMap (&maps)[4], const BwdTcParams &kp, int D, int score_kind,
+                                     cudaStream_t stream);
 // q blocks per kv block the tensor-core backward walks on chip (NQB limit for bf16)
 constexpr int kBwdTcMaxQBlocks = 2048;
 

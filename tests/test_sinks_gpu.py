@@ -263,3 +263,57 @@ def test_long_query_side_in_fp32(D):
         if name in ("dk", "dv"):
             bound += 2.0**-21 * terms * absolute[name]
         assert (diff <= bound + 1e-30).all(), (name, float((diff - bound).max()))
+
+
+def check_gradients(q, k, v, g, keep, got, score, r):
+    ref, absolute, product, e_s = reference(q, k, v, g, keep, score, 0.0, 1.0 / math.sqrt(q.shape[3]))
+    e_p = 2 * float(e_s.max()) + 2.0**-18
+    for name, x in got.items():
+        diff = (x.double() - ref[name]).abs()
+        bound = r * ref[name].abs() + 2 * r * absolute[name] + (e_p + 2.0**-18) * product[name]
+        assert (diff <= bound + 1e-30).all(), (name, float((diff - bound).max()))
+
+
+@pytest.mark.parametrize("H,q_len,kv_len,D,window,sinks", [(1, 4100, 4100, 64, 256, 4), (2, 5000, 5000, 128, 100, 130),
+                                                           (1, 3000, 200, 128, 70, 200), (3, 2048, 2048, 64, 0, 1)])
+def test_few_heads_and_many_query_tiles(H, q_len, kv_len, D, window, sinks):
+    """dk and dv of the tiles with sinks are summed over parts of the query axis."""
+    gen = torch.Generator().manual_seed(q_len + D)
+    q, k, v, g = (torch.randn((1, H, n, D), generator=gen).bfloat16().cuda() for n in (q_len, kv_len, kv_len, q_len))
+    keep = dense_mask(q_len, kv_len, window, sinks).cuda()
+    bm = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, 1, H, q_len, kv_len, window=window, sinks=sinks)
+    bq = fa.flex_block_mask_transpose(bm)
+    for score in (fa.FLEX_SCORE_IDENTITY, fa.FLEX_SCORE_ALIBI):
+        out, lse = fa.flex_attention_fwd(q, k, v, bm, score)
+        got = dict(zip(("dq", "dk", "dv"), fa.flex_attention_bwd(q, k, v, out, lse, g, bm, bq, score)))
+        assert fa.flex_device_status() == fa.FLEX_OK
+        check_gradients(q, k, v, g, keep, got, score, 2.0**-8)
+
+
+@pytest.mark.parametrize("score", [fa.FLEX_SCORE_IDENTITY, fa.FLEX_SCORE_SOFTCAP])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_head_as_many(D, score):
+    """One head, whose tile of sinks is summed over parts, and the same head thirty-two times, where one CTA walks it:
+    equal products, another order of float32 sums and one rounding each; and equal bits in a captured call."""
+    S, gen = 4100, torch.Generator().manual_seed(D + score)
+    q, k, v, g = (torch.randn((1, 1, S, D), generator=gen).bfloat16().cuda() for _ in range(4))
+
+    def run(H):
+        x = [t.expand(1, H, S, D).contiguous() for t in (q, k, v, g)]
+        bm = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, 1, H, S, S, window=256, sinks=7)
+        bq = fa.flex_block_mask_transpose(bm)
+        out, lse = fa.flex_attention_fwd(*x[:3], bm, score, 9.0)
+        f = lambda: fa.flex_attention_bwd(*x[:3], out, lse, x[3], bm, bq, score, 9.0)  # noqa: E731
+        return f(), f
+
+    (one, again), (many, _) = run(1), run(32)
+    for x, y in zip(one, many):
+        x, y = x[0, 0].float(), y[0, 5].float()
+        assert ((x - y).abs() <= 2.0**-7 * y.abs() + 2.0**-12 * y.abs().max()).all()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        replayed = again()
+    graph.replay()
+    graph.replay()
+    assert all(torch.equal(x, y) for x, y in zip(one, replayed))
