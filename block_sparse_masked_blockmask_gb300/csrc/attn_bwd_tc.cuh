@@ -861,16 +861,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                               *reinterpret_cast<float4 *>(sums + c0 + j) =
                                   make_float4(__uint_as_float(o[j]) * mul, __uint_as_float(o[j + 1]) * mul,
                                               __uint_as_float(o[j + 2]) * mul, __uint_as_float(o[j + 3]) * mul);
-                          continue;
-                      }
-                      uint32_t pk[16];
+                      } else {
+                          uint32_t pk[16];
   #pragma unroll
-                      for (int j = 0; j < 16; ++j)
-                          pk[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * mul, __uint_as_float(o[2 * j + 1]) * mul);
-                      // whole 32-byte sectors per store
-                      if (store) {
-                          st_global_32B(dst + c0, &pk[0]);
-                          st_global_32B(dst + c0 + 16, &pk[8]);
+                          for (int j = 0; j < 16; ++j)
+                              pk[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * mul, __uint_as_float(o[2 * j + 1]) * mul);
+                          // whole 32-byte sectors per store
+                          if (store) {
+                              st_global_32B(dst + c0, &pk[0]);
+                              st_global_32B(dst + c0 + 16, &pk[8]);
+                          }
                       }
                   }
               }

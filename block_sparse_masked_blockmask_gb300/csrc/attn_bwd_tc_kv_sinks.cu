@@ -1,7 +1,8 @@
 // Tensor-core backward, dK and dV of the tiles that hold a window + sinks
 // mask's sinks.  Every later row keeps those columns, so that one CTA would walk
 // all query tiles one after another while the other tiles' CTAs walk a window's
-// (S 32768, window 1024, one head of D 128: 436 us, of which 77 for the window).
+// (S 32768, window 1024, one head of D 128: 436 us for a backward that takes 108
+// with the parts, and 76 without sinks).
 // The query tiles are cut into chunks, one CTA each; the chunks' float32
 // sums go to the memory of dq, which is written afterwards, and a second launch
 // adds them in a fixed order and rounds once.
@@ -65,15 +66,18 @@ cudaError_t launch_parts_score(const CUtensorMap (&maps)[4], const BwdTcParams &
 
 // The number of kv tiles, from the first, that launch_bwd_tc_dkdv_parts is to
 // compute (0: none), and how it cuts them.  It pays where the walk of all query
-// tiles is much longer than an SM's share of all steps: a step takes 1 to 1.7
-// us, the two launches about 10.
+// tiles is longer than an SM's share of all steps, those of dQ (as many) among
+// them, by what the two launches take: about 10 us, a step 1 to 1.7.  Measured
+// with parts and without: 32 query tiles, share 5 (window 512, four heads of D
+// 128): 54 and 63 us; 64, share 36 (window 1024, eight heads): 163 and 149 us;
+// 16, share 8 (window 256, sixteen heads of D 64): 49 and 41 us.
 int bwd_tc_parts(const BwdTcParams &kp, int nqt, int &chunks, int &chunk_tiles) {
     constexpr int kSms = 152, kWorth = 12;
     if (mask_class(kp.mask.kind) != kMaskSinks || kp.mask.prefix <= 0) return 0;
     const int64_t tiles = ceil_blocks(std::min(kp.mask.prefix, kp.kv_len)), nbh = kp.nbh;
     const int64_t window_tiles = std::min<int64_t>(nqt, (int64_t)kp.mask.window / kBlock + 2);
     const int64_t share = nbh * ((kp.nblocks - tiles) * window_tiles + tiles * nqt) / kSms;
-    if (nqt - std::max(share, window_tiles) < kWorth) return 0;
+    if (nqt - std::max(2 * share, window_tiles) < kWorth) return 0;
     // two CTAs of parts for every SM, as far as dq's memory (2 bytes a value)
     // holds their sums (2 x 128 x D x 4 bytes each)
     int64_t n = std::min((2 * kSms + nbh * tiles - 1) / (nbh * tiles), (int64_t)kp.q_len / (4 * kBlock * tiles));
