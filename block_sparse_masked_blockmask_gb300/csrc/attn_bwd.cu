@@ -42,7 +42,7 @@
 namespace flex {
 
 // compiled in attn_bwd_fp32_sinks.cu
-extern template cudaError_t launch_bwd_fp32_tc_dkdv<true>(const AttnProblem &, const BwdF32TcArgs &, cudaStream_t);
+extern template cudaError_t launch_bwd_fp32_tc_dkdv<true>(const AttnProblem &, const BwdF32TcArgs &, int, cudaStream_t);
 extern template cudaError_t launch_bwd_fp32_tc_dq<true>(const AttnProblem &, const BwdF32TcArgs &, cudaStream_t);
 
 namespace {
@@ -524,11 +524,28 @@ cudaError_t launch_bwd_fp32(const AttnProblem &p, const BwdArgs &a, cudaStream_t
     attn_bwd_delta_kernel<D, float><<<(unsigned)((rows * 32 + 255) / 256), 256, 0, stream>>>(p, a, rows);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const BwdF32TcArgs ta{static_cast<const float *>(a.dout), a.delta, a.q_num, a.q_idx, a.fq_num, a.fq_idx,
+    BwdF32TcArgs ta{static_cast<const float *>(a.dout), a.delta, a.q_num, a.q_idx, a.fq_num, a.fq_idx,
                           static_cast<float *>(a.dk), static_cast<float *>(a.dv), static_cast<float *>(a.dq)};
     auto dq = [&](cudaStream_t s) { return launch_bwd_fp32_tc_dq<SINKS>(p, ta, s); };
-    if (p.nqt <= kBwdF32TcMaxQTiles)
-        return launch_dkdv_dq(stream, [&](cudaStream_t s) { return launch_bwd_fp32_tc_dkdv<SINKS>(p, ta, s); }, dq);
+    if (p.nqt <= kBwdF32TcMaxQTiles) {
+        int apart = 0;
+        if constexpr (SINKS) {
+            // tiles with sinks in parts, as in launch_bwd_bf16_tc (a step is 8 to 15 us)
+            BwdF32TcArgs parts = ta;
+            apart = bwd_parts(p, 4, 3, parts.chunks, parts.chunk_tiles);
+            if (apart > 0) {
+                parts.part = ta.dq;
+                parts.part_stride = (int64_t)p.q_len * D;
+                if ((e = launch_bwd_fp32_tc_dkdv<SINKS>(p, parts, apart, stream)) != cudaSuccess ||
+                    (e = launch_bwd_sum_parts(p, parts.part, parts.part_stride, apart, parts.chunks, ta.dv, ta.dk, false,
+                                              stream)) != cudaSuccess)
+                    return e;
+                ta.own_begin = apart;
+            }
+        }
+        return launch_dkdv_dq(
+            stream, [&](cudaStream_t s) { return launch_bwd_fp32_tc_dkdv<SINKS>(p, ta, p.nkvt - apart, s); }, dq);
+    }
     // dK/dV of a longer q side on the CUDA cores
     return launch_dkdv_dq(
         stream,
@@ -606,12 +623,15 @@ cudaError_t launch_bwd_bf16_tc(const AttnProblem &p, const BwdArgs &a, cudaStrea
     // tiles with sinks that would keep one CTA walking: first and apart, with dq
     // (not written yet) as the place of their parts' sums
     BwdTcParams parts = kp;
-    const int apart = bwd_tc_parts(kp, p.nqt, parts.chunks, parts.chunk_tiles);
+    const int apart = bwd_parts(p, 2, 12, parts.chunks, parts.chunk_tiles);
     if (apart > 0) {
         parts.nblocks = apart;
         parts.part = static_cast<float *>(a.dq);
         parts.part_stride = (int64_t)p.q_len * p.D / 2;
-        if ((e = launch_bwd_tc_dkdv_parts(kv_maps, parts, p.D, p.score_kind, stream)) != cudaSuccess) return e;
+        if ((e = launch_bwd_tc_dkdv_parts(kv_maps, parts, p.D, p.score_kind, stream)) != cudaSuccess ||
+            (e = launch_bwd_sum_parts(p, parts.part, parts.part_stride, apart, parts.chunks, a.dv, a.dk, true, stream)) !=
+                cudaSuccess)
+            return e;
         kp.own_begin = apart;
         kp.nblocks -= apart;
     }

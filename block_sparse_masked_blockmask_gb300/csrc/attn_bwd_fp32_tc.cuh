@@ -56,6 +56,12 @@ struct BwdF32TcArgs {
     const int32_t *q_num, *q_idx, *fq_num, *fq_idx;  // q side of the BlockMask
     float *dk, *dv;                                  // contiguous [B, H, kv_len, 64]
     float *dq;                                       // contiguous [B, H, q_len, 64]
+    // SINKS kernels: the first kv tile, and kv tiles in parts (chunks > 0), as in
+    // the bf16 backward: chunks of chunk_tiles q tiles along grid.z, whose sums
+    // go to part, per (b, h) part_stride floats, [tile][chunk][dv, dk][128][D]
+    int own_begin = 0, chunks = 0, chunk_tiles = 0;
+    float *part = nullptr;
+    int64_t part_stride = 0;
 };
 
 namespace bwdf32 {
@@ -175,6 +181,11 @@ __device__ __forceinline__ float score_t(float cap, float t, float slope, int q,
     return t;
 }
 
+// Where a part of a kv tile keeps its sums of row `row` (which: 0 dv, 1 dk).
+__device__ __forceinline__ float *part_row(const BwdF32TcArgs &a, int kvb, int bh, int which, int row, int D) {
+    return a.part + bh * a.part_stride + ((((int64_t)kvb * a.chunks + blockIdx.z) * 2 + which) * kBlock + row) * D;
+}
+
 template <int SCORE, bool SINKS>
 __global__ void __launch_bounds__(16 * 32, 1) dkdv_kernel(AttnProblem p, BwdF32TcArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -184,7 +195,7 @@ __global__ void __launch_bounds__(16 * 32, 1) dkdv_kernel(AttnProblem p, BwdF32T
     // (b, h) pairs along x, kv blocks along y (at most 1024): the first CTAs
     // to run are the kv blocks that come first in every pair (the longest q
     // sides of a causal mask)
-    const int kvb = blockIdx.y;
+    const int kvb = (int)blockIdx.y + (SINKS ? a.own_begin : 0);
     const int bh = p.bh_begin + (int)blockIdx.x, h = bh % p.H, b = bh / p.H;
     const int kv0 = kvb * kBlock;
 
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(16 * 32, 1) dkdv_kernel(AttnProblem p, BwdF32T
         for (int base = 0; base < p.nqt; base += 32) {
             const int i = base + lane;
             const uint32_t w = i < p.nqt ? ms.flags[i] : 0u;
-            const bool on = tl_listed(w, 0);
+            const bool on = tl_listed(w, 0) && (!SINKS || a.chunks == 0 || i / a.chunk_tiles == (int)blockIdx.z);
             const unsigned bal = __ballot_sync(0xffffffffu, on);
             if (on) ms.list[cnt + __popc(bal & lt)] = (uint32_t)i | (tl_full(expect, w, 0) ? (1u << 16) : 0u);
             cnt += __popc(bal);
@@ -424,6 +435,7 @@ __global__ void __launch_bounds__(16 * 32, 1) dkdv_kernel(AttnProblem p, BwdF32T
 #pragma unroll 1
             for (int o = 0; o < 2; ++o) {  // dV, then dK
                 float *dst = (o ? a.dk : a.dv) + orow * D;
+                if (SINKS && a.chunks > 0) dst = part_row(a, kvb, bh, o, kv - kv0, D);
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {  // every lane takes the warp-collective loads
                     uint32_t r[32];
@@ -1378,6 +1390,7 @@ __device__ __forceinline__ void dkdv128_role(const AttnProblem &p, const BwdF32T
             tc_fence_after_sync();
             const int64_t orow = (int64_t)bh * p.kv_len + (kv < p.kv_len ? kv : 0);
             float *dst = (ROLE == 0 ? a.dk : a.dv) + orow * c::D;
+            if (SINKS && a.chunks > 0) dst = part_row(a, kvb, bh, ROLE == 0 ? 1 : 0, kv - kvb * kBlock, c::D);
 #pragma unroll 1
             for (int c0 = 0; c0 < c::D; c0 += 32) {  // every lane takes the warp-collective loads
                 uint32_t r[32];
@@ -1405,7 +1418,8 @@ __global__ void __launch_bounds__(16 * 32, 1) dkdv128_kernel(AttnProblem p, BwdF
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc &ms = *reinterpret_cast<Misc *>(smem + d128kv::kMiscOff);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int kvb = (int)blockIdx.y / 2, role = (int)blockIdx.y & 1;  // role 0: dK, role 1: dV
+    const int kvb = (int)blockIdx.y / 2 + (SINKS ? a.own_begin : 0);
+    const int role = (int)blockIdx.y & 1;  // role 0: dK, role 1: dV
     const int bh = p.bh_begin + (int)blockIdx.x;
 
     if (threadIdx.x == 0) {
@@ -1436,7 +1450,7 @@ __global__ void __launch_bounds__(16 * 32, 1) dkdv128_kernel(AttnProblem p, BwdF
         for (int base = 0; base < p.nqt; base += 32) {
             const int i = base + lane;
             const uint32_t w = i < p.nqt ? ms.flags[i] : 0u;
-            const bool on = tl_listed(w, 0);
+            const bool on = tl_listed(w, 0) && (!SINKS || a.chunks == 0 || i / a.chunk_tiles == (int)blockIdx.z);
             const unsigned bal = __ballot_sync(0xffffffffu, on);
             if (on) ms.list[cnt + __popc(bal & lt)] = (uint32_t)i | (tl_full(expect, w, 0) ? (1u << 16) : 0u);
             cnt += __popc(bal);
@@ -1468,14 +1482,15 @@ __global__ void __launch_bounds__(16 * 32, 1) dkdv128_kernel(AttnProblem p, BwdF
 }  // namespace bwdf32
 
 // dK and dV of fp32 inputs on the tensor cores (p.D == 64 or 128; p.nqt <=
-// kBwdF32TcMaxQTiles).
+// kBwdF32TcMaxQTiles), of `tiles` kv tiles from a.own_begin on.
 template <bool SINKS>
-cudaError_t launch_bwd_fp32_tc_dkdv(const AttnProblem &p, const BwdF32TcArgs &a, cudaStream_t stream) {
+cudaError_t launch_bwd_fp32_tc_dkdv(const AttnProblem &p, const BwdF32TcArgs &a, int tiles, cudaStream_t stream) {
+    if (tiles == 0) return cudaSuccess;
     using namespace bwdf32;
     const bool d64 = p.D == 64;
     const size_t smem = d64 ? kSmemBytes : d128kv::kSmemBytes;
     // D = 128: two CTAs per kv block, one for dK and one for dV
-    const unsigned gy = (unsigned)p.nkvt * (d64 ? 1u : 2u);
+    const unsigned gy = (unsigned)tiles * (d64 ? 1u : 2u), gz = SINKS && a.chunks > 0 ? (unsigned)a.chunks : 1u;
     static_assert(2 * kMaxKvBlocks <= 65535, "kv blocks along grid.y");
     auto pick = [&](auto kern) -> cudaError_t {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -1484,7 +1499,7 @@ cudaError_t launch_bwd_fp32_tc_dkdv(const AttnProblem &p, const BwdF32TcArgs &a,
             AttnProblem part = p;
             part.bh_begin = begin;
             const int count = p.B * p.H - begin < 65535 ? p.B * p.H - begin : 65535;
-            kern<<<dim3(count, gy), kThreads, smem, stream>>>(part, a);
+            kern<<<dim3(count, gy, gz), kThreads, smem, stream>>>(part, a);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
         return cudaSuccess;

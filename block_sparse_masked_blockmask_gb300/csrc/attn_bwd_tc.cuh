@@ -21,8 +21,9 @@
 //   Q-major   a q block i, walking the kv side of the BlockMask:
 //               S = Q_i K_j^T, dP = dO_i V_j^T, dS, dQ_i += dS K_j.
 // One CTA computes an item's output rows whole, so nothing is accumulated
-// across CTAs and the result does not depend on scheduling.  P is recomputed from the saved
-// lse (no running max).  Roles (320 threads, one CTA per SM):
+// across CTAs (but the parts of attn_bwd_tc_kv_sinks.cu, in a fixed order) and the
+// result does not depend on scheduling.  P is recomputed from the saved lse (no
+// running max).  Roles (320 threads, one CTA per SM):
 //   warps 0-7  elementwise, two threads per owned row (TMEM lane = row):
 //              warps w and w + 4 share a TMEM lane quarter, the first takes
 //              the walked columns 0-63, the second 64-127 (the backward

@@ -20,7 +20,9 @@ cudaError_t launch_bwd_tc_dq(const CUtensorMap (&maps)[4], const BwdTcParams &kp
 cudaError_t launch_bwd_tc_dq_sinks(const CUtensorMap (&maps)[4], const BwdTcParams &kp, int D, int score_kind,
                                    cudaStream_t stream);
 // dK and dV of kv tiles that hold sinks, in parts (attn_bwd_tc_kv_sinks.cu)
-int bwd_tc_parts(const BwdTcParams &kp, int nqt, int &chunks, int &chunk_tiles);
+int bwd_parts(const AttnProblem &p, int dq_size, int worth, int &chunks, int &chunk_tiles);
+cudaError_t launch_bwd_sum_parts(const AttnProblem &p, const float *part, int64_t part_stride, int tiles, int chunks,
+                                 void *dv, void *dk, bool bf16, cudaStream_t stream);
 cudaError_t launch_bwd_tc_dkdv_parts(const CUtensorMap (&maps)[4], const BwdTcParams &kp, int D, int score_kind,
                                      cudaStream_t stream);
 // q blocks per kv block the tensor-core backward walks on chip (NQB limit for bf16)

@@ -385,7 +385,8 @@ FLEX_API int flex_block_mask_transpose(const flex_block_mask *bm, flex_block_mas
  *   dout: device, contiguous [B, H, q_len, D] in q's dtype, 16-byte aligned.
  *   bq:   the q side of bm, from flex_block_mask_transpose.
  *   dq:   device, contiguous [B, H, q_len, D]; dk, dv: [B, H, kv_len, D];
- *         q's dtype, 16-byte aligned.
+ *         q's dtype, 16-byte aligned.  None overlaps an input or another
+ *         output (dq's memory may hold sums of dk and dv until dq is written).
  *   delta: device workspace, [B, H, q_len] float32 (dout[i].out[i]).
  * Rows whose lse is -inf (no unmasked score) contribute nothing.  bf16
  * inputs run on the tensor cores (S, dP and the gradient products as tcgen05

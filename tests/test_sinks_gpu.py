@@ -276,10 +276,12 @@ def check_gradients(q, k, v, g, keep, got, score, r):
 
 @pytest.mark.parametrize("H,q_len,kv_len,D,window,sinks", [(1, 4100, 4100, 64, 256, 4), (2, 5000, 5000, 128, 100, 130),
                                                            (1, 3000, 200, 128, 70, 200), (3, 2048, 2048, 64, 0, 1)])
-def test_few_heads_and_many_query_tiles(H, q_len, kv_len, D, window, sinks):
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_few_heads_and_many_query_tiles(H, q_len, kv_len, D, window, sinks, dtype):
     """dk and dv of the tiles with sinks are summed over parts of the query axis."""
     gen = torch.Generator().manual_seed(q_len + D)
-    q, k, v, g = (torch.randn((1, H, n, D), generator=gen).bfloat16().cuda() for n in (q_len, kv_len, kv_len, q_len))
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, v, g = (torch.randn((1, H, n, D), generator=gen).to(dt).cuda() for n in (q_len, kv_len, kv_len, q_len))
     keep = dense_mask(q_len, kv_len, window, sinks).cuda()
     bm = fa.flex_block_mask_create(fa.FLEX_MASK_WINDOW_SINKS, 1, H, q_len, kv_len, window=window, sinks=sinks)
     bq = fa.flex_block_mask_transpose(bm)
@@ -287,7 +289,7 @@ def test_few_heads_and_many_query_tiles(H, q_len, kv_len, D, window, sinks):
         out, lse = fa.flex_attention_fwd(q, k, v, bm, score)
         got = dict(zip(("dq", "dk", "dv"), fa.flex_attention_bwd(q, k, v, out, lse, g, bm, bq, score)))
         assert fa.flex_device_status() == fa.FLEX_OK
-        check_gradients(q, k, v, g, keep, got, score, 2.0**-8)
+        check_gradients(q, k, v, g, keep, got, score, 2.0**-8 if dtype == "bf16" else 2.0**-18)
 
 
 @pytest.mark.parametrize("score", [fa.FLEX_SCORE_IDENTITY, fa.FLEX_SCORE_SOFTCAP])
