@@ -159,7 +159,7 @@ def _power_scale(amax):
     m, e = torch.frexp(amax)  # amax = m 2^e, m in [0.5, 1)
     e = torch.where(m <= 0.875, e - 9, e - 8)
     e = torch.where(amax > 0, e, torch.full_like(e, -126)).clamp(min=-126)
-    return ((e.to(torch.int32) + 127) << 23).view(torch.float32)
+    return torch.ldexp(torch.ones_like(amax), e)
 
 
 def _pool(gen, pages, case):
@@ -473,8 +473,7 @@ def _exact_append(s):
                 new = x[b, :, done:done + take]
                 if sc is not None:
                     amax = new.abs().amax((1, 2))
-                    want = torch.ceil(torch.log2(amax / E4M3_MAX)).clamp(min=-126.0).long()
-                    want = ((want + 1023) << 52).view(torch.float64)
+                    want = torch.exp2(torch.ceil(torch.log2(amax / E4M3_MAX)))
                     want = torch.where(amax / want > E4M3_MAX, 2 * want, want)
                     want = torch.where(amax / (0.5 * want) <= E4M3_MAX, 0.5 * want, want)
                     if at:
