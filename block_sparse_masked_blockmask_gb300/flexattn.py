@@ -203,14 +203,21 @@ def _stream_handle(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_stream(stream, device):
+    """A context in which torch allocates and works on `stream` (None: nothing to enter)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_handle(stream, device), device)
+    return torch.cuda.stream(stream)
+
+
 def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
     """Memory for a call on `stream`, from that stream's pool: what the pool last lent it for lies before the
     call in the stream's order (None: torch's current stream)."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_handle(stream, device), device)
-    with torch.cuda.stream(stream):
+    with _on_stream(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -288,14 +295,14 @@ class BlockMaskQ:
 
 
 def flex_block_mask_transpose(block_mask: BlockMask, stream=None) -> BlockMaskQ:
-    """The q side of a BlockMask (asynchronous on `stream`)."""
+    """The q side of a BlockMask, from `stream`'s pool (asynchronous on `stream`)."""
     s = block_mask.struct
     device = block_mask.kv_num_blocks.device
     t = {
-        "q_num_blocks": torch.empty((s.B, s.H, s.nkvb), dtype=torch.int32, device=device),
-        "q_indices": torch.empty((s.B, s.H, s.nkvb, s.nqb), dtype=torch.int32, device=device),
-        "full_q_num_blocks": torch.empty((s.B, s.H, s.nkvb), dtype=torch.int32, device=device),
-        "full_q_indices": torch.empty((s.B, s.H, s.nkvb, s.nqb), dtype=torch.int32, device=device),
+        "q_num_blocks": _empty((s.B, s.H, s.nkvb), torch.int32, device, stream),
+        "q_indices": _empty((s.B, s.H, s.nkvb, s.nqb), torch.int32, device, stream),
+        "full_q_num_blocks": _empty((s.B, s.H, s.nkvb), torch.int32, device, stream),
+        "full_q_indices": _empty((s.B, s.H, s.nkvb, s.nqb), torch.int32, device, stream),
     }
     bq = flex_block_mask_q()
     for key in BlockMaskQ.KEYS:
@@ -311,7 +318,7 @@ def flex_block_mask_transpose(block_mask: BlockMask, stream=None) -> BlockMaskQ:
 def flex_block_mask_create(mask_kind: int, B: int, H: int, q_len: int, kv_len: int, block: int = 128,
                            window: int = 0, prefix: int = 0, doc_ids: torch.Tensor | None = None,
                            device=None, stream=None, kv_block: int | None = None, sinks: int = 0) -> BlockMask:
-    """Build a BlockMask on the device (asynchronous on `stream`).
+    """Build a BlockMask on the device, in memory of `stream`'s pool (asynchronous on `stream`).
 
     Tiles are block (Q_BLOCK) rows by kv_block (KV_BLOCK; default: block)
     columns; flex_block_mask_create_qkv is called when kv_block is given.
@@ -324,14 +331,15 @@ def flex_block_mask_create(mask_kind: int, B: int, H: int, q_len: int, kv_len: i
     kvb = block if kv_block is None else kv_block
     nqb, nkvb = -(-q_len // block), -(-kv_len // kvb)  # a tail tile may reach past a length
     t = {
-        "kv_num_blocks": torch.empty((B, H, nqb), dtype=torch.int32, device=device),
-        "kv_indices": torch.empty((B, H, nqb, nkvb), dtype=torch.int32, device=device),
-        "full_kv_num_blocks": torch.empty((B, H, nqb), dtype=torch.int32, device=device),
-        "full_kv_indices": torch.empty((B, H, nqb, nkvb), dtype=torch.int32, device=device),
+        "kv_num_blocks": _empty((B, H, nqb), torch.int32, device, stream),
+        "kv_indices": _empty((B, H, nqb, nkvb), torch.int32, device, stream),
+        "full_kv_num_blocks": _empty((B, H, nqb), torch.int32, device, stream),
+        "full_kv_indices": _empty((B, H, nqb, nkvb), torch.int32, device, stream),
     }
     assert t["kv_num_blocks"].numel() == n_num and t["kv_indices"].numel() == n_idx
     if doc_ids is not None:
-        doc_ids = doc_ids.to(device=device, dtype=torch.int32).contiguous()
+        with _on_stream(stream, device):
+            doc_ids = doc_ids.to(device=device, dtype=torch.int32).contiguous()
     params = _mask_params(mask_kind, window, prefix, sinks, doc_ids)
     bm = flex_block_mask()
     bm.kv_num_blocks = t["kv_num_blocks"].data_ptr()
@@ -373,14 +381,15 @@ def flex_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_
                        score_kind: int = FLEX_SCORE_IDENTITY, score_param: float = 0.0,
                        scale: float | None = None, out: torch.Tensor | None = None,
                        lse: torch.Tensor | None = None, stream=None):
-    """Block-sparse attention forward; returns (out, lse).  Asynchronous on `stream`."""
+    """Block-sparse attention forward; returns (out, lse), allocated from `stream`'s pool where not given.
+    Asynchronous on `stream`."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     B, H, Sq, D = q.shape
     if out is None:
-        out = torch.empty((B, H, Sq, D), dtype=q.dtype, device=q.device)
+        out = _empty((B, H, Sq, D), q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H, Sq), torch.float32, q.device, stream)
     if not out.is_contiguous() or not lse.is_contiguous() or lse.dtype != torch.float32:
         raise ValueError("out and lse must be contiguous; lse float32")
     rc = _call(q.device, load_library().flex_attention_fwd, _tensor(q), _tensor(k), _tensor(v),
@@ -400,17 +409,18 @@ def flex_attention_fwd_opts(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, b
     """flex_attention_fwd with the op's kernel options; returns (out, lse, max_scores).
 
     max_scores (float32 [B, H, Sq]) is allocated when output_max is set and
-    none is given; it is None when OUTPUT_MAX is off.
+    none is given; it is None when OUTPUT_MAX is off.  What is allocated comes
+    from `stream`'s pool.
     """
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     B, H, Sq, D = q.shape
     if out is None:
-        out = torch.empty((B, H, Sq, D), dtype=q.dtype, device=q.device)
+        out = _empty((B, H, Sq, D), q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H, Sq), torch.float32, q.device, stream)
     if max_scores is None and output_max:
-        max_scores = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        max_scores = _empty((B, H, Sq), torch.float32, q.device, stream)
     if not out.is_contiguous() or not lse.is_contiguous() or lse.dtype != torch.float32:
         raise ValueError("out and lse must be contiguous; lse float32")
     if max_scores is not None and (not max_scores.is_contiguous() or max_scores.dtype != torch.float32
@@ -436,15 +446,16 @@ def flex_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: t
                        score_kind: int = FLEX_SCORE_IDENTITY, score_param: float = 0.0,
                        scale: float | None = None, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
                        dv: torch.Tensor | None = None, delta: torch.Tensor | None = None, stream=None):
-    """Gradients (dq, dk, dv) of sum(dout * out); asynchronous on `stream`."""
+    """Gradients (dq, dk, dv) of sum(dout * out); asynchronous on `stream`, from whose pool they and delta are
+    allocated where not given."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     B, H, Sq, D = q.shape
     Skv = k.shape[2]
-    dq = torch.empty((B, H, Sq, D), dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty((B, H, Skv, D), dtype=q.dtype, device=q.device) if dk is None else dk
-    dv = torch.empty((B, H, Skv, D), dtype=q.dtype, device=q.device) if dv is None else dv
-    delta = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device) if delta is None else delta
+    dq = _empty((B, H, Sq, D), q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty((B, H, Skv, D), q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty((B, H, Skv, D), q.dtype, q.device, stream) if dv is None else dv
+    delta = _empty((B, H, Sq), torch.float32, q.device, stream) if delta is None else delta
     for name, t in (("out", out), ("dout", dout), ("dq", dq), ("dk", dk), ("dv", dv)):
         if not t.is_contiguous() or t.dtype != q.dtype:
             raise ValueError(f"{name} must be contiguous in q's dtype")
