@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int he
                     codes[i] = w;
                 }
             }
-            inv = __uint_as_float((254u << 23) - __float_as_uint(now));  // 1 / now, a power of two
+            inv = 1.f / now;  // exact for a power of two, which `now` is unless the page came with another scale
             if (h + 1 < h_last) __syncthreads();  // the cleared word, before the next head's maxima
         }
 #pragma unroll

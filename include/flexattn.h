@@ -479,7 +479,8 @@ FLEX_API int flex_rope_bwd(const flex_tensor *dq, const flex_tensor *dk, const f
  * sequence for all heads; a page table [B, max_pages] int32 (device,
  * contiguous) maps position p of sequence b to page page_table[b][p / page_size],
  * slot p % page_size.  Entries outside 0 .. num_pages - 1 stand for no page.
- * FLEX_DTYPE_E4M3: value = code * scale[page][head] with power-of-two scales.
+ * FLEX_DTYPE_E4M3: value = code * scale[page][head]; scales are positive finite
+ * numbers, powers of two where the append wrote them.
  * The caller owns all of it; nothing need be initialised before the first
  * append.
  */
@@ -502,9 +503,11 @@ typedef struct {
  *                (in float32, with the result rounded once to the cache's type).
  * E4M3: a page's scale is the smallest power of two that keeps the largest
  * magnitude written to it since its first slot was written within 448 scale;
- * when an append raises it, the page's earlier codes are rounded to it.  NaN
- * and infinities are stored as NaN and do not raise the scale.  Tokens whose
- * position has no page (past max_pages, or a bad entry) are dropped; slots
+ * when an append raises it, the page's earlier codes are rounded to it.  A
+ * partly filled page that came with another scale keeps it while it is at least
+ * that power of two.  NaN and infinities are stored as NaN and do not raise the
+ * scale.  Tokens whose position has no page (past max_pages, or a bad entry)
+ * are dropped, and all tokens of a sequence whose cache_lens is negative; slots
  * that get no token keep their contents.  A page must not be appended to from
  * two places of the page table in one call, or by two calls that may run at
  * the same time (sequences may share pages that they only read).
