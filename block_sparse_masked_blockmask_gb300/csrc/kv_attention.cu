@@ -7,9 +7,9 @@
 //
 // Bound by memory: the visible tokens' keys and values are read once (1 or 2
 // bytes a value) for 4 G Q flops per pair of them.  Measured against the 6.77
-// TB/s of a copy (32 sequences x 8 heads x 8192 tokens, D 128, e4m3, G 4): 95 us,
-// 83%; bf16 of half the length 89 us, 89%; G 8: 80%; G 16, two row tiles: 68%.
-// Above 16 rows per head the products bind (170 TFLOP/s at G 8, Q 64).
+// TB/s of a copy (32 sequences x 8 heads x 8192 tokens, D 128, e4m3, G 4): 94 us,
+// 84%; bf16 of half the length 88 us, 90%; G 8: 82%; G 16, two row tiles: 75%.
+// Above 16 rows per head the products bind (192 TFLOP/s at G 8, Q 64; bf16 145).
 //
 // The products run on mma.sync m16n8k16: one such tile has 16 keys against 8
 // query rows, which is what a step of decoding has.  A tcgen05 tile has 128
@@ -37,8 +37,13 @@
 //    first so that they fit fp16 (bf16 values keep all their bits down to 2^-14
 //    of the row's largest).  The page's scale of K multiplies the scores, the
 //    one of V the weights: P is kept relative to the largest V scale met, which
-//    rescales the accumulators when it grows.  P is rounded to fp16 (11 bits),
-//    beside a bf16 cache to bf16 (8 bits) like the operands it meets.
+//    rescales the accumulators when it grows.  That reference is one for all rows
+//    of a tile and goes by scales alone, so that a page with less than 2^-6 of it
+//    would lose weights below fp16's smallest step to a page that a row may not
+//    even keep: such a page's products are taken by themselves, 16 tokens at a
+//    time, with the weights as they are, and scaled in float32.  P is rounded to
+//    fp16 (11 bits), beside a bf16 cache to bf16 (8 bits) like the operands it
+//    meets.
 //  * S^T's accumulators hold keys along lanes' g and rows along t: after
 //    exp, one 8 x 8 transpose (movmatrix) per 8 keys makes them the B operand
 //    P^T.  Statistics, sums and accumulators are float32, and the sum takes the
@@ -62,7 +67,10 @@
 //    evaluate the mask; there the values of tokens that no row keeps are
 //    zeroed, so that whatever lies in those slots has no effect, and where
 //    rows of the call differ in what they keep and such a token's value is not
-//    finite, the step's product is done once per query token.
+//    finite, the step's product is done once per query token.  These steps and
+//    those with a page of a small scale share one path, a head dim tile at a time,
+//    so that it needs no second set of accumulators (with one: 116 bytes of spills
+//    at 16 rows and D 128, and 115 us for 106 at G 16).
 #include <cfloat>
 #include <climits>
 
@@ -91,6 +99,7 @@ constexpr int kEnterCost = 3;
 constexpr int kMinShare = 1;
 constexpr float kTop = 7.f;     // raising the reference leaves the largest weight at 2^7
 constexpr float kRaise = 15.f;  // and is due when one would pass 2^15
+constexpr float kApart = 0x1p-6f;  // pages whose V scale is below this share of the largest are added apart
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
@@ -126,18 +135,17 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     return r;
 }
 template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (F16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // 16 or 8 bytes of shared memory.
 template <int BYTES>
@@ -585,6 +593,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         bool whole = base + C::kTokens <= all_hi && (base >= all_lo || base + C::kTokens <= p.sinks);
 #pragma unroll
         for (int j = 0; j < SUB; ++j) whole = whole && ph[0][j] >= 0;
+        // the largest V scale here; pages far below the largest of all are added
+        // apart (see the products), in steps that take the longer way like those
+        // at an edge
+        float vmax = vs[0][0];
+#pragma unroll
+        for (int j = 1; j < SUB; ++j) vmax = fmaxf(vmax, vs[0][j]);
+        bool apart = false;
+        if constexpr (E4M3) {
+            const float least = fmaxf(vref, vmax) * kApart;
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) apart |= vs[0][j] > 0.f && vs[0][j] < least;
+            whole = whole && !apart;
+        }
         const uint32_t k_at = ring_at + slot * 2 * C::kTile, v_at = k_at + C::kTile;
         // ---- S^T = K Q^T
         if (!__all_sync(0xffffffffu, mbar_wait(&ms.k_full[warp][slot], phase, &ms.abort))) {
@@ -616,20 +637,20 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int nt = 0; nt < NT; ++nt) q[nt] = qs[(nt * KS + s) * 32 + lane];
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
-                uint32_t a0, a1, a2, a3;
+                uint32_t a[4];
                 if constexpr (E4M3) {
-                    a0 = e4m3_lo(kw[j][0][s]);
-                    a1 = e4m3_lo(kw[j][1][s]);
-                    a2 = e4m3_hi(kw[j][0][s]);
-                    a3 = e4m3_hi(kw[j][1][s]);
+                    a[0] = e4m3_lo(kw[j][0][s]);
+                    a[1] = e4m3_lo(kw[j][1][s]);
+                    a[2] = e4m3_hi(kw[j][0][s]);
+                    a[3] = e4m3_hi(kw[j][1][s]);
                 } else {
-                    a0 = kw[j][0][2 * s];
-                    a1 = kw[j][1][2 * s];
-                    a2 = kw[j][0][2 * s + 1];
-                    a3 = kw[j][1][2 * s + 1];
+                    a[0] = kw[j][0][2 * s];
+                    a[1] = kw[j][1][2 * s];
+                    a[2] = kw[j][0][2 * s + 1];
+                    a[3] = kw[j][1][2 * s + 1];
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16816<E4M3>(x[nt][j], a0, a1, a2, a3, q[nt].x, q[nt].y);
+                for (int nt = 0; nt < NT; ++nt) mma16816<E4M3>(x[nt][j], a, q[nt].x, q[nt].y);
             }
         }
         // ---- the values into registers, and their slot free again
@@ -702,9 +723,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
         // ---- running maximum and V scale
-        float vmax = vs[0][0];
-#pragma unroll
-        for (int j = 1; j < SUB; ++j) vmax = fmaxf(vmax, vs[0][j]);
         bool raise = vmax > vref;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) raise |= top[nt][0] > m[nt][0] + kRaise || top[nt][1] > m[nt][1] + kRaise;
@@ -738,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t pb[NT][SUB][2];
 #pragma unroll
         for (int j = 0; j < SUB; ++j) {
-            const float vf = !E4M3 || vs[0][j] == vref ? 1.f : vs[0][j] / vref;
+            const float vf = !E4M3 || apart || vs[0][j] == vref ? 1.f : vs[0][j] / vref;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float w[4];
@@ -757,32 +775,24 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
         // ---- O^T += V^T P^T
-        auto product = [&](auto &&value, auto &&weight) {
-#pragma unroll
-            for (int j = 0; j < SUB; ++j)
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    uint32_t a0, a1, a2, a3;
-                    if constexpr (E4M3) {
-                        const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
-                        const uint32_t lo2 = prmt(value(j, 0, i / 2), value(j, 1, i / 2), sel);
-                        const uint32_t hi2 = prmt(value(j, 2, i / 2), value(j, 3, i / 2), sel);
-                        a0 = e4m3_lo(lo2);
-                        a1 = e4m3_hi(lo2);
-                        a2 = e4m3_lo(hi2);
-                        a3 = e4m3_hi(hi2);
-                    } else {
-                        a0 = prmt(value(j, 0, i), value(j, 1, i), 0x5410u);
-                        a1 = prmt(value(j, 0, i), value(j, 1, i), 0x7632u);
-                        a2 = prmt(value(j, 2, i), value(j, 3, i), 0x5410u);
-                        a3 = prmt(value(j, 2, i), value(j, 3, i), 0x7632u);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<E4M3>(acc[nt][i], a0, a1, a2, a3, weight(nt, j, 0), weight(nt, j, 1));
-                }
+        // operand of head dim tile i from the values of 16 tokens
+        auto operand = [&](int j, int i, auto &&value, uint32_t (&a)[4]) {
+            if constexpr (E4M3) {
+                const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
+                const uint32_t lo2 = prmt(value(j, 0, i / 2), value(j, 1, i / 2), sel);
+                const uint32_t hi2 = prmt(value(j, 2, i / 2), value(j, 3, i / 2), sel);
+                a[0] = e4m3_lo(lo2);
+                a[1] = e4m3_hi(lo2);
+                a[2] = e4m3_lo(hi2);
+                a[3] = e4m3_hi(hi2);
+            } else {
+                a[0] = prmt(value(j, 0, i), value(j, 1, i), 0x5410u);
+                a[1] = prmt(value(j, 0, i), value(j, 1, i), 0x7632u);
+                a[2] = prmt(value(j, 2, i), value(j, 3, i), 0x5410u);
+                a[3] = prmt(value(j, 2, i), value(j, 3, i), 0x7632u);
+            }
         };
-        bool mixed = false;  // a token that some rows keep and some do not has a value that is not finite
+        bool plain = true, mixed = false;  // mixed: a token that some rows keep and some do not has a value that is not finite
         if (!whole) {
             // values of tokens that no row keeps: zero, whatever lies there
 #pragma unroll
@@ -804,44 +814,64 @@ __global__ void __launch_bounds__(kThreads, 2)
                     mixed |= odd && !every;
                 }
             mixed = __any_sync(0xffffffffu, mixed);
+            plain = !mixed && !apart;
         }
-        if (!mixed) {
-            product([&](int j, int r, int c) { return v[j][r][c]; }, [&](int nt, int j, int e) { return pb[nt][j][e]; });
+        if (plain) {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j)
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    uint32_t a[4];
+                    operand(j, i, [&](int j, int r, int c) { return v[j][r][c]; }, a);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816<E4M3>(acc[nt][i], a, pb[nt][j][0], pb[nt][j][1]);
+                }
         } else {
-            // one query token's rows at a time, with what they do not keep
-            // zeroed; the other rows' columns keep their sums, since their
-            // zero weights must not meet a value that is not finite either
+            // mixed: one query token's rows at a time, with what they do not
+            // keep zeroed; the other rows' columns keep their sums, since their
+            // zero weights must not meet a value that is not finite either.
+            // apart: weights as they are, products of 16 tokens by themselves,
+            // which take their page's scale in float32
 #pragma unroll 1
-            for (int tok = tmin; tok <= tmax; ++tok) {
+            for (int tok = tmin; tok <= (mixed ? tmax : tmin); ++tok) {
                 const int at = n - p.Q + tok;
-                float saved[NT][KS][4];
+                auto value = [&](int j, int r, int c) {
+                    const int kv = base + 16 * j + 2 * t + (r & 1) + (r >> 1) * 8;
+                    const bool keep = p.causal ? kv <= at && (at - kv < p.window || kv < p.sinks) : at >= 0 && kv < n;
+                    return !mixed || keep ? v[j][r][c] : 0u;
+                };
+                auto weight = [&](int nt, int j, int e) {  // the operand's column is the lane's g
+                    return !mixed || (r0 + nt * 8 + g) / p.G == tok ? pb[nt][j][e] : 0u;
+                };
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < KS; ++i) {
+                    float sum[NT][4];
 #pragma unroll
-                    for (int i = 0; i < KS; ++i)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) saved[nt][i][e] = acc[nt][i][e];
-                product(
-                    [&](int j, int r, int c) {
-                        const int kv = base + 16 * j + 2 * t + (r & 1) + (r >> 1) * 8;
-                        const bool keep =
-                            p.causal ? kv <= at && (at - kv < p.window || kv < p.sinks) : at >= 0 && kv < n;
-                        return keep ? v[j][r][c] : 0u;
-                    },
-                    [&](int nt, int j, int e) {  // the operand's column is the lane's g
-                        return (r0 + nt * 8 + g) / p.G == tok ? pb[nt][j][e] : 0u;
-                    });
+                        for (int e = 0; e < 4; ++e) sum[nt][e] = acc[nt][i][e];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int j = 0; j < SUB; ++j) {
+                        uint32_t a[4];
+                        operand(j, i, value, a);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        if ((r0 + nt * 8 + 2 * t + u) / p.G != tok) {
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (!apart) {
+                                mma16816<E4M3>(sum[nt], a, weight(nt, j, 0), weight(nt, j, 1));
+                            } else {
+                                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma16816<E4M3>(part, a, weight(nt, j, 0), weight(nt, j, 1));
 #pragma unroll
-                            for (int i = 0; i < KS; ++i) {
-                                acc[nt][i][u] = saved[nt][i][u];
-                                acc[nt][i][u + 2] = saved[nt][i][u + 2];
+                                for (int e = 0; e < 4; ++e) sum[nt][e] += part[e] * (vs[0][j] / vref);
                             }
                         }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!mixed || (r0 + nt * 8 + 2 * t + (e & 1)) / p.G == tok) acc[nt][i][e] = sum[nt][e];
+                }
             }
         }
 #pragma unroll
