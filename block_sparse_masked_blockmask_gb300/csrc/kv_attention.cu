@@ -9,7 +9,7 @@
 // bytes a value) for 4 G Q flops per pair of them.  Measured against the 6.77
 // TB/s of a copy (32 sequences x 8 heads x 8192 tokens, D 128, e4m3, G 4): 94 us,
 // 84%; bf16 of half the length 88 us, 90%; G 8: 82%; G 16, two row tiles: 75%.
-// Above 16 rows per head the products bind (192 TFLOP/s at G 8, Q 64; bf16 145).
+// Above 16 rows per head the products bind (196 TFLOP/s at G 8, Q 64; bf16 148).
 //
 // The products run on mma.sync m16n8k16: one such tile has 16 keys against 8
 // query rows, which is what a step of decoding has.  A tcgen05 tile has 128
@@ -122,11 +122,20 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// cap tanh(s / cap) in base-2 units, as cap (1 - 2 / (1 + e^(2 s / cap))): within
-// 2^-21 cap absolutely (the softmax needs no more), at a tenth of tanhf's
-// instructions.  in = 2 log2(e) / cap, out = cap log2(e).
+// cap tanh(u), u = s / cap, in base-2 units.  From |u| = 1/4 on as cap (1 - 2 / (1
+// + e^(2 u))), which is within 2^-22 cap: about 2^-20 of the result, but nothing
+// of it where u is small.  There the Taylor series to u^9, which leaves out less
+// than 2^-26 of it.  Together a tenth of tanhf's instructions.
+// in = 2 log2(e) / cap, out = cap log2(e), both finite.
 __device__ __forceinline__ float softcap_log2(float s, float in, float out) {
-    return fmaf(-2.f * out, rcp_approx(1.f + ex2_approx(s * in)), out);
+    constexpr double k = 0.69314718055994530942 * 0.69314718055994530942 / 4;  // u^2 = k z^2
+    const float z = s * in, t = z * z;
+    float near = fmaf(t, (float)(62. / 2835 * k * k * k * k), (float)(-17. / 315 * k * k * k));
+    near = fmaf(t, near, (float)(2. / 15 * k * k));
+    near = fmaf(t, near, (float)(-1. / 3 * k));
+    near = fmaf(t, near, 1.f) * (s * kLog2e);
+    const float far = fmaf(out, -2.f * rcp_approx(1.f + ex2_approx(z)), out);
+    return fabsf(z) < 0.5f * kLog2e ? near : far;
 }
 // 8 x 8 transpose of 16-bit values across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -682,7 +691,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[nt][j][e] *= qscale[nt][e & 1] * ks[0][j];
         if (p.score_kind == FLEX_SCORE_SOFTCAP) {
-            const float cap_in = 2.f * kLog2e / p.score_param, cap_out = p.score_param * kLog2e;
+            const float cap_in = fminf(2.f * kLog2e / p.score_param, FLT_MAX),
+                        cap_out = fminf(p.score_param * kLog2e, FLT_MAX);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
