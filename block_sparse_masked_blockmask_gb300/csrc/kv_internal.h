@@ -63,12 +63,16 @@ int64_t cache_attention_workspace(const CacheAttnProblem &p, int cache_dtype);  
 cudaError_t launch_cache_attention(const CacheAttnProblem &p, int cache_dtype, cudaStream_t stream);
 
 // Angles are kept as turns in 64-bit fixed point: position * frequency wraps
-// modulo one turn by itself, so the angle of any int32 position is as exact as
-// the frequency (2^-53 of it).  In float32 the angle of position 131072 would
-// be off by 0.004 radians.
+// modulo one turn by itself.  The frequency's turns are within 2^-64 (of
+// frequencies up to 2^40), so that the angle of any int32 position is within
+// 2^-33 of a turn; the rounded product with a rounded 1 / (2 pi) would be off by
+// 2^-25 of a turn at position 2^31 and 0.75 radians per position, and by more
+// for larger frequencies.  In float32 the angle of position 131072 would be off
+// by 0.004 radians.
 __device__ __forceinline__ uint64_t turns_per_position(double inv_freq) {
-    const double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-    return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
+    constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi) as a sum
+    const double t = inv_freq * hi, rest = fma(inv_freq, lo, fma(inv_freq, hi, -t));  // the product, as a sum
+    return (uint64_t)__double2ll_rn((t - rint(t)) * 0x1p64) + (uint64_t)__double2ll_rn(rest * 0x1p64);
 }
 // Sine and cosine of a position's angle.  What is left of it beside whole
 // quarter turns goes to float32, x in [-1/4, 1/4] half turns: rounding it moves

@@ -457,8 +457,8 @@ FLEX_API int flex_rope_frequencies(int32_t rotary_dim, double base, int32_t scal
  *   q_out, k_out : tensors of the inputs' shapes with their own strides;
  *               they may be the inputs themselves (same data and strides) and
  *               must not overlap them otherwise.
- * Angles are within 2^-28 of a turn at every position; sine, cosine and the
- * rotation are float32, the result is rounded once.
+ * Angles are within 2^-28 + 2^-32 of a turn at every position, for frequencies up
+ * to 2^40; sine, cosine and the rotation are float32, the result is rounded once.
  * Errors: FLEX_ERR_INVALID_ARG, FLEX_ERR_SHAPE, FLEX_ERR_ALIGNMENT,
  * FLEX_ERR_UNSUPPORTED (head dim, rotary_dim not a multiple of 16, B > 65535,
  * heads > 32767), FLEX_ERR_CUDA.  Asynchronous on `stream`.
