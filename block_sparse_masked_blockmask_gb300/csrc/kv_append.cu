@@ -152,7 +152,12 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(AppendProblem p, int he
     };
     load();
     if (rotate) {
-        for (int i = threadIdx.x; i < p.rotary / 2; i += blockDim.x) turns[i] = turns_per_position(p.inv_freq[i]);
+        auto convert = [&](int i) { turns[i] = turns_per_position(p.inv_freq[i]); };
+        if constexpr (kItems > 1) {  // more than 128 threads for 64 pairs at most; a loop would spill more
+            if ((int)threadIdx.x < p.rotary / 2) convert((int)threadIdx.x);
+        } else {
+            for (int i = threadIdx.x; i < p.rotary / 2; i += blockDim.x) convert(i);
+        }
         __syncthreads();
         // a thread keeps its two pairs and walks the tokens
         constexpr int kPer = 4 * IT;  // entries per token
