@@ -7,9 +7,9 @@
 //
 // Bound by memory: the visible tokens' keys and values are read once (1 or 2
 // bytes a value) for 4 G Q flops per pair of them.  Measured against the 6.77
-// TB/s of a copy (32 sequences x 8 heads x 8192 tokens, D 128, e4m3, G 4): 94 us,
-// 84%; bf16 of half the length 88 us, 90%; G 8: 82%; G 16, two row tiles: 75%.
-// Above 16 rows per head the products bind (196 TFLOP/s at G 8, Q 64; bf16 148).
+// TB/s of a copy (32 sequences x 8 heads x 8192 tokens, D 128, e4m3, G 4): 93.4 us,
+// 85%; bf16 of half the length 88.7 us, 89%; G 8: 82%; G 16, two row tiles: 75%.
+// Above 16 rows per head the products bind (197 TFLOP/s at G 8, Q 64; bf16 149).
 //
 // The products run on mma.sync m16n8k16: one such tile has 16 keys against 8
 // query rows, which is what a step of decoding has.  A tcgen05 tile has 128
