@@ -534,13 +534,14 @@ FLEX_API int flex_kv_cache_append(const flex_kv_cache *cache, const flex_tensor 
  *               read, nor the pages that hold no others.
  *   score_kind, score_param, scale : as for flex_attention_fwd.
  *   out, lse  : device, contiguous [B, Hq, Q, D] bf16 and [B, Hq, Q] float32.
+ *               out may be a contiguous q itself; no other memory overlaps.
  * Rows that keep nothing get out = 0, lse = -inf; tokens on a bad page count
  * as masked.  What lies in slots that a row does not keep has no effect on
  * it, NaN included.  Scales are taken as positive numbers of any value, those
  * of V up to 2^80 apart within a sequence, and values of V up to 2^80 (weights
  * and sums are float32); the append writes powers of two.  Made for few query
  * tokens (a decoding step, a handful of tokens to check); any Q is computed, at
- * up to 190 TFLOP/s (a first prompt with as many key heads as query heads is
+ * up to 197 TFLOP/s (a first prompt with as many key heads as query heads is
  * faster in flex_attention_fwd).  Errors: as flex_kv_cache_append, and
  * FLEX_ERR_UNSUPPORTED for fp32 q and for the prefix and document masks.
  *   workspace : device, 16-byte aligned, at least as many bytes as

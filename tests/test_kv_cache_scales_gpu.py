@@ -176,3 +176,21 @@ def test_scale_beside_a_value_that_is_not_finite():
         diff = (out[0].double() - want).abs() <= bound
         diff[:, 2, 5] = True
         assert diff.all(), e
+
+
+@pytest.mark.parametrize("n,B,H,G,Q", [(700, 2, 2, 4, 1), (5000, 40, 8, 4, 1), (130, 3, 2, 5, 7), (3000, 1, 1, 16, 2)])
+def test_result_in_place_of_the_queries(n, B, H, G, Q):
+    gen = torch.Generator().manual_seed(n)
+    D, page = 128, 64
+    width = -(-n // page)
+    cache = fa.flex_kv_cache_create(width, H, D, page, E4M3)
+    cache.k.copy_(torch.randn(cache.k.shape, generator=gen))
+    cache.v.copy_(torch.randn(cache.v.shape, generator=gen))
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(1.0)
+    table = torch.arange(width, dtype=torch.int32, device="cuda").expand(B, width).contiguous()
+    lens = torch.randint(1, n + 1, (B,), generator=gen).int().cuda()
+    q = torch.randn((B, H * G, Q, D), generator=gen).bfloat16().cuda()
+    out, lse = fa.flex_kv_cache_attention(q, cache, table, lens)
+    again, l2 = fa.flex_kv_cache_attention(q, cache, table, lens, out=q)
+    assert again is q and torch.equal(out, q) and torch.equal(lse, l2)
