@@ -82,13 +82,15 @@ int check_tables(const int32_t *page_table, const int32_t *lens) {
 
 int check_cache(const flex_kv_cache *c, int32_t max_pages) {
     if (!c || !c->k || !c->v) return FLEX_ERR_INVALID_ARG;
-    if (c->dtype != FLEX_DTYPE_BF16 && c->dtype != FLEX_DTYPE_E4M3) return FLEX_ERR_INVALID_ARG;
-    if (c->dtype == FLEX_DTYPE_E4M3 && (!c->k_scale || !c->v_scale)) return FLEX_ERR_INVALID_ARG;
+    if (c->dtype != FLEX_DTYPE_BF16 && c->dtype != FLEX_DTYPE_E4M3 && c->dtype != FLEX_DTYPE_INT4)
+        return FLEX_ERR_INVALID_ARG;
+    if (c->dtype != FLEX_DTYPE_BF16 && (!c->k_scale || !c->v_scale)) return FLEX_ERR_INVALID_ARG;
     if (c->num_pages <= 0 || c->H <= 0 || c->page_size <= 0 || c->D <= 0 || max_pages <= 0) return FLEX_ERR_SHAPE;
     if (c->D != 64 && c->D != 128) return FLEX_ERR_UNSUPPORTED;
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return FLEX_ERR_UNSUPPORTED;
     if (c->H > 32767 || (int64_t)c->num_pages * c->H > INT32_MAX || (int64_t)max_pages * c->page_size > kMaxCacheLen) return FLEX_ERR_UNSUPPORTED;
-    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    const uintptr_t scale_bytes = c->dtype == FLEX_DTYPE_INT4 ? 16 : 4;  // INT4: copied in 16-byte words
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, scale_bytes) || !aligned(c->v_scale, scale_bytes))
         return FLEX_ERR_ALIGNMENT;
     return FLEX_OK;
 }
@@ -97,7 +99,52 @@ KvCache cache_of(const flex_kv_cache *c) {
     int shift = 4;
     while ((1 << shift) < c->page_size) ++shift;
     return KvCache{c->num_pages, c->H, c->page_size, c->D, shift, static_cast<uint8_t *>(c->k),
-                   static_cast<uint8_t *>(c->v), c->k_scale, c->v_scale};
+                   static_cast<uint8_t *>(c->v), static_cast<float *>(c->k_scale), static_cast<float *>(c->v_scale)};
+}
+
+// The checks that both forms of the append share; on success p holds all but
+// the sequences and what each of them appends.
+int append_problem(const flex_kv_cache *cache, const flex_tensor *k, const flex_tensor *v, const int32_t *page_table,
+                   int32_t max_pages, const int32_t *cache_lens, const flex_rope_params *r, AppendProblem &p) {
+    int rc = check_cache(cache, max_pages);
+    if (rc == FLEX_OK) rc = check_tables(page_table, cache_lens);
+    if (rc != FLEX_OK) return rc;
+    if ((rc = check_dtype_dim(k)) != FLEX_OK) return rc;
+    if (k->shape[3] != cache->D || k->shape[1] != cache->H) return FLEX_ERR_SHAPE;
+    if ((rc = check_tensor(k, k->dtype, k->shape[0], cache->H, k->shape[2], cache->D)) != FLEX_OK) return rc;
+    if ((rc = check_tensor(v, k->dtype, k->shape[0], cache->H, k->shape[2], cache->D)) != FLEX_OK) return rc;
+    if (r && (rc = check_rope(r, cache->D)) != FLEX_OK) return rc;
+    p.S = (int)k->shape[2];
+    p.cache = cache_of(cache);
+    p.k = k->data;
+    p.v = v->data;
+    take_strides(k, p.k_stride);
+    take_strides(v, p.v_stride);
+    p.page_table = page_table;
+    p.max_pages = max_pages;
+    p.cache_lens = cache_lens;
+    if (r) {
+        p.inv_freq = r->inv_freq;
+        p.rotary = r->rotary_dim;
+        p.layout = r->layout;
+        p.attention_scale = r->attention_scale;
+    }
+    return FLEX_OK;
+}
+
+int append(const AppendProblem &p, int src_dtype, int cache_dtype, void *stream) {
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = cache_dtype == FLEX_DTYPE_INT4 ? launch_kv_append_int4(p, src_dtype, s)
+                                                         : launch_kv_append(p, src_dtype, cache_dtype, s);
+    return e == cudaSuccess ? FLEX_OK : FLEX_ERR_CUDA;
+}
+
+// Packed sequences: a tensor of one batch entry and where they begin in it.
+int check_packed(const flex_tensor *t, const int32_t *starts, int32_t sequences) {
+    if (!starts) return FLEX_ERR_INVALID_ARG;
+    if (t->shape[0] != 1 || sequences <= 0) return FLEX_ERR_SHAPE;
+    if (sequences > 65535) return FLEX_ERR_UNSUPPORTED;
+    return aligned(starts, 4) ? FLEX_OK : FLEX_ERR_ALIGNMENT;
 }
 
 // The checks of sizes, types and mask that the attention and its workspace
@@ -107,6 +154,7 @@ int cache_problem(const flex_tensor *q, const flex_kv_cache *cache, int32_t max_
     int rc = check_cache(cache, max_pages);
     if (rc == FLEX_OK) rc = check_dtype_dim(q);
     if (rc != FLEX_OK) return rc;
+    if (cache->dtype == FLEX_DTYPE_INT4) return FLEX_ERR_UNSUPPORTED;
     if (q->dtype != FLEX_DTYPE_BF16) return FLEX_ERR_UNSUPPORTED;
     switch (mask_kind) {
         case FLEX_MASK_CAUSAL:
@@ -187,36 +235,54 @@ int flex_rope_bwd(const flex_tensor *dq, const flex_tensor *dk, const flex_rope_
 int flex_kv_cache_append(const flex_kv_cache *cache, const flex_tensor *k, const flex_tensor *v,
                          const int32_t *page_table, int32_t max_pages, const int32_t *cache_lens,
                          const int32_t *new_lens, const flex_rope_params *r, void *stream) {
-    int rc = check_cache(cache, max_pages);
-    if (rc == FLEX_OK) rc = check_tables(page_table, cache_lens);
-    if (rc != FLEX_OK) return rc;
-    if ((rc = check_dtype_dim(k)) != FLEX_OK) return rc;
-    if (k->shape[3] != cache->D || k->shape[1] != cache->H) return FLEX_ERR_SHAPE;
-    if ((rc = check_tensor(k, k->dtype, k->shape[0], cache->H, k->shape[2], cache->D)) != FLEX_OK) return rc;
-    if ((rc = check_tensor(v, k->dtype, k->shape[0], cache->H, k->shape[2], cache->D)) != FLEX_OK) return rc;
-    if (r && (rc = check_rope(r, cache->D)) != FLEX_OK) return rc;
-    if (!aligned(new_lens, 4)) return FLEX_ERR_ALIGNMENT;
     AppendProblem p = {};
+    const int rc = append_problem(cache, k, v, page_table, max_pages, cache_lens, r, p);
+    if (rc != FLEX_OK) return rc;
+    if (!aligned(new_lens, 4)) return FLEX_ERR_ALIGNMENT;
     p.B = (int)k->shape[0];
-    p.S = (int)k->shape[2];
+    p.new_lens = new_lens;
+    return append(p, k->dtype, cache->dtype, stream);
+}
+
+int flex_kv_cache_append_packed(const flex_kv_cache *cache, const flex_tensor *k, const flex_tensor *v,
+                                const int32_t *starts, int32_t sequences, const int32_t *page_table, int32_t max_pages,
+                                const int32_t *cache_lens, const flex_rope_params *r, void *stream) {
+    AppendProblem p = {};
+    int rc = append_problem(cache, k, v, page_table, max_pages, cache_lens, r, p);
+    if (rc == FLEX_OK) rc = check_packed(k, starts, sequences);
+    if (rc != FLEX_OK) return rc;
+    p.B = sequences;
+    p.starts = starts;
+    return append(p, k->dtype, cache->dtype, stream);
+}
+
+int flex_kv_cache_read(const flex_kv_cache *cache, const int32_t *page_table, int32_t max_pages, const int32_t *starts,
+                       int32_t sequences, const flex_tensor *k_out, const flex_tensor *v_out, void *stream) {
+    int rc = check_cache(cache, max_pages);
+    if (rc != FLEX_OK) return rc;
+    if (!page_table) return FLEX_ERR_INVALID_ARG;
+    if (!aligned(page_table, 4)) return FLEX_ERR_ALIGNMENT;
+    if ((rc = check_dtype_dim(k_out)) != FLEX_OK) return rc;
+    if ((rc = check_packed(k_out, starts, sequences)) != FLEX_OK) return rc;
+    if (k_out->shape[3] != cache->D || k_out->shape[1] != cache->H) return FLEX_ERR_SHAPE;
+    const int64_t T = k_out->shape[2];
+    if ((rc = check_tensor(k_out, k_out->dtype, 1, cache->H, T, cache->D)) != FLEX_OK) return rc;
+    if ((rc = check_tensor(v_out, k_out->dtype, 1, cache->H, T, cache->D)) != FLEX_OK) return rc;
+    ReadProblem p = {};
+    p.B = sequences;
+    p.T = (int)T;
     p.cache = cache_of(cache);
-    p.k = k->data;
-    p.v = v->data;
-    take_strides(k, p.k_stride);
-    take_strides(v, p.v_stride);
     p.page_table = page_table;
     p.max_pages = max_pages;
-    p.cache_lens = cache_lens;
-    p.new_lens = new_lens;
-    if (r) {
-        p.inv_freq = r->inv_freq;
-        p.rotary = r->rotary_dim;
-        p.layout = r->layout;
-        p.attention_scale = r->attention_scale;
+    p.starts = starts;
+    const flex_tensor *out[2] = {k_out, v_out};
+    for (int w = 0; w < 2; ++w) {
+        p.out[w] = const_cast<void *>(out[w]->data);
+        p.out_stride[w][0] = out[w]->stride[1];
+        p.out_stride[w][1] = out[w]->stride[2];
     }
-    return launch_kv_append(p, k->dtype, cache->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? FLEX_OK
-               : FLEX_ERR_CUDA;
+    return launch_kv_read(p, cache->dtype, k_out->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FLEX_OK
+                                                                                                         : FLEX_ERR_CUDA;
 }
 
 int flex_kv_cache_attention_workspace(const flex_tensor *q, const flex_kv_cache *cache, int32_t max_pages,

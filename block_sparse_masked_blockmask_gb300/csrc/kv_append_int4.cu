@@ -1,0 +1,257 @@
+// Appending keys and values to a paged cache of 4-bit codes: value = (code - 8)
+// * scale, with one bf16 scale for 32 neighbouring values of a key and one for
+// all values of a value row,
+//   scale = bf16(m / 7), m the largest magnitude;  code = 8 + round(x / scale),
+// halves away from zero, so that codes are 1 .. 15 (x / scale is 7 / (1 - 2^-8)
+// at most, which rounds to 7).  Keys are rotated by their position on the way,
+// in float32.
+//
+// No token's codes depend on another's, so a (token, head) is D / 32 threads
+// with 32 values each: the R = 1024 / D values from 32 j + R p on of every group
+// j for thread p, which is what its 16 bytes of codes hold (the order of codes
+// that the attention wants, see include/flexattn.h).  A group's largest
+// magnitude is one or two exchanges between the threads; a quotient is one fused
+// multiply-add: x times a reciprocal that is rounded up lies beyond a half where
+// x / scale is one (bf16 x: quotients that are not halves are 2^-9 away from
+// them), and the addend 2^23 + 2^22 + 8 leaves the code in the low bits.
+#include "kv_internal.h"
+#include "kv_values.cuh"
+
+namespace flex {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr float kLeastScale = 0x1p-120f;  // below it (m below 8e-36) a scale is 0 and the values are
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+// The lowest bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return prmt(prmt(a, b, 0x0040u), prmt(c, d, 0x0040u), 0x5410u);
+}
+
+// bf16 scale (its bits in a float's upper half) of the largest magnitude, from
+// that one's bits.  NaN and infinities make the scale NaN, which all values
+// of the group then stand for.
+__device__ __forceinline__ float scale_of(uint32_t most) {
+    if (most >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+    const float s = __uint_as_float(pack_bf16x2(0.f, __fdiv_rn(__uint_as_float(most), 7.f)));
+    return s >= kLeastScale ? s : 0.f;
+}
+// 1 / scale, rounded up past its nearest float; 0 for scales of 0 and NaN.
+__device__ __forceinline__ float reciprocal_up(float scale) {
+    return scale > 0.f ? __uint_as_float(__float_as_uint(__frcp_rn(scale)) + 1u) : 0.f;
+}
+
+// T: source type; IS_V: values (else keys).  Threads of a CTA: tokens x heads
+// at a time x D / 32.
+template <typename T, int D, bool IS_V>
+__device__ __forceinline__ void append_rows(const AppendProblem &p, int64_t token0, int tokens, int h_first, int h_last,
+                                            float2 *table, uint64_t *turns) {
+    constexpr int P = D / 32, J = D / 32, R = 1024 / D, RUNS = 4;  // threads; groups; values of a run; 8-value pieces
+    const int part = threadIdx.x % P, slot = threadIdx.x / P, heads = kThreads / P / tokens;
+    const int tok = slot % tokens, h0 = h_first + slot / tokens;
+    // this thread's token
+    const int64_t token = token0 + tok;
+    int b, t;
+    int64_t row;  // of the source: the batch entry's token, or the packed token
+    bool live;
+    if (p.starts) {
+        live = token < p.S;
+        b = live ? sequence_of(p.starts, p.B, (int)token) : -1;
+        live = b >= 0;
+        t = live ? (int)token - __ldg(p.starts + b) : 0;
+        row = token;
+    } else {
+        live = token < (int64_t)p.B * p.S;
+        b = live ? (int)(token / p.S) : 0;
+        t = (int)(token % p.S);
+        row = t;
+        live = live && t < (p.new_lens ? __ldg(p.new_lens + b) : p.S);
+    }
+    int64_t position = 0, at = 0;
+    if (live) {
+        const int first = __ldg(p.cache_lens + b);
+        position = (int64_t)first + t;
+        const int64_t entry = position >> p.cache.page_shift;
+        live = first >= 0 && entry < p.max_pages;
+        if (live) {
+            const int id = __ldg(p.page_table + (int64_t)b * p.max_pages + entry);
+            live = id >= 0 && id < p.cache.num_pages;
+            at = (int64_t)id * p.cache.H * p.cache.page + (position & (p.cache.page - 1));  // of head 0
+        }
+    }
+    const int pairs = IS_V || !p.inv_freq ? 0 : p.rotary / 2;
+    if (pairs) {
+        for (int i = threadIdx.x; i < pairs; i += kThreads) turns[i] = turns_per_position(p.inv_freq[i]);
+        __syncthreads();
+        // the threads of a slot share out the pairs of its token; slots of the same token write the same
+        if (live) {
+            const int sharers = heads * P, me = slot / tokens * P + part;
+            for (int i = me; i < pairs; i += sharers) {
+                float2 cs;
+                sincos_at(turns[i], (int32_t)position, &cs.y, &cs.x);
+                cs.x *= p.attention_scale;
+                cs.y *= p.attention_scale;
+                table[tok * pairs + i] = cs;
+            }
+        }
+        __syncthreads();
+    }
+    const int64_t *st = IS_V ? p.v_stride : p.k_stride;
+    const T *src = static_cast<const T *>(IS_V ? p.v : p.k) + (p.starts ? 0 : b * st[0]) + row * st[2];
+    const float2 *cs = table + tok * pairs;
+    for (int h = h0; h - slot / tokens < h_last; h += heads) {
+        const bool mine = live && h < h_last;
+        float x[RUNS][8];
+        uint32_t most[J];
+        if (mine) {
+            Raw8<T> raw[RUNS];
+#pragma unroll
+            for (int k = 0; k < RUNS; ++k) raw[k].load(src + h * st[1] + 32 * (k * J / RUNS) + R * part + 8 * (k % (RUNS / J)));
+#pragma unroll
+            for (int k = 0; k < RUNS; ++k) raw[k].unpack(x[k]);
+            if (pairs && p.layout == FLEX_ROPE_HALF) {
+                if (p.rotary == D) {  // a run's partner is the thread's own, two further on
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int d = 32 * (k * J / RUNS) + R * part + 8 * (k % (RUNS / J));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 w = cs[d + e];
+                            const float a = x[k][e], z = x[k + 2][e];
+                            x[k][e] = a * w.x - z * w.y;
+                            x[k + 2][e] = z * w.x + a * w.y;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < RUNS; ++k) {
+                        const int d = 32 * (k * J / RUNS) + R * part + 8 * (k % (RUNS / J));
+                        if (d >= p.rotary) continue;
+                        const bool low = d < pairs;
+                        Raw8<T> other;
+                        other.load(src + h * st[1] + (low ? d + pairs : d - pairs));
+                        float z[8];
+                        other.unpack(z);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 w = cs[(low ? d : d - pairs) + e];
+                            x[k][e] = x[k][e] * w.x + (low ? -z[e] : z[e]) * w.y;
+                        }
+                    }
+                }
+            } else if (pairs) {
+#pragma unroll
+                for (int k = 0; k < RUNS; ++k) {
+                    const int d = 32 * (k * J / RUNS) + R * part + 8 * (k % (RUNS / J));
+                    if (d >= p.rotary) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float2 w = cs[(d + e) / 2];
+                        const float a = x[k][e], z = x[k][e + 1];
+                        x[k][e] = a * w.x - z * w.y;
+                        x[k][e + 1] = z * w.x + a * w.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) most[j] = 0u;
+#pragma unroll
+            for (int k = 0; k < RUNS; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    uint32_t &m = most[IS_V ? 0 : k * J / RUNS];
+                    m = max(m, __float_as_uint(x[k][e]) & 0x7FFFFFFFu);
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j) most[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < (IS_V ? 1 : J); ++j)
+#pragma unroll
+            for (int o = 1; o < P; o <<= 1) most[j] = max(most[j], __shfl_xor_sync(0xffffffffu, most[j], o));
+        if (!mine) continue;
+        float scale[J], inv[J];
+#pragma unroll
+        for (int j = 0; j < (IS_V ? 1 : J); ++j) {
+            scale[j] = scale_of(most[j]);
+            inv[j] = reciprocal_up(scale[j]);
+        }
+        const int64_t out = at + (int64_t)h * p.cache.page;
+        // codes in the low bytes, 8 where the scale is 0 or NaN
+        uint32_t c[RUNS][8];
+#pragma unroll
+        for (int k = 0; k < RUNS; ++k) {
+            const float f = inv[IS_V ? 0 : k * J / RUNS];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[k][e] = __float_as_uint(fmaf(f > 0.f ? x[k][e] : 0.f, f, 12582920.f));
+        }
+        // a 16-bit unit of four codes for each group j and each four of the R values; units of all groups together
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const int unit = 2 * i + n / 4, g = unit / J, j = unit % J, r = 4 * g + n % 4;  // r: within the run
+                v[n] = c[j * (RUNS / J) + r / 8][r % 8];
+            }
+            w[i] = low_bytes(v[0], v[2], v[4], v[6]) | low_bytes(v[1], v[3], v[5], v[7]) << 4;
+        }
+        *reinterpret_cast<uint4 *>((IS_V ? p.cache.v : p.cache.k) + out * (D / 2) + part * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (part == 0) {
+            if constexpr (IS_V)
+                reinterpret_cast<uint16_t *>(p.cache.v_scale)[out] = (uint16_t)(__float_as_uint(scale[0]) >> 16);
+            else
+#pragma unroll
+                for (int j = 0; j < J; j += 2)
+                    reinterpret_cast<uint32_t *>(p.cache.k_scale)[(out * J + j) / 2] =
+                        prmt(__float_as_uint(scale[j]), __float_as_uint(scale[j + 1]), 0x7632u);
+        }
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) kv_append_int4_kernel(const AppendProblem p, int tokens, int heads_per_cta, int groups) {
+    extern __shared__ __align__(16) float2 table[];  // [token][pair] (cos, sin)
+    __shared__ uint64_t turns[64];
+    const bool is_v = (int)blockIdx.y >= groups;
+    const int h_first = ((int)blockIdx.y - (is_v ? groups : 0)) * heads_per_cta;
+    const int h_last = min(h_first + heads_per_cta, p.cache.H);
+    const int64_t token0 = (int64_t)blockIdx.x * tokens;
+    if (is_v)
+        append_rows<T, D, true>(p, token0, tokens, h_first, h_last, table, turns);
+    else
+        append_rows<T, D, false>(p, token0, tokens, h_first, h_last, table, turns);
+}
+
+template <typename T, int D>
+cudaError_t launch(const AppendProblem &p, cudaStream_t stream) {
+    const int64_t all = p.starts ? p.S : (int64_t)p.B * p.S;
+    // a CTA takes a power of two of tokens and walks the heads with their sines and cosines
+    int tokens = kThreads / (D / 32);
+    while (tokens > 1 && (all + tokens - 1) / tokens * 2 < 2 * 152) tokens /= 2;
+    int heads = p.cache.H;
+    const int64_t tiles = (all + tokens - 1) / tokens;
+    const int at_once = kThreads / (D / 32) / tokens;
+    while (heads > at_once && tiles * 2 * ((p.cache.H + heads - 1) / heads) < 6 * 152) heads = (heads + 1) / 2;
+    const int groups = (p.cache.H + heads - 1) / heads;
+    if (tiles > INT32_MAX || 2 * groups > 65535) return cudaErrorInvalidValue;
+    const int smem = p.inv_freq ? tokens * p.rotary * 4 : 0;
+    kv_append_int4_kernel<T, D><<<dim3((unsigned)tiles, 2u * groups), kThreads, smem, stream>>>(p, tokens, heads, groups);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append_int4(const AppendProblem &p, int src_dtype, cudaStream_t stream) {
+    if (src_dtype == FLEX_DTYPE_BF16) return p.cache.D == 64 ? launch<uint16_t, 64>(p, stream) : launch<uint16_t, 128>(p, stream);
+    return p.cache.D == 64 ? launch<float, 64>(p, stream) : launch<float, 128>(p, stream);
+}
+
+}  // namespace flex

@@ -1,0 +1,10 @@
+// Appending packed sequences' keys and values to a paged cache of bf16 or e4m3.
+#include "kv_append_kernel.cuh"
+
+namespace flex {
+
+cudaError_t launch_kv_append_packed(const AppendProblem &p, int src_dtype, int cache_dtype, cudaStream_t stream) {
+    return launch_append_typed<true>(p, src_dtype, cache_dtype, stream);
+}
+
+}  // namespace flex

@@ -23,20 +23,31 @@ struct RopeProblem {
 struct KvCache {
     int num_pages, H, page, D, page_shift;
     uint8_t *k, *v;
-    float *k_scale, *v_scale;        // e4m3 only
+    float *k_scale, *v_scale;        // e4m3: float32; int4: bf16 (cast where they are used); else unused
 };
 
 struct AppendProblem {
-    int B, S;
+    int B, S;                        // sequences; tokens of each, or of all where they are packed
     KvCache cache;
     const void *k, *v;
     int64_t k_stride[3], v_stride[3];  // b, h, s (elements)
     const int32_t *page_table;       // [B, max_pages]
     int max_pages;
     const int32_t *cache_lens, *new_lens;
+    const int32_t *starts;           // [B + 1]: where packed sequences begin; null: k, v are [B, H, S, D]
     const double *inv_freq;          // null: no rotation
     int rotary, layout;
     float attention_scale;
+};
+
+struct ReadProblem {
+    int B, T;                        // sequences, packed tokens
+    KvCache cache;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *starts;           // [B + 1]
+    void *out[2];                    // keys, values
+    int64_t out_stride[2][2];        // h, token (elements)
 };
 
 struct CacheAttnProblem {
@@ -59,6 +70,9 @@ struct CacheAttnProblem {
 
 cudaError_t launch_rope(const RopeProblem &p, int dtype, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendProblem &p, int src_dtype, int cache_dtype, cudaStream_t stream);
+cudaError_t launch_kv_append_packed(const AppendProblem &p, int src_dtype, int cache_dtype, cudaStream_t stream);
+cudaError_t launch_kv_append_int4(const AppendProblem &p, int src_dtype, cudaStream_t stream);
+cudaError_t launch_kv_read(const ReadProblem &p, int cache_dtype, int out_dtype, cudaStream_t stream);
 int64_t cache_attention_workspace(const CacheAttnProblem &p, int cache_dtype);  // bytes
 cudaError_t launch_cache_attention(const CacheAttnProblem &p, int cache_dtype, cudaStream_t stream);
 

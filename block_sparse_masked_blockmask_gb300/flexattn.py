@@ -41,6 +41,7 @@ FLEX_SCORE_ALIBI = 2
 FLEX_DTYPE_BF16 = 0
 FLEX_DTYPE_FP32 = 1
 FLEX_DTYPE_E4M3 = 2
+FLEX_DTYPE_INT4 = 3
 
 FLEX_ROPE_HALF = 0
 FLEX_ROPE_INTERLEAVED = 1
@@ -54,7 +55,8 @@ EXPORTED = ("flex_block_mask_sizes", "flex_block_mask_sizes_qkv", "flex_block_ma
             "flex_block_mask_transpose", "flex_attention_fwd",
             "flex_attention_fwd_opts", "flex_attention_bwd", "flex_attention_fwd_noalloc", "flex_attention_fwd_host", "flex_device_status",
             "flex_selftest_wait_timeout", "flex_status_string", "flex_rope_frequencies", "flex_rope_fwd", "flex_rope_bwd",
-            "flex_kv_cache_append", "flex_kv_cache_attention", "flex_kv_cache_attention_workspace")
+            "flex_kv_cache_append", "flex_kv_cache_append_packed", "flex_kv_cache_read",
+            "flex_kv_cache_attention", "flex_kv_cache_attention_workspace")
 
 
 class FlexError(RuntimeError):
@@ -180,6 +182,10 @@ def load_library():
             cp = ctypes.POINTER(flex_kv_cache)
             lib.flex_kv_cache_append.argtypes = [cp, tp, tp, vp, i32, vp, vp, vp, vp]
             lib.flex_kv_cache_append.restype = ctypes.c_int
+            lib.flex_kv_cache_append_packed.argtypes = [cp, tp, tp, vp, i32, vp, i32, vp, vp, vp]
+            lib.flex_kv_cache_append_packed.restype = ctypes.c_int
+            lib.flex_kv_cache_read.argtypes = [cp, vp, i32, vp, i32, tp, tp, vp]
+            lib.flex_kv_cache_read.restype = ctypes.c_int
             lib.flex_kv_cache_attention.argtypes = [tp, cp, vp, i32, vp, i32, ctypes.POINTER(flex_mask_params), i32,
                                                     ctypes.c_float, ctypes.c_float, vp, vp, vp, ctypes.c_int64, vp]
             lib.flex_kv_cache_attention.restype = ctypes.c_int
@@ -639,38 +645,51 @@ def flex_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, inv_freq: torch.Ten
     return _rope("flex_rope_bwd", dq, dk, inv_freq, positions, layout, attention_scale, dq_out, dk_out, stream)
 
 
-_CACHE_DTYPES = {torch.bfloat16: FLEX_DTYPE_BF16, torch.float8_e4m3fn: FLEX_DTYPE_E4M3}
+_CACHE_DTYPES = {torch.bfloat16: FLEX_DTYPE_BF16, torch.float8_e4m3fn: FLEX_DTYPE_E4M3, torch.uint8: FLEX_DTYPE_INT4}
 
 
 class KVCache:
     """Paged key/value cache: the C struct plus the torch tensors that own its memory.
 
     k, v: contiguous [num_pages, H, page_size, D], bfloat16 or float8_e4m3fn;
-    the latter with k_scale, v_scale: contiguous float32 [num_pages, H].
+    the latter with k_scale, v_scale: contiguous float32 [num_pages, H].  Or
+    uint8 [num_pages, H, page_size, D / 2], two 4-bit codes a byte, with
+    k_scale bfloat16 [num_pages, H, page_size, D / 32] and v_scale bfloat16
+    [num_pages, H, page_size] (the order of codes is in include/flexattn.h).
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):
         if k.dim() != 4 or k.dtype not in _CACHE_DTYPES:
-            raise ValueError("k must be a bfloat16 or float8_e4m3fn [num_pages, H, page_size, D] tensor")
-        scaled = k.dtype == torch.float8_e4m3fn
+            raise ValueError("k must be a bfloat16, float8_e4m3fn or uint8 [num_pages, H, page_size, D] tensor")
+        dtype = _CACHE_DTYPES[k.dtype]
+        scaled = dtype != FLEX_DTYPE_BF16
         if scaled != (k_scale is not None) or scaled != (v_scale is not None):
-            raise ValueError("an e4m3 cache needs k_scale and v_scale, a bf16 cache takes none")
+            raise ValueError("an e4m3 or 4-bit cache needs k_scale and v_scale, a bf16 cache takes none")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         n, h, page, d = k.shape
-        self.struct = flex_kv_cache(n, h, page, d, _CACHE_DTYPES[k.dtype], 0,
+        scales = (torch.float32, (n, h), (n, h))
+        if dtype == FLEX_DTYPE_INT4:
+            d *= 2
+            scales = (torch.bfloat16, (n, h, page, d // 32), (n, h, page))
+        self.shape = (n, h, page, d)  # pages, heads, page size, head dim
+        self.struct = flex_kv_cache(n, h, page, d, dtype, 0,
                                     _device_array(k, "k", k.dtype, k.device, k.shape),
                                     _device_array(v, "v", k.dtype, k.device, k.shape),
-                                    _device_array(k_scale, "k_scale", torch.float32, k.device, (n, h)),
-                                    _device_array(v_scale, "v_scale", torch.float32, k.device, (n, h)))
+                                    _device_array(k_scale, "k_scale", scales[0], k.device, scales[1]),
+                                    _device_array(v_scale, "v_scale", scales[0], k.device, scales[2]))
         self._ref = ctypes.byref(self.struct)
 
 
 def flex_kv_cache_create(num_pages: int, H: int, D: int, page_size: int = 64,
                          dtype: torch.dtype = torch.float8_e4m3fn, device=None) -> KVCache:
-    """A new cache of num_pages pages (uninitialised) on `device`."""
+    """A new cache of num_pages pages (uninitialised) on `device`; dtype torch.uint8 makes one of 4-bit codes."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    k, v = (torch.empty((num_pages, H, page_size, D), dtype=dtype, device=device) for _ in range(2))
+    row = D // 2 if dtype == torch.uint8 else D
+    k, v = (torch.empty((num_pages, H, page_size, row), dtype=dtype, device=device) for _ in range(2))
+    if dtype == torch.uint8:
+        return KVCache(k, v, torch.empty((num_pages, H, page_size, D // 32), dtype=torch.bfloat16, device=device),
+                       torch.empty((num_pages, H, page_size), dtype=torch.bfloat16, device=device))
     if dtype != torch.float8_e4m3fn:
         return KVCache(k, v)
     return KVCache(k, v, *(torch.empty((num_pages, H), dtype=torch.float32, device=device) for _ in range(2)))
@@ -700,6 +719,70 @@ def flex_kv_cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_
                _stream_handle(stream, device))
     if rc != FLEX_OK:
         raise FlexError(rc, "flex_kv_cache_append")
+
+
+def _starts(starts: torch.Tensor, device) -> tuple[int, int]:
+    """The address of a [sequences + 1] array of packed sequences' first tokens, and how many sequences those are."""
+    if starts.dim() != 1 or starts.shape[0] < 2:
+        raise ValueError("starts must be an int32 [sequences + 1] tensor")
+    return _device_array(starts, "starts", torch.int32, device, starts.shape), starts.shape[0] - 1
+
+
+def flex_kv_cache_append_packed(cache: KVCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor,
+                                page_table: torch.Tensor, cache_lens: torch.Tensor,
+                                inv_freq: torch.Tensor | None = None, layout: int = FLEX_ROPE_HALF,
+                                attention_scale: float = 1.0, stream=None) -> None:
+    """flex_kv_cache_append of packed sequences: tokens starts[b] .. starts[b + 1] - 1 of k, v [1, H, T, D] go behind
+    sequence b's cache_lens[b] tokens (asynchronous on `stream`).
+
+    starts int32 [sequences + 1], ascending; page_table int32 [sequences, max_pages], cache_lens int32 [sequences].
+    """
+    device = cache.k.device
+    if k.device != device or v.device != device:
+        raise ValueError("k and v must be on the cache's device")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 [sequences, max_pages] tensor")
+    at, B = _starts(starts, device)
+    max_pages = page_table.shape[1]
+    rc = _call(device, load_library().flex_kv_cache_append_packed, cache._ref, _tensor(k), _tensor(v), at, B,
+               _device_array(page_table, "page_table", torch.int32, device, (B, max_pages)), max_pages,
+               _device_array(cache_lens, "cache_lens", torch.int32, device, (B,)),
+               None if inv_freq is None else _rope_params(inv_freq, layout, attention_scale, device),
+               _stream_handle(stream, device))
+    if rc != FLEX_OK:
+        raise FlexError(rc, "flex_kv_cache_append_packed")
+
+
+def flex_kv_cache_read(cache: KVCache, page_table: torch.Tensor, starts: torch.Tensor, total: int | None = None,
+                       dtype: torch.dtype = torch.bfloat16, k_out: torch.Tensor | None = None,
+                       v_out: torch.Tensor | None = None, stream=None):
+    """The cache's tokens as packed sequences: position p of sequence b is token starts[b] + p of the returned
+    (k, v) [1, H, total, D], for the starts[b + 1] - starts[b] first positions of each (asynchronous on `stream`).
+
+    page_table int32 [sequences, max_pages], starts int32 [sequences + 1].  Outputs not given are allocated
+    from `stream`'s pool with `total` tokens, in `dtype` (bfloat16 or float32), a token's heads next to each other in
+    memory, as flex_attention_packed_fwd and a projection have them.
+    """
+    device = cache.k.device
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 [sequences, max_pages] tensor")
+    at, B = _starts(starts, device)
+    max_pages = page_table.shape[1]
+    table = _device_array(page_table, "page_table", torch.int32, device, (B, max_pages))
+    outs = []
+    for x in (k_out, v_out):
+        if x is None:
+            if total is None:
+                raise ValueError("total is needed where k_out and v_out are not both given")
+            x = _empty((1, total, cache.shape[1], cache.shape[3]), dtype, device, stream).transpose(1, 2)
+        elif x.device != device:
+            raise ValueError("the outputs must be on the cache's device")
+        outs.append(x)
+    rc = _call(device, load_library().flex_kv_cache_read, cache._ref, table, max_pages, at, B, _tensor(outs[0]),
+               _tensor(outs[1]), _stream_handle(stream, device))
+    if rc != FLEX_OK:
+        raise FlexError(rc, "flex_kv_cache_read")
+    return outs[0], outs[1]
 
 
 def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -735,7 +818,7 @@ def flex_kv_cache_attention(q: torch.Tensor, cache: KVCache, page_table: torch.T
     params = None if mask_kind == FLEX_MASK_CAUSAL and not sinks else \
         ctypes.byref(_mask_params(mask_kind, window, 0, sinks))
     if workspace is None:
-        size = _cache_workspace_bytes(shape, cache.k.shape, cache.struct.dtype, max_pages, mask_kind, window, sinks)
+        size = _cache_workspace_bytes(shape, cache.shape, cache.struct.dtype, max_pages, mask_kind, window, sinks)
         workspace = _empty((size,), torch.uint8, device, stream)
     else:
         _device_array(workspace, "workspace", torch.uint8, device, workspace.shape)
@@ -768,7 +851,7 @@ def flex_kv_cache_attention_workspace(q: torch.Tensor, cache: KVCache, max_pages
     """Bytes of workspace that flex_kv_cache_attention needs for these sizes."""
     if q.dim() != 4:
         raise ValueError("q must be a [B, Hq, Q, D] tensor")
-    return _cache_workspace_bytes(q.shape, cache.k.shape, cache.struct.dtype, max_pages, mask_kind, window, sinks)
+    return _cache_workspace_bytes(q.shape, cache.shape, cache.struct.dtype, max_pages, mask_kind, window, sinks)
 
 
 def flex_selftest_wait_timeout(limit_ms: int = 50, stream=None, device=None) -> None:

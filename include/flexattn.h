@@ -13,7 +13,9 @@
  *                           (flex_block_mask_transpose) for dk and dv.
  *   flex_rope_fwd, flex_rope_bwd       rotary positions of q and k, and the gradient
  *   flex_kv_cache_append               new keys (rotated on the way) and values
- *                                      into a paged cache (bf16 or e4m3)
+ *                                      into a paged cache (bf16, e4m3 or 4 bits)
+ *   flex_kv_cache_append_packed        the same for packed sequences
+ *   flex_kv_cache_read                 the cache's tokens as packed tensors
  *   flex_kv_cache_attention            the newest tokens' attention against it
  * Helpers size the BlockMask buffers, name status codes and read the device
  * status word.
@@ -100,7 +102,8 @@ typedef enum {
 typedef enum {
     FLEX_DTYPE_BF16 = 0,           /* bfloat16 storage; tensor-core path, fp32 accumulation */
     FLEX_DTYPE_FP32 = 1,           /* float32 storage; float32-accurate tensor-core forward */
-    FLEX_DTYPE_E4M3 = 2            /* 8-bit floating point with scales; key/value caches only */
+    FLEX_DTYPE_E4M3 = 2,           /* 8-bit floating point with scales; key/value caches only */
+    FLEX_DTYPE_INT4 = 3            /* 4-bit codes with scales; key/value caches only        */
 } flex_dtype;
 
 /* Parameters of a mask_mod.  Unused fields are ignored for kinds that do not need them. */
@@ -481,16 +484,25 @@ FLEX_API int flex_rope_bwd(const flex_tensor *dq, const flex_tensor *dk, const f
  * slot p % page_size.  Entries outside 0 .. num_pages - 1 stand for no page.
  * FLEX_DTYPE_E4M3: value = code * scale[page][head]; scales are positive finite
  * numbers, powers of two where the append wrote them.
+ * FLEX_DTYPE_INT4: value = (code - 8) * scale, codes 1 .. 15 where the append wrote
+ * them (0 reads as -8); one scale for 32 neighbouring values of a key
+ * (k_scale[page][head][slot][value / 32]) and one for all D of a value
+ * (v_scale[page][head][slot]), bfloat16, zero or positive.  A token's row is D / 4
+ * little-endian 16-bit words of four codes, the first in the lowest bits: word
+ * (D / 32) g + j holds values 32 j + 4 g .. 32 j + 4 g + 3.
  * The caller owns all of it; nothing need be initialised before the first
  * append.
  */
 typedef struct {
     int32_t num_pages, H;          /* pages; key/value heads                                  */
     int32_t page_size, D;          /* a power of two from 16 to 256; head dim 64 or 128       */
-    int32_t dtype;                 /* FLEX_DTYPE_BF16 or FLEX_DTYPE_E4M3                      */
+    int32_t dtype;                 /* FLEX_DTYPE_BF16, FLEX_DTYPE_E4M3 or FLEX_DTYPE_INT4     */
     int32_t reserved;
-    void *k, *v;                   /* device, [num_pages, H, page_size, D], 16-byte aligned   */
-    float *k_scale, *v_scale;      /* device, [num_pages, H] float32 (E4M3; else unused)      */
+    void *k, *v;                   /* device, [num_pages, H, page_size, D] values or codes (INT4:
+                                      D / 2 bytes a token), 16-byte aligned                   */
+    void *k_scale, *v_scale;       /* device; E4M3: [num_pages, H] float32; INT4: [num_pages, H,
+                                      page_size, D / 32] and [num_pages, H, page_size] bfloat16,
+                                      16-byte aligned; BF16: unused                           */
 } flex_kv_cache;
 
 /*
@@ -506,7 +518,12 @@ typedef struct {
  * when an append raises it, the page's earlier codes are rounded to it.  A
  * partly filled page that came with another scale keeps it while it is at least
  * that power of two.  NaN and infinities are stored as NaN and do not raise the
- * scale.  Tokens whose position has no page (past max_pages, or a bad entry)
+ * scale.
+ * INT4: scale = bfloat16(m / 7), m the largest magnitude of the values it is for (0
+ * below 2^-120), code = 8 + x / scale rounded to the nearest whole number, halves
+ * away from zero.  A NaN or an infinity makes the scale NaN, and all values that
+ * share it.
+ * Tokens whose position has no page (past max_pages, or a bad entry)
  * are dropped, and all tokens of a sequence whose cache_lens is negative; slots
  * that get no token keep their contents.  A page must not be appended to from
  * two places of the page table in one call, or by two calls that may run at
@@ -519,6 +536,38 @@ typedef struct {
 FLEX_API int flex_kv_cache_append(const flex_kv_cache *cache, const flex_tensor *k, const flex_tensor *v,
                                   const int32_t *page_table, int32_t max_pages, const int32_t *cache_lens,
                                   const int32_t *new_lens, const flex_rope_params *rope, void *stream);
+
+/*
+ * flex_kv_cache_append for packed sequences: k, v [1, H, T, D]; tokens starts[b]
+ * .. starts[b + 1] - 1 of them are sequence b's new ones.
+ *   starts     : device, [sequences + 1] int32, ascending (equal neighbours: no new
+ *                tokens), within 0 .. T; tokens before starts[0] and from
+ *                starts[sequences] on are not read.  Entries that do not ascend
+ *                within 0 .. T reach no memory outside the tensors, but which tokens
+ *                are appended where is then not defined.
+ *   page_table : [sequences, max_pages];  cache_lens : [sequences].
+ * Everything else, and the errors, as flex_kv_cache_append.
+ */
+FLEX_API int flex_kv_cache_append_packed(const flex_kv_cache *cache, const flex_tensor *k, const flex_tensor *v,
+                                         const int32_t *starts, int32_t sequences, const int32_t *page_table,
+                                         int32_t max_pages, const int32_t *cache_lens, const flex_rope_params *rope,
+                                         void *stream);
+
+/*
+ * Read the cache back as packed sequences: position p of sequence b goes to
+ * token starts[b] + p of k_out, v_out [1, H, T, D], for starts[b] + p <
+ * starts[b + 1].
+ *   starts     : device, [sequences + 1] int32, as for flex_kv_cache_append_packed.
+ *   k_out, v_out : bf16 or fp32 (one type), with their own strides; they do not
+ *                overlap each other or the cache.  Values are code times scale,
+ *                rounded once to the type.
+ * Positions that have no page read as zeros; tokens before starts[0] and from
+ * starts[sequences] on are left as they were.  Errors: as flex_kv_cache_append.
+ * Asynchronous on `stream`.
+ */
+FLEX_API int flex_kv_cache_read(const flex_kv_cache *cache, const int32_t *page_table, int32_t max_pages,
+                                const int32_t *starts, int32_t sequences, const flex_tensor *k_out,
+                                const flex_tensor *v_out, void *stream);
 
 /*
  * Attention of each sequence's newest tokens against the cache.  q is
