@@ -154,7 +154,6 @@ int cache_problem(const flex_tensor *q, const flex_kv_cache *cache, int32_t max_
     int rc = check_cache(cache, max_pages);
     if (rc == FLEX_OK) rc = check_dtype_dim(q);
     if (rc != FLEX_OK) return rc;
-    if (cache->dtype == FLEX_DTYPE_INT4) return FLEX_ERR_UNSUPPORTED;
     if (q->dtype != FLEX_DTYPE_BF16) return FLEX_ERR_UNSUPPORTED;
     switch (mask_kind) {
         case FLEX_MASK_CAUSAL:

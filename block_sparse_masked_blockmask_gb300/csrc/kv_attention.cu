@@ -71,41 +71,13 @@
 //    those with a page of a small scale share one path, a head dim tile at a time,
 //    so that it needs no second set of accumulators (with one: 116 bytes of spills
 //    at 16 rows and D 128, and 115 us for 106 at G 16).
-#include <cfloat>
-#include <climits>
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "kv_internal.h"
-#include "ptx.cuh"
+#include "kv_attention_common.cuh"
 
 namespace flex {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kJoinThreads = 512;
-constexpr int kJoinMany = 8;       // warps of the main launch per pair, from which CTAs join a row
-constexpr int kMaxCtas = 152 * 2;  // of the main launch: two on every SM
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-// Entering and finishing a (sequence, head, row tile) costs a warp the time of
-// some steps: the list counts that many units more for each (512 pairs, ragged
-// to 8192 tokens: none 134 us, 1: 114, 2 to 6: 98).  A warp takes one unit at
-// least: few steps are over sooner with more of them in flight (513 tokens of 8
-// heads: 12.5 us, and 14.6 with two, 18.1 with four).
-constexpr int kEnterCost = 3;
-constexpr int kMinShare = 1;
-constexpr float kTop = 7.f;     // raising the reference leaves the largest weight at 2^7
-constexpr float kRaise = 15.f;  // and is due when one would pass 2^15
 constexpr float kApart = 0x1p-6f;  // pages whose V scale is below this share of the largest are added apart
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-    uint32_t r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-    return r;
-}
 // Two e4m3 codes (low or high half of w) to fp16x2, exactly.
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
     uint32_t r;
@@ -117,60 +89,6 @@ __device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
     return r;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// cap tanh(u), u = s / cap, in base-2 units.  From |u| = 1/4 on as cap (1 - 2 / (1
-// + e^(2 u))), which is within 2^-22 cap: about 2^-20 of the result, but nothing
-// of it where u is small.  There the Taylor series to u^9, which leaves out less
-// than 2^-26 of it.  Together a tenth of tanhf's instructions.
-// in = 2 log2(e) / cap, out = cap log2(e), both finite.
-__device__ __forceinline__ float softcap_log2(float s, float in, float out) {
-    constexpr double k = 0.69314718055994530942 * 0.69314718055994530942 / 4;  // u^2 = k z^2
-    const float z = s * in, t = z * z;
-    float near = fmaf(t, (float)(62. / 2835 * k * k * k * k), (float)(-17. / 315 * k * k * k));
-    near = fmaf(t, near, (float)(2. / 15 * k * k));
-    near = fmaf(t, near, (float)(-1. / 3 * k));
-    near = fmaf(t, near, 1.f) * (s * kLog2e);
-    const float far = fmaf(out, -2.f * rcp_approx(1.f + ex2_approx(z)), out);
-    return fabsf(z) < 0.5f * kLog2e ? near : far;
-}
-// 8 x 8 transpose of 16-bit values across the warp.
-__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
-    return r;
-}
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (F16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// 16 or 8 bytes of shared memory.
-template <int BYTES>
-__device__ __forceinline__ void load_shared(uint32_t *w, uint32_t addr) {
-    if constexpr (BYTES == 8)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-    else
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(addr));
-}
-
-// Zero, once the loads that a depends on have returned (a warp's loads from
-// shared memory return in order): a slot is refilled only after its last word
-// was read.  The bit test cannot be folded away, and lane 0 alone uses it.
-__device__ __forceinline__ uint32_t zero_after(uint32_t a, uint32_t zero) { return a & zero; }
 
 // D: head dim; E4M3: cache type (else bf16); NT: tiles of 8 query rows.
 template <int D, bool E4M3, int NT>
@@ -201,49 +119,6 @@ struct Misc {
     int abort;
 };
 
-// Steps of a sequence: tokens that any of its query rows keeps, [0, send) and
-// [lo_min, hi), in whole steps.
-struct Steps {
-    int n, hi, send, lo, nsink, count;
-    int64_t lo_min;
-    __device__ __forceinline__ int base(int i, int tokens) const {
-        return i < nsink ? i * tokens : lo + (i - nsink) * tokens;
-    }
-};
-template <int TOKENS>
-__device__ __forceinline__ Steps steps_of(const CacheAttnProblem &p, int kv_len) {
-    Steps s;
-    s.n = (int)min((int64_t)max(kv_len, 0), (int64_t)p.max_pages * p.cache.page);
-    s.hi = s.n;  // the last query token is the last token
-    s.lo_min = p.causal ? max((int64_t)s.n - p.Q - p.window + 1, (int64_t)0) : 0;
-    s.lo = (int)min(s.lo_min, (int64_t)s.hi) / TOKENS * TOKENS;
-    s.send = min(p.sinks, s.hi);
-    s.nsink = (s.send + TOKENS - 1) / TOKENS;
-    if (s.nsink * (int64_t)TOKENS >= s.lo) {
-        s.nsink = 0;
-        s.lo = 0;
-    }
-    s.count = max(s.nsink + (s.hi - s.lo + TOKENS - 1) / TOKENS, 1);  // an empty sequence: one empty step
-    return s;
-}
-
-// The workspace: the size of a warp's share of the list, where each sequence
-// begins in it, and two partial results per warp (rows x (D + 2) floats:
-// accumulators, maximum, sum): of a piece that begins inside its (sequence,
-// head, row tile), and of one that begins with it but does not end it.
-__host__ __device__ constexpr int64_t workspace_partials(int64_t B) { return (8 * (B + 1) + 15) / 16 * 16; }
-__host__ __device__ constexpr int64_t partial_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
-
-// Two neighbouring output values of query row `row` of a head group, and its lse.
-template <int D>
-__device__ __forceinline__ void store_pair(const CacheAttnProblem &p, int b, int hk, int row, int d, float a, float z,
-                                           float top, float sum) {
-    const int64_t o = ((int64_t)b * p.Hq + hk * p.G + row % p.G) * p.Q + row / p.G;
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays
-    *reinterpret_cast<uint32_t *>(p.out + o * D + d) = pack_bf16x2(a * inv, z * inv);
-    if (d == 0) p.lse[o] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-}
-
 // CAP: softcap scores, compiled apart: their instructions in the loop's body, which
 // outgrows the instruction caches near the warps, cost the other scores 1% (64
 // sequences ragged to 8192: 98.5 us for 97.4).
@@ -273,95 +148,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         fence_barrier_init();
     }
 
-    // ---- the warp's share of the list.  Thread i adds up a run of sequences;
-    // the block's prefix sums then give the total and where a step falls.
+    // ---- the warp's share of the list
     const int pairs_per_seq = p.cache.H * row_tiles;  // (head, row tile) pairs, the row tiles innermost
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b_first = min((int)threadIdx.x * per, p.B), b_last = min(b_first + per, p.B);
-    auto seq_units = [&](int i) {
-        return (int64_t)(steps_of<C::kTokens>(p, __ldg(p.kv_lens + i)).count + kEnterCost) * pairs_per_seq;
-    };
-    int64_t mine = 0;
-    for (int i = b_first; i < b_last; ++i) mine += seq_units(i);
-    int64_t upto = mine;  // inclusive scan
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) ms.sums[warp] = upto;
-    __syncthreads();
-    int64_t total = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += ms.sums[w];
-        total += ms.sums[w];
-    }
-    const int64_t workers = (int64_t)gridDim.x * kWarps;
-    const int64_t share = max((total + workers - 1) / workers, (int64_t)kMinShare);
-    int64_t *head = reinterpret_cast<int64_t *>(p.workspace);
-    if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) head[0] = share;
-        int64_t at = before + upto - mine;
-        for (int i = b_first; i < b_last; ++i) {
-            head[1 + i] = at;
-            at += seq_units(i);
-        }
-    }
-    // neighbouring shares go to different CTAs, so that few steps spread over
-    // the SMs
-    const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
-    const int64_t begin = worker * share;
-    if (begin >= total) return;
-    // the sequence that `begin` falls in: first the block's warp, then its lane, then its run
-    int b = 0;
-    int64_t off = begin;
-    {
-        int64_t skipped = 0;
-        int w0 = 0;
-        while (w0 + 1 < kWarps && begin >= skipped + ms.sums[w0]) skipped += ms.sums[w0++];
-        off = begin - skipped;
-        b = w0 * 32 * per;
-        for (int i0 = 0; i0 < 32 * per; i0 += 32) {  // 32 sequences at a time
-            const int64_t size = b + lane < p.B ? seq_units(b + lane) : 0;
-            int64_t sum = size;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += v;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, sum > off);
-            if (past) {
-                const int f = __ffs(past) - 1;
-                off -= __shfl_sync(0xffffffffu, sum - size, f);
-                b += f;
-                break;
-            }
-            off -= __shfl_sync(0xffffffffu, sum, 31);
-            b += 32;
-        }
-    }
-
-    // from units of the list to the steps among them: those of this warp, and
-    // the first of them within its sequence
-    int steps = 0;
-    {
-        int64_t left = min(share, total - begin), from = off;
-        for (int i = b; left > 0; ++i) {
-            const int count = steps_of<C::kTokens>(p, __ldg(p.kv_lens + i)).count, unit = count + kEnterCost;
-            auto real = [&](int64_t o) { return o / unit * count + max((int)(o % unit) - kEnterCost, 0); };
-            const int64_t to = min(from + left, (int64_t)unit * pairs_per_seq);
-            const int64_t here = real(to) - real(from);
-            if (steps == 0) {
-                b = i;
-                off = real(from);
-            }
-            steps += (int)here;
-            left -= to - from;
-            from = 0;
-        }
-    }
-    if (steps == 0) return;
+    int b, worker, steps;
+    int64_t off;
+    if (!take_share<C::kTokens>(p, pairs_per_seq, ms.sums, b, off, steps, worker)) return;
 
     // ---- steps ahead of the computation.  Lane i looks up the warp's step
     // 32 k + i, so that the loads' latencies are met once in 32 steps: its first
@@ -928,139 +719,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-// Joins the pieces of one (sequence, head, row tile), one warp a row; nothing
-// to do for one that a single warp covered.  For lists in which a pair is a few
-// warps' share (512 pairs: 98 us in all, 137 with the kernel below).
-template <int D, int ROWS, int TOKENS>
-__global__ void __launch_bounds__(32 * ROWS) cache_attention_join_few_kernel(const CacheAttnProblem p, int row_tiles) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int V = D / 32;  // values per lane
-    const int pairs_per_seq = p.cache.H * row_tiles;
-    const int b = (int)(blockIdx.x / pairs_per_seq), pair = (int)(blockIdx.x % pairs_per_seq);
-    const int r = threadIdx.x / 32, d = threadIdx.x % 32 * V, r0 = pair % row_tiles * ROWS;
-    if (r0 + r >= p.Q * p.G) return;
-    const int64_t *head = reinterpret_cast<const int64_t *>(p.workspace);
-    const int64_t share = head[0];
-    const int count = steps_of<TOKENS>(p, __ldg(p.kv_lens + b)).count;
-    const int64_t begin = head[1 + b] + (int64_t)pair * (count + kEnterCost) + kEnterCost;  // of its first step
-    const int c0 = (int)(begin / share), c1 = (int)((begin + count - 1) / share);
-    if (c0 == c1) return;
-    const float *parts =
-        reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(p.workspace) + workspace_partials(p.B));
-    float top = -FLT_MAX, sum = 0.f, acc[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    constexpr int U = 4;  // pieces in flight
-    for (int c = c0; c <= c1; c += U) {
-        float2 ml[U];
-        float o[U][V];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            ml[u] = make_float2(-FLT_MAX, 0.f);
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[u][v] = 0.f;
-            if (c + u <= c1) {
-                const float *part = parts + (2 * (int64_t)(c + u) + (c + u == c0)) * partial_floats(ROWS, D);
-                ml[u] = __ldcg(reinterpret_cast<const float2 *>(part + ROWS * D + 2 * r));
-#pragma unroll
-                for (int v = 0; v < V; v += 2) {
-                    const float2 w = __ldcg(reinterpret_cast<const float2 *>(part + r * D + d + v));
-                    o[u][v] = w.x;
-                    o[u][v + 1] = w.y;
-                }
-            }
-        }
-        float now = top;
-#pragma unroll
-        for (int u = 0; u < U; ++u) now = fmaxf(now, ml[u].x);
-        const float f0 = exp2f(top - now);
-        top = now;
-        sum *= f0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] *= f0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const float f = exp2f(ml[u].x - now);
-            sum += f * ml[u].y;
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] += f * o[u][v];
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < V; v += 2)
-        store_pair<D>(p, b, pair / row_tiles, r0 + r, d + v, acc[v], acc[v + 1], top, sum);
-}
-
-// The same for pairs that many warps share: one CTA for 32 head dims of a row,
-// two of them a thread, in groups that share out the pieces (16 pairs of 76
-// pieces: 96 us in all, 109 with the kernel above).
-template <int D, int ROWS, int TOKENS>
-__global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(const CacheAttnProblem p, int row_tiles) {
-    constexpr int kColumns = 16, kGroups = kJoinThreads / kColumns, kJoinWarps = kJoinThreads / 32;
-    __shared__ float top_s[kJoinWarps], sum_s[kJoinWarps], factor[kMaxCtas * kWarps];
-    __shared__ float2 value_s[kJoinWarps][kColumns];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int pairs_per_seq = p.cache.H * row_tiles, warp = threadIdx.x / 32;
-    const int b = (int)(blockIdx.x / pairs_per_seq), pair = (int)(blockIdx.x % pairs_per_seq), r = (int)blockIdx.y;
-    const int64_t *head = reinterpret_cast<const int64_t *>(p.workspace);
-    const int64_t share = head[0];
-    const int count = steps_of<TOKENS>(p, __ldg(p.kv_lens + b)).count;
-    const int64_t begin = head[1 + b] + (int64_t)pair * (count + kEnterCost) + kEnterCost;  // of its first step
-    const int c0 = (int)(begin / share), c1 = (int)((begin + count - 1) / share);
-    const int r0 = pair % row_tiles * ROWS;
-    if (c0 == c1 || r0 + r >= p.Q * p.G) return;
-    const float *parts =
-        reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(p.workspace) + workspace_partials(p.B));
-    auto part = [&](int c) { return parts + (2 * (int64_t)c + (c == c0)) * partial_floats(ROWS, D); };
-    auto stats = [&](int c) { return __ldcg(reinterpret_cast<const float2 *>(part(c) + ROWS * D + 2 * r)); };
-    // the pieces' maxima, and what each is worth relative to the largest
-    const int pieces = c1 - c0 + 1;
-    float top = -FLT_MAX;
-    for (int c = threadIdx.x; c < pieces; c += kJoinThreads) {
-        factor[c] = stats(c0 + c).x;
-        top = fmaxf(top, factor[c]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (threadIdx.x % 32 == 0) top_s[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, top_s[w]);
-    float sum = 0.f;
-    for (int c = threadIdx.x; c < pieces; c += kJoinThreads) {
-        factor[c] = exp2f(factor[c] - top);
-        sum += factor[c] * stats(c0 + c).y;
-    }
-    __syncthreads();
-    const int column = threadIdx.x % kColumns, group = threadIdx.x / kColumns;
-    const int d = (int)blockIdx.z * 2 * kColumns + 2 * column;
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll 8
-    for (int c = group; c < pieces; c += kGroups) {
-        const float2 o = __ldcg(reinterpret_cast<const float2 *>(part(c0 + c) + r * D + d));
-        s.x += o.x * factor[c];
-        s.y += o.y * factor[c];
-    }
-    // over the threads: the row's sum, and each column's values
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    s.x += __shfl_xor_sync(0xffffffffu, s.x, kColumns);
-    s.y += __shfl_xor_sync(0xffffffffu, s.y, kColumns);
-    if (threadIdx.x % 32 == 0) sum_s[warp] = sum;
-    if (threadIdx.x % 32 < kColumns) value_s[warp][column] = s;
-    __syncthreads();
-    if (threadIdx.x >= kColumns) return;
-    sum = 0.f;
-    s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        sum += sum_s[w];
-        s.x += value_s[w][column].x;
-        s.y += value_s[w][column].y;
-    }
-    store_pair<D>(p, b, pair / row_tiles, r0 + r, d, s.x, s.y, top, sum);
-}
-
 // The cache's keys or values as [pages * heads][page][D]: boxes of box_rows
 // tokens by one panel.
 template <int D, bool E4M3>
@@ -1072,24 +730,6 @@ bool make_cache_map(CUtensorMap *map, const void *base, const KvCache &c, int bo
     return make_tile_map_3d(map, base, E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims,
                             strides, box,
                             C::kPanelBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
-// Query rows per tile: 8, or 16 from nine rows on (the keys are converted once
-// for both halves).
-int tile_rows(const CacheAttnProblem &p) { return (int64_t)p.Q * p.G <= 8 ? 8 : 16; }
-
-// CTAs of the main launch: one wave, or as many as there can be steps, from
-// what the host knows of the lengths.
-int64_t main_ctas(const CacheAttnProblem &p, int tokens) {
-    const int rows = tile_rows(p);
-    const int64_t pairs = (int64_t)p.B * p.cache.H * (((int64_t)p.Q * p.G + rows - 1) / rows);
-    int64_t most = (int64_t)p.max_pages * p.cache.page;
-    if (p.window != INT_MAX) {
-        const int64_t w = (int64_t)p.window + p.sinks + p.Q + 2 * tokens;
-        most = most < w ? most : w;
-    }
-    const int64_t steps = pairs * ((most + tokens - 1) / tokens + 1), wave = kMaxCtas;
-    return steps < wave ? steps : wave;
 }
 
 template <int D, bool E4M3, int NT, bool CAP>
@@ -1108,21 +748,7 @@ cudaError_t launch_cache(const CacheAttnProblem &p, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     kernel<<<(unsigned)main_ctas(p, C::kTokens), kThreads, C::kSmem, stream>>>(map_k, map_v, p, row_tiles, box_rows);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // the join is launched while the main kernel runs and waits for its end on
-    // the device, which hides its launch
-    cudaLaunchConfig_t cfg = {};
-    const bool many = main_ctas(p, C::kTokens) * kWarps >= pairs * kJoinMany;
-    const int live = (int)((int64_t)p.Q * p.G < C::kRows ? (int64_t)p.Q * p.G : C::kRows);
-    cfg.gridDim = dim3((unsigned)pairs, many ? live : 1, many ? D / 32 : 1);
-    cfg.blockDim = dim3(many ? kJoinThreads : 32 * C::kRows);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<D, C::kRows, C::kTokens>, p, row_tiles)
-                : cudaLaunchKernelEx(&cfg, cache_attention_join_few_kernel<D, C::kRows, C::kTokens>, p, row_tiles);
+    return launch_join<D, C::kRows, C::kTokens>(p, row_tiles, pairs, stream);
 }
 
 template <int D, bool E4M3>
@@ -1140,11 +766,13 @@ int step_tokens(const CacheAttnProblem &p, int cache_dtype) {
 }  // namespace
 
 int64_t cache_attention_workspace(const CacheAttnProblem &p, int cache_dtype) {
+    if (cache_dtype == FLEX_DTYPE_INT4) return cache_attention_int4_workspace(p);
     return workspace_partials(p.B) +
            2 * kWarps * main_ctas(p, step_tokens(p, cache_dtype)) * partial_floats(tile_rows(p), p.cache.D) * 4;
 }
 
 cudaError_t launch_cache_attention(const CacheAttnProblem &p, int cache_dtype, cudaStream_t stream) {
+    if (cache_dtype == FLEX_DTYPE_INT4) return launch_cache_attention_int4(p, stream);
     if (cache_dtype == FLEX_DTYPE_E4M3)
         return p.cache.D == 64 ? launch_cache_rows<64, true>(p, stream) : launch_cache_rows<128, true>(p, stream);
     return p.cache.D == 64 ? launch_cache_rows<64, false>(p, stream) : launch_cache_rows<128, false>(p, stream);

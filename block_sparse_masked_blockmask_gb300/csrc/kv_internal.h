@@ -74,6 +74,8 @@ cudaError_t launch_kv_append_packed(const AppendProblem &p, int src_dtype, int c
 cudaError_t launch_kv_append_int4(const AppendProblem &p, int src_dtype, cudaStream_t stream);
 cudaError_t launch_kv_read(const ReadProblem &p, int cache_dtype, int out_dtype, cudaStream_t stream);
 int64_t cache_attention_workspace(const CacheAttnProblem &p, int cache_dtype);  // bytes
+int64_t cache_attention_int4_workspace(const CacheAttnProblem &p);
+cudaError_t launch_cache_attention_int4(const CacheAttnProblem &p, cudaStream_t stream);
 cudaError_t launch_cache_attention(const CacheAttnProblem &p, int cache_dtype, cudaStream_t stream);
 
 // Angles are kept as turns in 64-bit fixed point: position * frequency wraps
