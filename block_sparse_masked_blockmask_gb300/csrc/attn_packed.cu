@@ -1,0 +1,104 @@
+// The plan of an attention over packed sequences, and the dispatch to its
+// kernels.
+//
+// A plan lists, for every sequence, its runs of two Q tiles (PlanEntry), those
+// with the most kv tiles first: the items that the attention's CTAs take last
+// are then short.  One CTA: it counts the entries of each length, adds the counts
+// up, and places the entries; entries of one length have no order, which no result depends on.  It
+// is made once for a batch and serves all its layers.
+#include <algorithm>
+
+#include "attn_packed_kernel.cuh"
+
+namespace flex {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kLengths = 1024;  // lengths told apart, in kv tiles (longer ones count as the longest)
+
+__global__ void __launch_bounds__(kPlanThreads)
+    packed_plan_kernel(const int32_t *q_starts, const int32_t *k_starts, int sequences, int total_q, int total_k, int tokens,
+                       PackedMask mask, PlanEntry *plan, int max_entries) {
+    __shared__ int at[kLengths], sums[kPlanThreads / 32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    at[threadIdx.x] = 0;
+    __syncthreads();
+    // a warp takes every 32nd sequence, or several share one
+    const int sharers = sequences >= kPlanThreads / 32 ? 1 : kPlanThreads / 32 / sequences, takers = kPlanThreads / 32 / sharers;
+    auto each = [&](auto &&f) {
+        if (warp / sharers >= takers) return;
+        for (int b = warp / sharers; b < sequences; b += takers) {
+            const int q0 = __ldg(q_starts + b), q1 = __ldg(q_starts + b + 1), k0 = __ldg(k_starts + b), k1 = __ldg(k_starts + b + 1);
+            if (q0 < 0 || q1 <= q0 || q1 > total_q) continue;  // no queries, or starts that do not ascend
+            const int k_len = k0 >= 0 && k1 > k0 && k1 <= total_k ? k1 - k0 : 0;
+            for (int t = ((warp % sharers) * 32 + lane) * 2 * tokens; t < q1 - q0; t += sharers * 32 * 2 * tokens) {
+                PlanEntry e = {q0 + t, q1 - q0 - t, k_len - (q1 - q0) + t, k0, k_len, {0, 0, 0}};
+                const ItemTiles n = packed_item_tiles(mask, e.pos, min(e.q_tokens, 2 * tokens), tokens, k_len);
+                f(kLengths - 1 - min(n.n_main + n.n_sink, kLengths - 1), e);
+            }
+        }
+    };
+    each([&](int bucket, const PlanEntry &) { atomicAdd(&at[bucket], 1); });
+    __syncthreads();
+    // from counts to first places
+    const int mine = at[threadIdx.x];
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    at[threadIdx.x] = before + upto - mine;
+    if (threadIdx.x == kPlanThreads - 1) {
+        PlanEntry head = {};
+        head.q_row = min(before + upto, max_entries);
+        plan[0] = head;
+    }
+    __syncthreads();
+    each([&](int bucket, const PlanEntry &e) {
+        const int i = atomicAdd(&at[bucket], 1);
+        if (i < max_entries) plan[1 + i] = e;  // starts that do not ascend may make more than fit
+    });
+}
+static_assert(kLengths == kPlanThreads, "a thread scans one length");
+
+}  // namespace
+
+cudaError_t launch_packed_plan(const int32_t *q_starts, const int32_t *k_starts, int sequences, int total_q, int total_k,
+                               int G, const PackedMask &mask, PlanEntry *plan, int max_entries, cudaStream_t stream) {
+    packed_plan_kernel<<<1, kPlanThreads, 0, stream>>>(q_starts, k_starts, sequences, total_q, total_k, packed_tile_tokens(G),
+                                                       mask, plan, max_entries);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_packed(const PackedProblem &p, cudaStream_t stream) {
+    PackedParams kp;
+    kp.G = p.Hq / p.Hk;
+    kp.tokens = packed_tile_tokens(kp.G);
+    kp.Hk = p.Hk;
+    kp.Hq = p.Hq;
+    kp.total_q = p.total_q;
+    // key heads scheduled together: as many as keep their K and V within 64 MB of L2
+    const int64_t kv_bytes = 4 * (int64_t)p.total_k * p.D;
+    kp.head_group = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t(64) << 20) / kv_bytes, p.Hk));
+    kp.plan = p.plan;
+    kp.mask = p.mask;
+    kp.scale = p.scale;
+    kp.score_param = p.score_param;
+    kp.v = static_cast<const uint16_t *>(p.v);
+    for (int i = 0; i < 2; ++i) {
+        kp.v_stride[i] = p.v_stride[i];
+        kp.out_stride[i] = p.out_stride[i];
+    }
+    kp.out = p.out;
+    kp.lse = p.lse;
+    kp.status = p.status;
+    kp.wide_out = (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.out_stride[0] * 2 | (uintptr_t)p.out_stride[1] * 2) % 32 == 0;
+    return p.D == 64 ? launch_packed_d64(p, kp, stream) : launch_packed_d128(p, kp, stream);
+}
+
+}  // namespace flex

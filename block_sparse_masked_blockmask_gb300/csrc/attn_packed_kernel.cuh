@@ -1,0 +1,890 @@
+// Attention over packed sequences with grouped query heads, bf16 on the tensor
+// cores: for token t of a sequence with n queries and m keys (position m - n + t)
+// and query head h, which reads key head h / G,
+//   s[kv] = score_mod(scale q.k[kv])  for the kv its mask keeps,
+//   out   = sum_kv exp(s[kv] - lse) v[kv],   lse = ln sum_kv exp(s[kv]).
+//
+// Bound by the tensor cores: 4 D flops per kept (row, key) pair, in whole tiles of
+// 128 rows x 128 keys.  The pipeline is that of attn_bf16_kernel.cuh (one
+// persistent CTA an SM; two Q tiles share the K/V tiles that TMA brings; S and O
+// in tensor memory; a softmax thread per row).  What differs:
+//  * A Q tile holds 128 / G tokens with the G query heads of one key head next to
+//    each other (one TMA box), so that few tokens fill a tile and a key head's K
+//    and V are read once for all its query heads.  Rows left over when G does not
+//    divide 128 hold whatever was in shared memory; rows are independent and these are
+//    not stored.
+//  * Work items come from a plan in device memory (tokens of one sequence, longest
+//    kv ranges first); which kv tiles an item needs follows from positions, so no
+//    lists are read.  Item i's CTA takes further items of CTAs that have not
+//    started (cluster launch control); items beyond the plan's count end it.
+//  * A tile of keys may reach into the next sequence: its columns are masked like
+//    those behind a row's position.  A masked column has weight 0, which a value
+//    that is not finite would turn into NaN; so in tiles that some row does not
+//    keep whole, the softmax warps look through the staged values before they hand
+//    over P (16 reads a thread at D = 128), zero what is not finite, and such an
+//    item's rows add those of them that they keep at the end.
+//  * lse to float32's accuracy: the row sum takes the weights before their
+//    rounding to bf16, softcap is not the hardware's tanh, and ALiBi's distances
+//    are whole numbers until they meet the slope.
+#pragma once
+
+#include "attn_bf16_kernel.cuh"
+#include "attn_packed.h"
+#include "softcap.cuh"
+
+namespace flex {
+
+struct PackedParams {
+    int G, tokens;          // query heads of a key head; tokens of a Q tile
+    int Hk, Hq, total_q, head_group;
+    const PlanEntry *plan;
+    PackedMask mask;
+    float scale, score_param;
+    const uint16_t *v;      // for values that are not finite
+    int64_t v_stride[2], out_stride[2];
+    uint16_t *out;
+    float *lse;
+    int *status;
+    int wide_out;           // out rows are 32-byte aligned
+};
+
+// One work item as the scheduler warp publishes it.
+struct PackedItem {
+    int nu;                  // kv tiles of both Q tiles; -1: no more work for this CTA
+    int n_main, hi, n_sink;  // of them hi, hi - 1, ... (n_main), then n_sink - 1, ... 0
+    int hk, q_row, q_tokens, pos, k_row, k_len;
+    int has1;
+    TileRange range[2];
+    volatile int odd;        // a value that is not finite was zeroed in a staged tile
+    __device__ __forceinline__ int tile(int u) const { return u < n_main ? hi - u : n_sink - 1 - (u - n_main); }
+    __device__ __forceinline__ bool present(int i, int c) const {
+        return (c >= range[i].lo && c <= range[i].hi) || c < range[i].sinks;
+    }
+};
+
+struct PackedMisc {
+    uint64_t q_full, q_empty, near_end;
+    uint64_t k_full[4], v_full[4], k_empty[4], v_empty[4];
+    uint64_t s_full[2], p_full[2], s_free[2], pv_done[2], o_full[2], drain[2];
+    uint64_t item_ready[2], item_free[2];
+    uint64_t clc_bar;
+    uint32_t tmem_base;
+    int abort;
+    alignas(16) uint32_t clc_resp[4];
+    PackedItem slot[2];
+};
+static_assert(offsetof(PackedMisc, clc_resp) % 16 == 0, "clc_resp alignment");
+
+template <int D>
+struct PackedCfg : Bf16Cfg<D> {
+    static constexpr uint32_t kSmemBytes = Bf16Cfg<D>::kMiscOff + sizeof(PackedMisc) + 1024;
+};
+
+__device__ __forceinline__ void record_failure(PackedMisc &ms, int *status) {
+    *reinterpret_cast<volatile int *>(&ms.abort) = 1;
+    atomicCAS(status, 0, kDeviceTimeout);
+}
+
+// The columns that a row keeps of a sequence: [lo, hi] and [0, sink]; none: all
+// are before 0.
+struct RowKeep {
+    int lo, hi, sink;
+};
+__device__ __forceinline__ RowKeep packed_keep(const PackedMask &m, int pos, int k_len) {
+    if (!m.causal) return {0, k_len - 1, -1};
+    if (pos < 0 || k_len == 0) return {0, -1, -1};
+    RowKeep r = {pos >= m.window ? pos - m.window + 1 : 0, min(pos, k_len - 1), min(m.sinks - 1, pos)};
+    if (r.lo <= r.sink + 1) r = {0, r.hi, -1};
+    return r;
+}
+// Whether rows of positions first .. last all keep the whole of kv tile c.
+__device__ __forceinline__ bool packed_full(const PackedMask &m, int first, int last, int k_len, int c) {
+    const int end = c * kBlock + kBlock - 1;
+    if (end >= k_len) return false;
+    return !m.causal || (end <= first && ((int64_t)c * kBlock > (int64_t)last - m.window || end < m.sinks));
+}
+
+__device__ __forceinline__ void apply_packed_mask(const RowKeep &r, int kv0, uint64_t (&x2)[64]) {
+    const int csink = r.sink - kv0, clo = r.lo - kv0, chi = r.hi - kv0;
+    const bool sink_here = csink >= 0, main_here = clo < kBlock && chi >= 0;
+    if (!__any_sync(0xffffffffu, sink_here && main_here)) {
+        const int a = sink_here ? 0 : clo, e = sink_here ? csink : chi;
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            x2[j] = keep_pair(x2[j], 2 * j >= a && 2 * j <= e, 2 * j + 1 >= a && 2 * j + 1 <= e);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            x2[j] = keep_pair(x2[j], 2 * j <= csink || (2 * j >= clo && 2 * j <= chi),
+                              2 * j + 1 <= csink || (2 * j + 1 >= clo && 2 * j + 1 <= chi));
+    }
+}
+
+// score_mod in base-2 units plus an addend A, two columns at a time, in order.
+template <int SCORE>
+struct PackedScore {
+    uint64_t k0, add2, slope2, far2;
+    float in, out;
+    __device__ __forceinline__ void init(const PackedParams &p, int h) {
+        const float a = p.scale * (SCORE == FLEX_SCORE_SOFTCAP ? 1.f : kLog2e);
+        k0 = f2_pack(a, a);
+        if constexpr (SCORE == FLEX_SCORE_SOFTCAP) {
+            in = fminf(2.f * kLog2e / p.score_param, FLT_MAX);
+            out = fminf(p.score_param * kLog2e, FLT_MAX);
+        }
+        if constexpr (SCORE == FLEX_SCORE_ALIBI) {
+            const float s = kLog2e * exp2f(-8.f * (float)(h + 1) / (float)p.Hq);
+            slope2 = f2_pack(s, s);
+        }
+    }
+    __device__ __forceinline__ void tile(int kv0, int pos, float a) {
+        add2 = f2_pack(a, a);
+        if constexpr (SCORE == FLEX_SCORE_ALIBI) far2 = f2_pack((float)(kv0 - pos), (float)(kv0 + 1 - pos));
+    }
+    __device__ __forceinline__ uint64_t pair(uint64_t s2) {
+        if constexpr (SCORE == FLEX_SCORE_SOFTCAP) {
+            float a, b;
+            f2_unpack(f2_mul(s2, k0), a, b);
+            return f2_add(f2_pack(softcap_log2(a, in, out), softcap_log2(b, in, out)), add2);
+        } else if constexpr (SCORE == FLEX_SCORE_ALIBI) {
+            const uint64_t x = f2_fma(s2, k0, f2_fma(far2, slope2, add2));
+            far2 = f2_add(far2, f2_pack(2.f, 2.f));
+            return x;
+        } else {
+            return f2_fma(s2, k0, add2);
+        }
+    }
+};
+
+// The largest magnitude's bits of the two bf16 of each word, and whether one is
+// an infinity or NaN.
+__device__ __forceinline__ uint32_t most_bf16x2(uint32_t most, uint32_t w) { return __vmaxu2(most, w & 0x7FFF7FFFu); }
+__device__ __forceinline__ bool odd_bf16x2(uint32_t most) {
+    return (most & 0x7FFFu) >= 0x7F80u || (most >> 16) >= 0x7F80u;
+}
+
+// Zero what is not finite in a staged tile of values (the 128 softmax threads of
+// a Q tile; those of the other one may do the same at the same time).
+template <int D>
+__device__ __forceinline__ void clean_values(uint8_t *tile, int t, volatile int *odd) {
+    constexpr int N = 128 * D * 2 / 16 / 128;  // 16-byte words of a thread
+    uint4 *v = reinterpret_cast<uint4 *>(tile);
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint4 w = v[i * 128 + t];
+        most = most_bf16x2(most_bf16x2(most_bf16x2(most_bf16x2(most, w.x), w.y), w.z), w.w);
+    }
+    if (!odd_bf16x2(most)) {
+        __threadfence_block();  // a zero that the other tile's thread wrote is seen after its flag
+        if (*odd) fence_proxy_async_smem();
+        return;
+    }
+    *odd = 1;
+    __threadfence_block();
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+        uint4 w = v[i * 128 + t];
+        uint32_t *e = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if ((e[j] & 0x7F80u) == 0x7F80u) e[j] &= 0xFFFF0000u;
+            if ((e[j] & 0x7F800000u) == 0x7F800000u) e[j] &= 0xFFFFu;
+        }
+        v[i * 128 + t] = w;
+    }
+    fence_proxy_async_smem();  // the MMAs read these generic-proxy writes
+}
+
+// Item `item` of the grid into `sl` (all lanes of the scheduler warp compute it).
+__device__ __forceinline__ void build_packed(const PackedParams &p, PackedItem &sl, int item, int count, int lane) {
+    // heads in groups whose K and V stay in L2; inside a group the plan's entries,
+    // longest first, the group's heads innermost
+    const int group_items = p.head_group * count;
+    const int g0 = item / group_items * p.head_group, r = item % group_items;
+    const int gsize = min(p.head_group, p.Hk - g0);
+    const int4 *e = reinterpret_cast<const int4 *>(p.plan + 1 + r / gsize);
+    const int4 a = __ldg(e), z = __ldg(e + 1);
+    const int k_len = z.x, pos = a.z, tokens = min(a.y, 2 * p.tokens);
+    const ItemTiles t = packed_item_tiles(p.mask, pos, tokens, p.tokens, k_len);
+    if (lane == 0) {
+        sl.n_main = t.n_main;
+        sl.hi = t.hi;
+        sl.n_sink = t.n_sink;
+        sl.nu = t.n_main + t.n_sink;
+        sl.hk = g0 + r % gsize;
+        sl.q_row = a.x;
+        sl.q_tokens = a.y;
+        sl.pos = pos;
+        sl.k_row = a.w;
+        sl.k_len = k_len;
+        sl.has1 = tokens > p.tokens;
+        sl.range[0] = t.range[0];
+        sl.range[1] = t.range[1];
+        sl.odd = 0;
+    }
+    __syncwarp();
+}
+
+template <int D, int SCORE>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, const PackedParams p) {
+    using C = PackedCfg<D>;
+    constexpr int NS = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    PackedMisc &ms = *reinterpret_cast<PackedMisc *>(smem + C::kMiscOff);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int count = __ldg(&p.plan->q_row), items = count * p.Hk;
+    if ((int)blockIdx.x >= items) return;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&ms.q_full, 1);
+        mbar_init(&ms.q_empty, C::kIssuers);
+        mbar_init(&ms.near_end, 1);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&ms.k_full[s], 1);
+            mbar_init(&ms.v_full[s], 1);
+            mbar_init(&ms.k_empty[s], C::kIssuers);
+            mbar_init(&ms.v_empty[s], C::kIssuers);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ms.s_full[i], 1);
+            mbar_init(&ms.p_full[i], 128);
+            mbar_init(&ms.s_free[i], 128);
+            mbar_init(&ms.pv_done[i], 1);
+            mbar_init(&ms.o_full[i], 1);
+            mbar_init(&ms.drain[i], 1);
+            mbar_init(&ms.item_ready[i], 1);
+            mbar_init(&ms.item_free[i], kItemConsumers);
+        }
+        mbar_init(&ms.clc_bar, 1);
+        ms.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ms.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = ms.tmem_base;
+    volatile int *abort_flag = &ms.abort;
+
+    if (warp >= 8) regs_decrease<kRegsControl>();
+    if (warp == kSchedWarp) {
+        // ----------------------------------------------------------- scheduler
+        // as in attn_bf16_kernel.cuh: item n goes to slot n % 2 once its item
+        // n - 2 is released, Q is loaded when the previous item's S MMAs are
+        // done, the next item is taken when the current one's last K tile is on
+        // the way
+        int item = blockIdx.x;
+        uint32_t nq = 0, nne = 0, nclc = 0;  // Q loads issued; near_end phases and responses consumed
+        bool ok = true;
+        const uint32_t q_bytes = (uint32_t)(p.tokens * p.G) * 128u * C::kAtoms;  // of one Q tile
+        if (lane == 0) prefetch_tensormap(&tmap_q);
+        for (uint32_t n = 0;; ++n) {
+            const int k = (int)(n & 1u);
+            PackedItem &sl = ms.slot[k];
+            if (n >= 2 && !warp_wait(&ms.item_free[k], ((n - 2) >> 1) & 1u, abort_flag)) {
+                ok = false;
+                break;
+            }
+            if (item >= items) item = -1;
+            if (item >= 0) {
+                build_packed(p, sl, item, count, lane);
+            } else if (lane == 0) {
+                sl.nu = -1;
+            }
+            __threadfence_block();
+            __syncwarp();
+            const int nu = sl.nu;
+            if (lane == 0) mbar_arrive(&ms.item_ready[k]);
+            if (item < 0) break;
+            if (nu > 0) {
+                const int has1 = sl.has1;
+                if (nq > 0 && !warp_wait(&ms.q_empty, (nq - 1) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&ms.q_full, (has1 ? 2u : 1u) * q_bytes);
+                    for (int a = 0; a < C::kAtoms; ++a)
+                        for (int i = 0; i <= has1; ++i)
+                            tma_load_3d(smem + C::kQOff + i * C::kTileBytes + a * C::kAtomBytes, &tmap_q, &ms.q_full, 64 * a,
+                                        sl.hk * p.G, sl.q_row + i * p.tokens);
+                }
+                ++nq;
+                if (!warp_wait(&ms.near_end, nne & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                ++nne;
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&ms.clc_bar, 16u);
+                clc_try_cancel(ms.clc_resp, &ms.clc_bar);
+            }
+            if (!warp_wait(&ms.clc_bar, nclc & 1u, abort_flag)) {
+                ok = false;
+                break;
+            }
+            ++nclc;
+            int next = 0;
+            if (lane == 0) next = clc_cancelled_x(ms.clc_resp);
+            item = __shfl_sync(0xffffffffu, next, 0);
+        }
+        if (!ok && lane == 0) record_failure(ms, p.status);
+        // every Q copy issued above lands before the CTA exits
+        if (lane == 0 && nq > 0) drain_wait(&ms.q_full, (nq - 1) & 1u);
+        __syncwarp();
+    } else if (warp == kTmaWarp || (!C::kSepP && warp == kTmaVWarp)) {
+        // ----------------------------------------------------- TMA producers
+        // D = 128: warp 8 loads K, warp 10 V; D = 64: warp 8 both
+        if (lane == 0) {
+            const bool does_k = warp == kTmaWarp, does_v = C::kSepP || warp == kTmaVWarp;
+            if (does_k) prefetch_tensormap(&tmap_k);
+            if (does_v) prefetch_tensormap(&tmap_v);
+            uint32_t g = 0;  // steps issued over all items
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                const int k = (int)(n & 1u);
+                const PackedItem &sl = ms.slot[k];
+                if (!mbar_wait(&ms.item_ready[k], (n >> 1) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const int nu = sl.nu;
+                if (nu < 0) break;
+                const int hk = sl.hk, k_row = sl.k_row;
+                for (int u = 0; u < nu; ++u, ++g) {
+                    const int s = (int)(g % NS);
+                    const uint32_t use = g / NS;
+                    const int row = k_row + sl.tile(u) * kBlock;
+                    uint8_t *dst = smem + C::kKvOff + s * C::kStageBytes;
+                    if (does_k) {
+                        if (use > 0 && !mbar_wait(&ms.k_empty[s], (use - 1) & 1u, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&ms.k_full[s], C::kTileBytes);
+                        for (int a = 0; a < C::kAtoms; ++a)
+                            tma_load_3d(dst + a * C::kAtomBytes, &tmap_k, &ms.k_full[s], 64 * a, row, hk);
+                    }
+                    if (does_v) {
+                        if (use > 0 && !mbar_wait(&ms.v_empty[s], (use - 1) & 1u, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&ms.v_full[s], C::kTileBytes);
+                        for (int a = 0; a < C::kAtoms; ++a)
+                            tma_load_3d(dst + C::kTileBytes + a * C::kAtomBytes, &tmap_v, &ms.v_full[s], 64 * a, row, hk);
+                    }
+                }
+                if (ok && does_k && nu > 0) mbar_arrive(&ms.near_end);
+                if (ok) mbar_arrive(&ms.item_free[k]);
+            }
+            if (!ok) record_failure(ms, p.status);
+            // Drain: every copy issued above lands before the CTA exits (a step
+            // that gave up between its K and its V has none of the latter).
+            for (uint32_t s = 0; s < (uint32_t)NS && s < g; ++s) {
+                const uint32_t last = s + ((g - 1 - s) / NS) * NS;
+                if (does_k) drain_wait(&ms.k_full[s], (last / NS) & 1u);
+                if (does_v) drain_wait(&ms.v_full[s], (last / NS) & 1u);
+            }
+            if (!ok && C::kSepP) drain_wait(&ms.k_full[g % NS], (g / NS) & 1u);
+        }
+        __syncwarp();
+    } else if (C::kSepP && (warp == kMmaWarp || warp == kTmaVWarp)) {
+        // ------------------------------------------- MMA issuers (D = 64)
+        // one thread per Q tile, S two steps ahead of PV
+        if (lane == 0) {
+            const int ti = warp == kMmaWarp ? 0 : 1;
+            constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1);
+            constexpr uint32_t kHi = smem_desc_hi_sw128(1024);
+            const uint32_t kv_lo0 = smem_desc_lo(smem_u32(smem + C::kKvOff), 16);
+            const uint32_t v_lo0 = smem_desc_lo(smem_u32(smem + C::kKvOff + C::kTileBytes), C::kAtomBytes);
+            const uint32_t qa = smem_desc_lo(smem_u32(smem + C::kQOff + ti * C::kTileBytes), 16);
+            uint32_t s_total = 0, pv_total = 0;  // this tile's S and PV groups over all items
+            auto issue_s = [&](int s) -> bool {
+                if (s_total > 0 && !mbar_wait(&ms.s_free[ti], (s_total - 1) & 1u, abort_flag)) return false;
+                tc_fence_after_sync();
+                ++s_total;
+                const uint32_t ka = kv_lo0 + ((s * C::kStageBytes) >> 4);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k / 4) * C::kAtomBytes + (k % 4) * 32) >> 4;
+                    mma_ss_lo<kHi, kHi>(tmem + C::s_col(ti), qa + off, ka + off, idesc_s, k > 0 ? 1u : 0u);
+                }
+                mma_commit(&ms.s_full[ti]);
+                return true;
+            };
+            auto issue_pv = [&](int s, bool acc) -> bool {
+                if (!mbar_wait(&ms.p_full[ti], pv_total & 1u, abort_flag)) return false;
+                tc_fence_after_sync();
+                const uint32_t va = v_lo0 + ((s * C::kStageBytes) >> 4);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts_lo<kHi>(tmem + C::o_col(ti), tmem + C::p_col(ti) + k * 8, va + ((k * 2048) >> 4), idesc_o,
+                                   (k > 0 || acc) ? 1u : 0u);
+                mma_commit(&ms.pv_done[ti]);
+                ++pv_total;
+                return true;
+            };
+            uint32_t g = 0, nq = 0;
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                const int k = (int)(n & 1u);
+                const PackedItem &sl = ms.slot[k];
+                if (!mbar_wait(&ms.item_ready[k], (n >> 1) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const int nu = sl.nu;
+                if (nu < 0) break;
+                if (nu > 0) {
+                    auto present = [&](int u) { return sl.present(ti, sl.tile(u)); };
+                    ok = mbar_wait(&ms.q_full, nq & 1u, abort_flag);
+                    tc_fence_after_sync();
+                    for (int u = 0; ok && u < min(nu, 2); ++u) {
+                        const uint32_t gu = g + (uint32_t)u;
+                        const int s = (int)(gu % NS);
+                        ok = mbar_wait(&ms.k_full[s], (gu / NS) & 1u, abort_flag) && (!present(u) || issue_s(s));
+                        mma_commit(&ms.k_empty[s]);
+                        if (u + 1 == nu) mma_commit(&ms.q_empty);  // the item's last S is issued
+                    }
+                    uint32_t pv_item = 0;
+                    for (int u = 0; ok && u < nu; ++u) {
+                        const uint32_t gu = g + (uint32_t)u;
+                        const int s = (int)(gu % NS);
+                        if (!mbar_wait(&ms.v_full[s], (gu / NS) & 1u, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        if (present(u)) {
+                            if (!issue_pv(s, pv_item > 0)) {
+                                ok = false;
+                                break;
+                            }
+                            ++pv_item;
+                        }
+                        mma_commit(&ms.v_empty[s]);
+                        if (u + 2 < nu) {
+                            const uint32_t g2 = gu + 2;
+                            const int s2 = (int)(g2 % NS);
+                            if (!mbar_wait(&ms.k_full[s2], (g2 / NS) & 1u, abort_flag) || (present(u + 2) && !issue_s(s2))) {
+                                ok = false;
+                                break;
+                            }
+                            mma_commit(&ms.k_empty[s2]);
+                            if (u + 3 == nu) mma_commit(&ms.q_empty);
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(&ms.o_full[ti]);
+                    g += (uint32_t)nu;
+                    ++nq;
+                }
+                mbar_arrive(&ms.item_free[k]);
+            }
+            if (!ok) record_failure(ms, p.status);
+            mma_commit(&ms.drain[ti]);  // every MMA issued above completes before TMEM is freed
+            drain_wait(&ms.drain[ti], 0);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------- MMA issuer (D = 128)
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1);
+            constexpr uint32_t kHi = smem_desc_hi_sw128(1024);
+            uint32_t pv_total[2] = {0u, 0u}, pv_item[2] = {0u, 0u};
+            const uint32_t kv_lo0 = smem_desc_lo(smem_u32(smem + C::kKvOff), 16);
+            const uint32_t v_lo0 = smem_desc_lo(smem_u32(smem + C::kKvOff + C::kTileBytes), C::kAtomBytes);
+            const uint32_t q_lo0 = smem_desc_lo(smem_u32(smem + C::kQOff), 16);
+            auto issue_s = [&](int i, int s) {
+                const uint32_t qa = q_lo0 + ((i * C::kTileBytes) >> 4);
+                const uint32_t ka = kv_lo0 + ((s * C::kStageBytes) >> 4);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k / 4) * C::kAtomBytes + (k % 4) * 32) >> 4;
+                    mma_ss_lo<kHi, kHi>(tmem + C::s_col(i), qa + off, ka + off, idesc_s, k > 0 ? 1u : 0u);
+                }
+                mma_commit(&ms.s_full[i]);
+            };
+            auto issue_pv = [&](int i, int s) -> bool {
+                const uint32_t va = v_lo0 + ((s * C::kStageBytes) >> 4);
+                const uint32_t acc = pv_item[i] > 0 ? 1u : 0u;
+                if (!mbar_wait(&ms.p_full[i], pv_total[i] & 1u, abort_flag)) return false;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts_lo<kHi>(tmem + C::o_col(i), tmem + C::s_col(i) + k * 8, va + ((k * 2048) >> 4), idesc_o,
+                                   (k > 0 || acc) ? 1u : 0u);
+                ++pv_total[i];
+                ++pv_item[i];
+                return true;
+            };
+            uint32_t g = 0, nq = 0;
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                const int k = (int)(n & 1u);
+                const PackedItem &sl = ms.slot[k];
+                if (!mbar_wait(&ms.item_ready[k], (n >> 1) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const int nu = sl.nu;
+                if (nu < 0) break;
+                if (nu > 0) {
+                    // which Q tiles a step is for: bits 0 and 1
+                    auto flags = [&](int u) {
+                        const int c = sl.tile(u);
+                        return (sl.present(0, c) ? 1u : 0u) | (sl.present(1, c) ? 2u : 0u);
+                    };
+                    pv_item[0] = pv_item[1] = 0u;
+                    const int s0 = (int)(g % NS);
+                    ok = mbar_wait(&ms.q_full, nq & 1u, abort_flag) &&
+                         mbar_wait(&ms.k_full[s0], (g / NS) & 1u, abort_flag);
+                    tc_fence_after_sync();
+                    uint32_t f = flags(0);
+                    if (ok) {
+                        if (f & 1u) issue_s(0, s0);
+                        if (f & 2u) issue_s(1, s0);
+                        mma_commit(&ms.k_empty[s0]);
+                        if (nu == 1) mma_commit(&ms.q_empty);  // Q no longer read
+                    }
+                    for (int u = 0; ok && u < nu; ++u) {
+                        const uint32_t gu = g + (uint32_t)u;
+                        const int s = (int)(gu % NS);
+                        const bool nxt = u + 1 < nu;
+                        const int s1 = (int)((gu + 1) % NS);
+                        const uint32_t f1 = nxt ? flags(u + 1) : 0u;
+                        if (!mbar_wait(&ms.v_full[s], (gu / NS) & 1u, abort_flag) ||
+                            (nxt && !mbar_wait(&ms.k_full[s1], ((gu + 1) / NS) & 1u, abort_flag))) {
+                            ok = false;
+                            break;
+                        }
+                        if ((f & 1u) && !issue_pv(0, s)) {
+                            ok = false;
+                            break;
+                        }
+                        if (f1 & 1u) issue_s(0, s1);
+                        if ((f & 2u) && !issue_pv(1, s)) {
+                            ok = false;
+                            break;
+                        }
+                        mma_commit(&ms.v_empty[s]);
+                        if (nxt) {
+                            if (f1 & 2u) issue_s(1, s1);
+                            mma_commit(&ms.k_empty[s1]);
+                            if (u + 2 == nu) mma_commit(&ms.q_empty);  // the item's last S is issued
+                        }
+                        f = f1;
+                    }
+                    if (!ok) break;
+                    mma_commit(&ms.o_full[0]);
+                    g += (uint32_t)nu;
+                    ++nq;
+                }
+                mbar_arrive(&ms.item_free[k]);
+            }
+            if (!ok) record_failure(ms, p.status);
+            mma_commit(&ms.drain[0]);  // every MMA issued above completes before TMEM is freed
+            drain_wait(&ms.drain[0], 0);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ----------------------------------------------------------- softmax
+        regs_increase<kRegsSoftmax>();
+        const int i = warp / 4;
+        const int t = threadIdx.x % 128;
+        const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + C::s_col(i);
+        const uint32_t p_addr = tmem + lane_base + C::p_col(i);
+        const uint32_t o_addr = tmem + lane_base + C::o_col(i);
+        const int token_in = t / p.G, head_in = t % p.G;  // of this thread's row
+        uint32_t cnt_total = 0, g = 0, nq = 0;
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+          const int k = (int)(n & 1u);
+          PackedItem &sl = ms.slot[k];
+          if (!warp_wait(&ms.item_ready[k], (n >> 1) & 1u, abort_flag)) {
+              ok = false;
+              break;
+          }
+          const int nu = sl.nu;
+          if (nu < 0) break;
+          const bool valid = i == 0 || sl.has1;
+          const int token = i * p.tokens + token_in, h = sl.hk * p.G + head_in;
+          const bool live_row = token_in < p.tokens && token < sl.q_tokens;
+          const int pos = sl.pos + token, k_len = sl.k_len;
+          // positions of the tile's rows, and of the other tile's
+          const int first = sl.pos + i * p.tokens, last = sl.pos + min((i + 1) * p.tokens, sl.q_tokens) - 1;
+          RowKeep keep = packed_keep(p.mask, pos, k_len);
+          if (!live_row) keep = {0, -1, -1};
+          // whether some row of the item's tiles does not keep the whole of kv tile c that its tile needs
+          auto touched = [&](int c) {
+              if (!packed_full(p.mask, first, last, k_len, c)) return true;
+              const int f1 = sl.pos + (1 - i) * p.tokens, l1 = sl.pos + min((2 - i) * p.tokens, sl.q_tokens) - 1;
+              return (i == 1 || sl.has1) && sl.present(1 - i, c) && !packed_full(p.mask, f1, l1, k_len, c);
+          };
+          PackedScore<SCORE> score;
+          score.init(p, h);
+          // see attn_bf16_kernel.cuh for the finite floor of the running max and
+          // the shift that the scores carry
+          float m_run = -FLT_MAX, l_run = 0.f;
+          uint32_t cnt = 0;
+          if (valid) {
+            for (int u = 0; u < nu; ++u) {
+                const int c = sl.tile(u);
+                if (!sl.present(i, c)) continue;
+                const int kv0 = c * kBlock;
+                if (!warp_wait(&ms.s_full[i], cnt_total & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const float a_shift = m_run > -FLT_MAX ? -m_run : 0.f;
+                uint64_t x2[64];
+                {
+                    uint32_t r[128];
+                    tmem_ld128_sync(s_addr, r);
+                    if constexpr (C::kSepP) {
+                        tc_fence_before_sync();
+                        mbar_arrive(&ms.s_free[i]);  // S_i may be overwritten by the next S MMA
+                    }
+                    score.tile(kv0, pos, a_shift);
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        x2[j] = score.pair(f2_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+                }
+                if (!packed_full(p.mask, first, last, k_len, c)) apply_packed_mask(keep, kv0, x2);
+                float mx[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float lo, hi;
+                    f2_unpack(x2[k], lo, hi);
+                    mx[k] = fmaxf(lo, hi);
+                }
+#pragma unroll
+                for (int j = 8; j < 64; ++j) {
+                    float lo, hi;
+                    f2_unpack(x2[j], lo, hi);
+                    mx[j & 7] = fmax3(mx[j & 7], lo, hi);
+                }
+                const float m_tile =
+                    fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) - a_shift;
+                float alpha = 1.f;
+                if (m_tile > m_run + kRescaleThreshold) {  // always taken at the row's first live tile
+                    alpha = ex2_approx(m_run - m_tile);
+                    m_run = m_tile;
+                }
+                const float shift = -m_run - a_shift;
+                if (__any_sync(0xffffffffu, shift != 0.f)) {
+                    const uint64_t shift2 = f2_pack(shift, shift);
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) x2[j] = f2_add(x2[j], shift2);
+                }
+                if (touched(c)) {  // masked columns meet no value that is not finite
+                    const uint32_t gu = g + (uint32_t)u;
+                    const int stage = (int)(gu % NS);
+                    if (!warp_wait(&ms.v_full[stage], (gu / NS) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    clean_values<D>(smem + C::kKvOff + stage * C::kStageBytes + C::kTileBytes, t, &sl.odd);
+                }
+                auto rescale_o = [&]() {
+                    if (cnt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32_sync(o_addr + c0, o);
+                            const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float lo, hi;
+                                f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1])), a2),
+                                          lo, hi);
+                                o[2 * j] = __float_as_uint(lo);
+                                o[2 * j + 1] = __float_as_uint(hi);
+                            }
+                            tmem_st32(o_addr + c0, o);
+                        }
+                    }
+                };
+                uint64_t rsum2[2] = {0, 0};
+                auto weights = [&](int j) {
+                    float d0, d1;
+                    f2_unpack(x2[j], d0, d1);
+                    d0 = ex2_approx(d0);
+                    d1 = ex2_approx(d1);
+                    rsum2[j & 1] = f2_add(rsum2[j & 1], f2_pack(d0, d1));
+                    return pack_bf16x2(d0, d1);
+                };
+                if constexpr (C::kSepP) {
+                    uint32_t pk[64];
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) pk[j] = weights(j);
+                    if (cnt_total > 0 && !warp_wait(&ms.pv_done[i], (cnt_total - 1) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    rescale_o();
+#pragma unroll
+                    for (int gq = 0; gq < 4; ++gq)
+                        tmem_st16(p_addr + 16 * gq, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * gq]));
+                } else {
+                    rescale_o();
+#pragma unroll
+                    for (int gq = 0; gq < 4; ++gq) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int t2 = 0; t2 < 16; ++t2) pk[t2] = weights(16 * gq + t2);
+                        tmem_st16(p_addr + 16 * gq, pk);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before_sync();
+                mbar_arrive(&ms.p_full[i]);
+                float r0, r1, r2, r3;
+                f2_unpack(rsum2[0], r0, r1);
+                f2_unpack(rsum2[1], r2, r3);
+                l_run = fmaf(l_run, alpha, (r0 + r1) + (r2 + r3));
+                ++cnt;
+                ++cnt_total;
+            }
+            // ---------------------------------------------------- epilogue
+            bool have = ok && cnt > 0;
+            if (have && !warp_wait(&ms.o_full[C::kSepP ? i : 0], nq & 1u, abort_flag)) {
+                have = false;
+                ok = false;
+            }
+            if (!ok) record_failure(ms, p.status);
+            if (ok) {
+                tc_fence_after_sync();
+                __threadfence_block();
+                const bool odd = sl.odd != 0;
+                const int64_t row = sl.q_row + token;
+                uint16_t *dst = p.out + h * p.out_stride[0] + row * p.out_stride[1];
+                const bool kept = have && l_run != 0.f;  // NaN stays
+                const float inv = kept ? 1.f / l_run : 0.f;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    if (have) {
+                        tmem_ld32_sync(o_addr + c0, o);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+                    }
+                    float x[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = kept ? __uint_as_float(o[j]) * inv : 0.f;
+                    if (odd && live_row) {
+                        // the values that were zeroed, of the columns that this row keeps
+#pragma unroll 1
+                        for (int u = 0; u < nu; ++u) {
+                            const int c = sl.tile(u);
+                            if (!sl.present(i, c) || !touched(c)) continue;
+#pragma unroll 1
+                            for (int kv = c * kBlock; kv < (c + 1) * kBlock && kv < k_len; ++kv) {
+                                if (!((kv >= keep.lo && kv <= keep.hi) || kv <= keep.sink)) continue;
+                                const uint16_t *src = p.v + sl.hk * p.v_stride[0] + (sl.k_row + (int64_t)kv) * p.v_stride[1] + c0;
+#pragma unroll
+                                for (int j = 0; j < 32; j += 8) {
+                                    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + j));
+                                    const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                    for (int z = 0; z < 4; ++z) {
+                                        if ((e[z] & 0x7F80u) == 0x7F80u) x[j + 2 * z] += __uint_as_float(e[z] << 16);
+                                        if ((e[z] & 0x7F800000u) == 0x7F800000u)
+                                            x[j + 2 * z + 1] += __uint_as_float(e[z] & 0xFFFF0000u);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+                    if (live_row) {
+                        if (p.wide_out) {  // whole 32-byte sectors per store
+                            st_global_32B(dst + c0, &pk[0]);
+                            st_global_32B(dst + c0 + 16, &pk[8]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                *reinterpret_cast<uint4 *>(dst + c0 + 8 * j) =
+                                    make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                        }
+                    }
+                }
+                if (live_row) p.lse[(int64_t)h * p.total_q + row] = kept ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+            }
+          }
+          if (nu > 0) {
+              g += (uint32_t)nu;
+              ++nq;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.item_free[k]);
+        }
+        if (!ok) record_failure(ms, p.status);
+    }
+
+    // ---------------------------------------------------------- teardown
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, int SCORE>
+cudaError_t launch_packed_kernel(const PackedProblem &p, const PackedParams &kp, cudaStream_t stream) {
+    using C = PackedCfg<D>;
+    CUtensorMap tq, tk, tv;
+    const uint64_t qd[3] = {D, (uint64_t)p.Hq, (uint64_t)p.total_q}, qs[2] = {(uint64_t)p.q_stride[0] * 2, (uint64_t)p.q_stride[1] * 2};
+    const uint32_t qb[3] = {64, (uint32_t)kp.G, (uint32_t)kp.tokens};
+    const uint64_t kd[3] = {D, (uint64_t)p.total_k, (uint64_t)p.Hk}, ks[2] = {(uint64_t)p.k_stride[1] * 2, (uint64_t)p.k_stride[0] * 2},
+                   vs[2] = {(uint64_t)p.v_stride[1] * 2, (uint64_t)p.v_stride[0] * 2};
+    const uint32_t kb[3] = {64, (uint32_t)kBlock, 1};
+    if (!make_tile_map_3d(&tq, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tile_map_3d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tile_map_3d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kd, vs, kb, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    auto kernel = attn_packed_kernel<D, SCORE>;
+    // the register split assumes exactly kRegsAtLaunch registers at launch
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != (int)kRegsAtLaunch) return cudaErrorInvalidDeviceFunction;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(p.max_entries * p.Hk), kAttnThreads, C::kSmemBytes, stream>>>(tq, tk, tv, kp);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_packed_dim(const PackedProblem &p, const PackedParams &kp, cudaStream_t stream) {
+    switch (p.score_kind) {
+        case FLEX_SCORE_SOFTCAP:
+            return launch_packed_kernel<D, FLEX_SCORE_SOFTCAP>(p, kp, stream);
+        case FLEX_SCORE_ALIBI:
+            return launch_packed_kernel<D, FLEX_SCORE_ALIBI>(p, kp, stream);
+        default:
+            return launch_packed_kernel<D, FLEX_SCORE_IDENTITY>(p, kp, stream);
+    }
+}
+
+cudaError_t launch_packed_d64(const PackedProblem &p, const PackedParams &kp, cudaStream_t stream);
+cudaError_t launch_packed_d128(const PackedProblem &p, const PackedParams &kp, cudaStream_t stream);
+
+}  // namespace flex

@@ -11,6 +11,7 @@
 
 #include "kv_internal.h"
 #include "ptx.cuh"
+#include "softcap.cuh"
 
 namespace flex {
 namespace {
@@ -20,7 +21,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kJoinThreads = 512;
 constexpr int kJoinMany = 8;       // warps of the main launch per pair, from which CTAs join a row
 constexpr int kMaxCtas = 152 * 2;  // of the main launch: two on every SM
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = kLog2eF;
 constexpr float kLn2 = 0.6931471805599453f;
 // Entering and finishing a (sequence, head, row tile) costs a warp the time of
 // some steps: the list counts that many units more for each (512 pairs, ragged
@@ -41,21 +42,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-// cap tanh(u), u = s / cap, in base-2 units.  From |u| = 1/4 on as cap (1 - 2 / (1
-// + e^(2 u))), which is within 2^-22 cap: about 2^-20 of the result, but nothing
-// of it where u is small.  There the Taylor series to u^9, which leaves out less
-// than 2^-26 of it.  Together a tenth of tanhf's instructions.
-// in = 2 log2(e) / cap, out = cap log2(e), both finite.
-__device__ __forceinline__ float softcap_log2(float s, float in, float out) {
-    constexpr double k = 0.69314718055994530942 * 0.69314718055994530942 / 4;  // u^2 = k z^2
-    const float z = s * in, t = z * z;
-    float near = fmaf(t, (float)(62. / 2835 * k * k * k * k), (float)(-17. / 315 * k * k * k));
-    near = fmaf(t, near, (float)(2. / 15 * k * k));
-    near = fmaf(t, near, (float)(-1. / 3 * k));
-    near = fmaf(t, near, 1.f) * (s * kLog2e);
-    const float far = fmaf(out, -2.f * rcp_approx(1.f + ex2_approx(z)), out);
-    return fabsf(z) < 0.5f * kLog2e ? near : far;
 }
 // 8 x 8 transpose of 16-bit values across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {

@@ -56,7 +56,8 @@ EXPORTED = ("flex_block_mask_sizes", "flex_block_mask_sizes_qkv", "flex_block_ma
             "flex_attention_fwd_opts", "flex_attention_bwd", "flex_attention_fwd_noalloc", "flex_attention_fwd_host", "flex_device_status",
             "flex_selftest_wait_timeout", "flex_status_string", "flex_rope_frequencies", "flex_rope_fwd", "flex_rope_bwd",
             "flex_kv_cache_append", "flex_kv_cache_append_packed", "flex_kv_cache_read",
-            "flex_kv_cache_attention", "flex_kv_cache_attention_workspace")
+            "flex_kv_cache_attention", "flex_kv_cache_attention_workspace",
+            "flex_packed_plan_bytes", "flex_packed_plan_create", "flex_attention_packed_fwd")
 
 
 class FlexError(RuntimeError):
@@ -106,6 +107,12 @@ class flex_kv_cache(ctypes.Structure):
                 ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class flex_packed_plan(ctypes.Structure):
+    _fields_ = [("sequences", ctypes.c_int32), ("total_q", ctypes.c_int32), ("total_k", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("mask_kind", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("entries", ctypes.c_void_p)]
 
 
 class flex_device_buffers(ctypes.Structure):
@@ -191,6 +198,14 @@ def load_library():
             lib.flex_kv_cache_attention.restype = ctypes.c_int
             lib.flex_kv_cache_attention_workspace.argtypes = [tp, cp, i32, i32, ctypes.POINTER(flex_mask_params), i64p]
             lib.flex_kv_cache_attention_workspace.restype = ctypes.c_int
+            pp = ctypes.POINTER(flex_packed_plan)
+            lib.flex_packed_plan_bytes.argtypes = [i32, i32, i32, i32, i64p]
+            lib.flex_packed_plan_bytes.restype = ctypes.c_int
+            lib.flex_packed_plan_create.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32,
+                                                    ctypes.POINTER(flex_mask_params), pp, vp]
+            lib.flex_packed_plan_create.restype = ctypes.c_int
+            lib.flex_attention_packed_fwd.argtypes = [tp, tp, tp, pp, i32, ctypes.c_float, ctypes.c_float, tp, vp, vp]
+            lib.flex_attention_packed_fwd.restype = ctypes.c_int
             lib.flex_status_string.argtypes = [ctypes.c_int]
             lib.flex_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -852,6 +867,83 @@ def flex_kv_cache_attention_workspace(q: torch.Tensor, cache: KVCache, max_pages
     if q.dim() != 4:
         raise ValueError("q must be a [B, Hq, Q, D] tensor")
     return _cache_workspace_bytes(q.shape, cache.shape, cache.struct.dtype, max_pages, mask_kind, window, sinks)
+
+
+class PackedPlan:
+    """The plan of a batch of packed sequences: the C struct plus the tensor that owns its entries."""
+
+    def __init__(self, struct: flex_packed_plan, entries: torch.Tensor):
+        self.struct, self.entries = struct, entries
+        self._ref = ctypes.byref(struct)
+
+
+def flex_packed_plan_bytes(sequences: int, total_q: int, Hq: int, Hk: int) -> int:
+    """Bytes of a plan's entries."""
+    size = ctypes.c_int64()
+    rc = load_library().flex_packed_plan_bytes(sequences, total_q, Hq, Hk, ctypes.byref(size))
+    if rc != FLEX_OK:
+        raise FlexError(rc, "flex_packed_plan_bytes")
+    return size.value
+
+
+def flex_packed_plan_create(q_starts: torch.Tensor, k_starts: torch.Tensor | None, total_q: int, total_k: int | None,
+                            Hq: int, Hk: int, mask_kind: int = FLEX_MASK_CAUSAL, window: int = 0, sinks: int = 0,
+                            stream=None) -> PackedPlan:
+    """Plan of a batch of packed sequences for flex_attention_packed_fwd (asynchronous on `stream`, in its pool's memory).
+
+    Sequence b has tokens q_starts[b] .. q_starts[b + 1] - 1 of q (total_q tokens, Hq heads), and k_starts[b] ..
+    k_starts[b + 1] - 1 of k and v (total_k tokens, Hk heads; None: the same as q's).  Both int32 [sequences + 1],
+    ascending; they are not needed any more once `stream` has passed the call.  With more keys than queries the queries
+    are the last tokens.
+    """
+    device = q_starts.device
+    qs, sequences = _starts(q_starts, device)
+    if k_starts is None:
+        if total_k is not None and total_k != total_q:
+            raise ValueError("total_k without k_starts")
+        ks, total_k = qs, total_q
+    else:
+        if total_k is None:
+            raise ValueError("k_starts without total_k")
+        ks = _device_array(k_starts, "k_starts", torch.int32, device, (sequences + 1,))
+    entries = _empty((flex_packed_plan_bytes(sequences, total_q, Hq, Hk),), torch.uint8, device, stream)
+    plan = flex_packed_plan(entries=entries.data_ptr())
+    rc = _call(device, load_library().flex_packed_plan_create, qs, ks, sequences, total_q, total_k, Hq, Hk, mask_kind,
+               ctypes.byref(_mask_params(mask_kind, window, 0, sinks)), ctypes.byref(plan), _stream_handle(stream, device))
+    if rc != FLEX_OK:
+        raise FlexError(rc, "flex_packed_plan_create")
+    return PackedPlan(plan, entries)
+
+
+def flex_attention_packed_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: PackedPlan,
+                              score_kind: int = FLEX_SCORE_IDENTITY, score_param: float = 0.0, scale: float | None = None,
+                              out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """Attention over the packed sequences of a plan: q [1, Hq, total_q, D], k and v [1, Hk, total_k, D], bf16 with any
+    strides (a projection's [tokens, heads, D] is passed transposed); returns (out, lse).
+
+    out [1, Hq, total_q, D] may have any strides; one that is not given has a token's heads next to each other in
+    memory.  lse: contiguous float32 [1, Hq, total_q].  What is not given is allocated from `stream`'s pool.
+    Asynchronous on `stream`.
+    """
+    device, shape = plan.entries.device, q.shape
+    for x in (q, k, v):
+        if x.device != device:
+            raise ValueError("q, k and v must be on the plan's device")
+    tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
+    if out is None:
+        out = _empty((shape[0], shape[2], shape[1], shape[3]), q.dtype, device, stream).transpose(1, 2)
+    elif out.device != device:
+        raise ValueError("out must be on the plan's device")
+    if lse is None:
+        lse = _empty(shape[:3], torch.float32, device, stream)
+    else:
+        _device_array(lse, "lse", torch.float32, device, shape[:3])
+    rc = _call(device, load_library().flex_attention_packed_fwd, tq, tk, tv, plan._ref, score_kind, float(score_param),
+               shape[3] ** -0.5 if scale is None else float(scale), _tensor(out), lse.data_ptr(),
+               _stream_handle(stream, device))
+    if rc != FLEX_OK:
+        raise FlexError(rc, "flex_attention_packed_fwd")
+    return out, lse
 
 
 def flex_selftest_wait_timeout(limit_ms: int = 50, stream=None, device=None) -> None:

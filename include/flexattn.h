@@ -17,6 +17,9 @@
  *   flex_kv_cache_append_packed        the same for packed sequences
  *   flex_kv_cache_read                 the cache's tokens as packed tensors
  *   flex_kv_cache_attention            the newest tokens' attention against it
+ *   flex_packed_plan_create, flex_attention_packed_fwd   attention over packed
+ *                                      sequences of different lengths, query
+ *                                      heads sharing key heads
  * Helpers size the BlockMask buffers, name status codes and read the device
  * status word.
  *
@@ -614,6 +617,66 @@ FLEX_API int flex_kv_cache_attention(const flex_tensor *q, const flex_kv_cache *
  */
 FLEX_API int flex_kv_cache_attention_workspace(const flex_tensor *q, const flex_kv_cache *cache, int32_t max_pages,
                                                int32_t mask_kind, const flex_mask_params *params, int64_t *bytes);
+
+/*
+ * Attention over packed sequences (prompts of different lengths one behind the
+ * other), with query heads that share key heads.  A plan holds what depends on the
+ * lengths and the mask: it is made once for a batch and serves all layers, on any
+ * stream that is ordered behind it, and is only read by the attention.
+ */
+typedef struct {
+    int32_t sequences, total_q, total_k;  /* packed sequences; tokens of q and of k, v         */
+    int32_t Hq, Hk;                       /* query heads and key heads                         */
+    int32_t mask_kind, window, sinks;     /* as the plan was made (window INT32_MAX: no window) */
+    void *entries;                        /* device, flex_packed_plan_bytes, 16-byte aligned   */
+} flex_packed_plan;
+
+/* Bytes of a plan's entries (32 for every run of 2 floor(128 / (Hq / Hk)) tokens that `sequences`
+ * sequences of total_q tokens can have).  Errors: as flex_packed_plan_create. */
+FLEX_API int flex_packed_plan_bytes(int32_t sequences, int32_t total_q, int32_t Hq, int32_t Hk, int64_t *bytes);
+
+/*
+ * Make the plan of a batch.
+ *   q_starts, k_starts : device, [sequences + 1] int32, ascending: sequence b has
+ *               the tokens q_starts[b] .. q_starts[b + 1] - 1 of q, and k_starts[b] ..
+ *               k_starts[b + 1] - 1 of k and v (the same array where all keys are new;
+ *               more keys than queries where earlier tokens lie before them).  Within
+ *               0 .. total_q and 0 .. total_k: a sequence whose queries are not has no rows,
+ *               one whose keys are not has no keys.
+ *   total_q, total_k : tokens of the q, and of the k and v that the plan is for.
+ *   Hq, Hk    : query head h reads key head h / (Hq / Hk); Hq / Hk at most 128.
+ *   mask_kind : FLEX_MASK_CAUSAL, FLEX_MASK_SLIDING_WINDOW, FLEX_MASK_WINDOW_SINKS
+ *               (params) with a row's position in place of q, where row t of n with
+ *               m keys has position m - n + t (rows at negative positions keep
+ *               nothing); FLEX_MASK_ALL: every row keeps every key of its sequence.
+ *   plan      : in: entries; out: the other fields, and the entries by a kernel on
+ *               `stream`.
+ * Errors: FLEX_ERR_INVALID_ARG, FLEX_ERR_SHAPE (Hq not a multiple of Hk, sizes not
+ * positive), FLEX_ERR_ALIGNMENT, FLEX_ERR_UNSUPPORTED (other masks, more than 65535
+ * sequences, 32767 heads or 128 query heads per key head), FLEX_ERR_CUDA.
+ */
+FLEX_API int flex_packed_plan_create(const int32_t *q_starts, const int32_t *k_starts, int32_t sequences, int32_t total_q,
+                                     int32_t total_k, int32_t Hq, int32_t Hk, int32_t mask_kind,
+                                     const flex_mask_params *params, flex_packed_plan *plan, void *stream);
+
+/*
+ * The attention of a plan's rows: s, out and lse as in flex_attention_fwd over the
+ * keys that a row keeps of its sequence (softcap and lse to float32's accuracy).
+ *   q    : [1, Hq, total_q, D];  k, v : [1, Hk, total_k, D]; bf16, D in {64, 128},
+ *          strides as in flex_tensor, 16-byte aligned.
+ *   out  : bf16 [1, Hq, total_q, D] with its own strides; it overlaps no input.
+ *   lse  : device, contiguous [1, Hq, total_q] float32.
+ * Rows that keep nothing get out = 0, lse = -inf; tokens outside of the sequences
+ * are left as they were.  Keys and values that a row does not keep have no effect
+ * on it, NaN included, nor have other sequences'.  Made for prompts (rows of 128 /
+ * (Hq / Hk) tokens fill a tile); a decoding step belongs in
+ * flex_kv_cache_attention.  Forward only.  Errors: FLEX_ERR_INVALID_ARG,
+ * FLEX_ERR_SHAPE (tensors that are not the plan's sizes), FLEX_ERR_ALIGNMENT,
+ * FLEX_ERR_UNSUPPORTED (fp32, head dim), FLEX_ERR_CUDA.  Asynchronous on `stream`.
+ */
+FLEX_API int flex_attention_packed_fwd(const flex_tensor *q, const flex_tensor *k, const flex_tensor *v,
+                                       const flex_packed_plan *plan, int32_t score_kind, float score_param, float scale,
+                                       const flex_tensor *out, float *lse, void *stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of
