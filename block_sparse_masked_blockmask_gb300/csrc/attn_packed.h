@@ -61,6 +61,21 @@ __host__ __device__ __forceinline__ TileRange packed_range(const PackedMask &m, 
     return r;
 }
 
+// The kv tiles that all rows of positions first .. last keep whole: [lo, hi], and
+// the first `sinks` tiles.
+__host__ __device__ __forceinline__ TileRange packed_full(const PackedMask &m, int first, int last, int k_len) {
+    TileRange r = {0, (k_len >> 7) - 1, 0};
+    if (m.causal) {
+        const int seen = first + 1 < k_len ? first + 1 : k_len;
+        if (seen <= 0) return {0, -1, 0};
+        const int64_t low = (int64_t)last - m.window + 1;
+        r.lo = low > 0 ? (int)((low + 127) >> 7) : 0;
+        r.hi = (seen >> 7) - 1;
+        r.sinks = (m.sinks < seen ? m.sinks : seen) >> 7;
+    }
+    return r;
+}
+
 // The kv tiles of an item's two Q tiles together (`tokens` of them from position
 // `pos` on, `per` a tile): hi, hi - 1, ... (n_main of them), then n_sink - 1, ... 0.
 struct ItemTiles {

@@ -48,18 +48,27 @@ struct PackedParams {
     int wide_out;           // out rows are 32-byte aligned
 };
 
+// Kv tiles as the steps of an item that walk them: first .. last, and from `sinks`
+// on (where the walk leaves out tiles between a window and the sinks, no tile
+// of the window's part is one of the sinks').
+struct alignas(16) StepRange {
+    int first, last, sinks, pad;
+    __device__ __forceinline__ bool has(int u) const { return (u >= first && u <= last) || u >= sinks; }
+};
+__device__ __forceinline__ StepRange step_range(const TileRange &r, int hi, int nu) {
+    return {hi - r.hi, hi - r.lo, nu - r.sinks, 0};
+}
+
 // One work item as the scheduler warp publishes it.
 struct PackedItem {
     int nu;                  // kv tiles of both Q tiles; -1: no more work for this CTA
-    int n_main, hi, n_sink;  // of them hi, hi - 1, ... (n_main), then n_sink - 1, ... 0
+    int n_main, hi;          // of them hi, hi - 1, ... (n_main), then nu - n_main - 1, ... 0
     int hk, q_row, q_tokens, pos, k_row, k_len;
     int has1;
-    TileRange range[2];
+    StepRange need[2];       // steps whose kv tile a Q tile needs
+    StepRange full[2];       // those whose kv tile all rows of a Q tile keep whole
+    StepRange clean;         // those that are so for both: the values of other steps are cleaned
     volatile int odd;        // a value that is not finite was zeroed in a staged tile
-    __device__ __forceinline__ int tile(int u) const { return u < n_main ? hi - u : n_sink - 1 - (u - n_main); }
-    __device__ __forceinline__ bool present(int i, int c) const {
-        return (c >= range[i].lo && c <= range[i].hi) || c < range[i].sinks;
-    }
 };
 
 struct PackedMisc {
@@ -97,13 +106,6 @@ __device__ __forceinline__ RowKeep packed_keep(const PackedMask &m, int pos, int
     if (r.lo <= r.sink + 1) r = {0, r.hi, -1};
     return r;
 }
-// Whether rows of positions first .. last all keep the whole of kv tile c.
-__device__ __forceinline__ bool packed_full(const PackedMask &m, int first, int last, int k_len, int c) {
-    const int end = c * kBlock + kBlock - 1;
-    if (end >= k_len) return false;
-    return !m.causal || (end <= first && ((int64_t)c * kBlock > (int64_t)last - m.window || end < m.sinks));
-}
-
 __device__ __forceinline__ void apply_packed_mask(const RowKeep &r, int kv0, uint64_t (&x2)[64]) {
     const int csink = r.sink - kv0, clo = r.lo - kv0, chi = r.hi - kv0;
     const bool sink_here = csink >= 0, main_here = clo < kBlock && chi >= 0;
@@ -210,7 +212,6 @@ __device__ __forceinline__ void build_packed(const PackedParams &p, PackedItem &
     if (lane == 0) {
         sl.n_main = t.n_main;
         sl.hi = t.hi;
-        sl.n_sink = t.n_sink;
         sl.nu = t.n_main + t.n_sink;
         sl.hk = g0 + r % gsize;
         sl.q_row = a.x;
@@ -219,8 +220,15 @@ __device__ __forceinline__ void build_packed(const PackedParams &p, PackedItem &
         sl.k_row = a.w;
         sl.k_len = k_len;
         sl.has1 = tokens > p.tokens;
-        sl.range[0] = t.range[0];
-        sl.range[1] = t.range[1];
+        const int nu = t.n_main + t.n_sink;
+        for (int i = 0; i < 2; ++i) {
+            const int first = i * p.tokens, last = min(first + p.tokens, tokens) - 1;
+            sl.need[i] = step_range(t.range[i], t.hi, nu);
+            sl.full[i] = i == 1 && tokens <= p.tokens ? sl.full[0]
+                                                      : step_range(packed_full(p.mask, pos + first, pos + last, k_len), t.hi, nu);
+        }
+        sl.clean = {max(sl.full[0].first, sl.full[1].first), min(sl.full[0].last, sl.full[1].last),
+                    max(sl.full[0].sinks, sl.full[1].sinks), 0};
         sl.odd = 0;
     }
     __syncwarp();
@@ -358,11 +366,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 const int nu = sl.nu;
                 if (nu < 0) break;
-                const int hk = sl.hk, k_row = sl.k_row;
+                const int hk = sl.hk, k_row = sl.k_row, hi = sl.hi, n_main = sl.n_main;
                 for (int u = 0; u < nu; ++u, ++g) {
                     const int s = (int)(g % NS);
                     const uint32_t use = g / NS;
-                    const int row = k_row + sl.tile(u) * kBlock;
+                    const int row = k_row + (u < n_main ? hi - u : nu - 1 - u) * kBlock;
                     uint8_t *dst = smem + C::kKvOff + s * C::kStageBytes;
                     if (does_k) {
                         if (use > 0 && !mbar_wait(&ms.k_empty[s], (use - 1) & 1u, abort_flag)) {
@@ -446,13 +454,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int nu = sl.nu;
                 if (nu < 0) break;
                 if (nu > 0) {
-                    auto present = [&](int u) { return sl.present(ti, sl.tile(u)); };
+                    const StepRange need = sl.need[ti];
                     ok = mbar_wait(&ms.q_full, nq & 1u, abort_flag);
                     tc_fence_after_sync();
                     for (int u = 0; ok && u < min(nu, 2); ++u) {
                         const uint32_t gu = g + (uint32_t)u;
                         const int s = (int)(gu % NS);
-                        ok = mbar_wait(&ms.k_full[s], (gu / NS) & 1u, abort_flag) && (!present(u) || issue_s(s));
+                        ok = mbar_wait(&ms.k_full[s], (gu / NS) & 1u, abort_flag) && (!need.has(u) || issue_s(s));
                         mma_commit(&ms.k_empty[s]);
                         if (u + 1 == nu) mma_commit(&ms.q_empty);  // the item's last S is issued
                     }
@@ -464,7 +472,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             ok = false;
                             break;
                         }
-                        if (present(u)) {
+                        if (need.has(u)) {
                             if (!issue_pv(s, pv_item > 0)) {
                                 ok = false;
                                 break;
@@ -475,7 +483,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (u + 2 < nu) {
                             const uint32_t g2 = gu + 2;
                             const int s2 = (int)(g2 % NS);
-                            if (!mbar_wait(&ms.k_full[s2], (g2 / NS) & 1u, abort_flag) || (present(u + 2) && !issue_s(s2))) {
+                            if (!mbar_wait(&ms.k_full[s2], (g2 / NS) & 1u, abort_flag) || (need.has(u + 2) && !issue_s(s2))) {
                                 ok = false;
                                 break;
                             }
@@ -541,10 +549,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (nu < 0) break;
                 if (nu > 0) {
                     // which Q tiles a step is for: bits 0 and 1
-                    auto flags = [&](int u) {
-                        const int c = sl.tile(u);
-                        return (sl.present(0, c) ? 1u : 0u) | (sl.present(1, c) ? 2u : 0u);
-                    };
+                    const StepRange need0 = sl.need[0], need1 = sl.need[1];
+                    auto flags = [&](int u) { return (need0.has(u) ? 1u : 0u) | (need1.has(u) ? 2u : 0u); };
                     pv_item[0] = pv_item[1] = 0u;
                     const int s0 = (int)(g % NS);
                     ok = mbar_wait(&ms.q_full, nq & 1u, abort_flag) &&
@@ -622,16 +628,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int token = i * p.tokens + token_in, h = sl.hk * p.G + head_in;
           const bool live_row = token_in < p.tokens && token < sl.q_tokens;
           const int pos = sl.pos + token, k_len = sl.k_len;
-          // positions of the tile's rows, and of the other tile's
-          const int first = sl.pos + i * p.tokens, last = sl.pos + min((i + 1) * p.tokens, sl.q_tokens) - 1;
-          RowKeep keep = packed_keep(p.mask, pos, k_len);
-          if (!live_row) keep = {0, -1, -1};
-          // whether some row of the item's tiles does not keep the whole of kv tile c that its tile needs
-          auto touched = [&](int c) {
-              if (!packed_full(p.mask, first, last, k_len, c)) return true;
-              const int f1 = sl.pos + (1 - i) * p.tokens, l1 = sl.pos + min((2 - i) * p.tokens, sl.q_tokens) - 1;
-              return (i == 1 || sl.has1) && sl.present(1 - i, c) && !packed_full(p.mask, f1, l1, k_len, c);
-          };
+          // what the row keeps: worked out where it is needed, which few steps do
+          auto kept_columns = [&]() { return live_row ? packed_keep(p.mask, pos, k_len) : RowKeep{0, -1, -1}; };
+          const int hi = sl.hi, n_main = sl.n_main;
           PackedScore<SCORE> score;
           score.init(p, h);
           // see attn_bf16_kernel.cuh for the finite floor of the running max and
@@ -640,9 +639,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           uint32_t cnt = 0;
           if (valid) {
             for (int u = 0; u < nu; ++u) {
-                const int c = sl.tile(u);
-                if (!sl.present(i, c)) continue;
-                const int kv0 = c * kBlock;
+                if (!sl.need[i].has(u)) continue;
+                const bool full = sl.full[i].has(u), clean = sl.clean.has(u);
+                const int kv0 = (u < n_main ? hi - u : nu - 1 - u) * kBlock;
                 if (!warp_wait(&ms.s_full[i], cnt_total & 1u, abort_flag)) {
                     ok = false;
                     break;
@@ -662,7 +661,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int j = 0; j < 64; ++j)
                         x2[j] = score.pair(f2_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
                 }
-                if (!packed_full(p.mask, first, last, k_len, c)) apply_packed_mask(keep, kv0, x2);
+                if (!full) apply_packed_mask(kept_columns(), kv0, x2);
                 float mx[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -689,7 +688,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 64; ++j) x2[j] = f2_add(x2[j], shift2);
                 }
-                if (touched(c)) {  // masked columns meet no value that is not finite
+                if (!clean) {  // masked columns meet no value that is not finite
                     const uint32_t gu = g + (uint32_t)u;
                     const int stage = (int)(gu % NS);
                     if (!warp_wait(&ms.v_full[stage], (gu / NS) & 1u, abort_flag)) {
@@ -783,36 +782,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) o[j] = 0u;
                     }
-                    float x[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = kept ? __uint_as_float(o[j]) * inv : 0.f;
-                    if (odd && live_row) {
-                        // the values that were zeroed, of the columns that this row keeps
-#pragma unroll 1
-                        for (int u = 0; u < nu; ++u) {
-                            const int c = sl.tile(u);
-                            if (!sl.present(i, c) || !touched(c)) continue;
-#pragma unroll 1
-                            for (int kv = c * kBlock; kv < (c + 1) * kBlock && kv < k_len; ++kv) {
-                                if (!((kv >= keep.lo && kv <= keep.hi) || kv <= keep.sink)) continue;
-                                const uint16_t *src = p.v + sl.hk * p.v_stride[0] + (sl.k_row + (int64_t)kv) * p.v_stride[1] + c0;
-#pragma unroll
-                                for (int j = 0; j < 32; j += 8) {
-                                    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + j));
-                                    const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                    for (int z = 0; z < 4; ++z) {
-                                        if ((e[z] & 0x7F80u) == 0x7F80u) x[j + 2 * z] += __uint_as_float(e[z] << 16);
-                                        if ((e[z] & 0x7F800000u) == 0x7F800000u)
-                                            x[j + 2 * z + 1] += __uint_as_float(e[z] & 0xFFFF0000u);
-                                    }
-                                }
-                            }
-                        }
-                    }
                     uint32_t pk[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+                    for (int j = 0; j < 16; ++j) {
+                        pk[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        if (!kept) pk[j] = 0u;
+                    }
                     if (live_row) {
                         if (p.wide_out) {  // whole 32-byte sectors per store
                             st_global_32B(dst + c0, &pk[0]);
@@ -826,6 +801,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
                 if (live_row) p.lse[(int64_t)h * p.total_q + row] = kept ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+                if (odd && live_row) {
+                    // the values that were zeroed, of the columns that this row keeps, on top of what was stored
+                    const RowKeep keep = kept_columns();
+#pragma unroll 1
+                    for (int u = 0; u < nu; ++u) {
+                        if (!sl.need[i].has(u) || sl.clean.has(u)) continue;
+                        const int kv0 = (u < n_main ? hi - u : nu - 1 - u) * kBlock;
+#pragma unroll 1
+                        for (int kv = kv0; kv < kv0 + kBlock && kv < k_len; ++kv) {
+                            if (!((kv >= keep.lo && kv <= keep.hi) || kv <= keep.sink)) continue;
+                            const uint16_t *src = p.v + sl.hk * p.v_stride[0] + (sl.k_row + (int64_t)kv) * p.v_stride[1];
+#pragma unroll 1
+                            for (int d = 0; d < D; ++d)
+                                if ((src[d] & 0x7F80u) == 0x7F80u)
+                                    dst[d] = (uint16_t)pack_bf16x2(__uint_as_float((uint32_t)dst[d] << 16) +
+                                                                       __uint_as_float((uint32_t)src[d] << 16), 0.f);
+                        }
+                    }
+                }
             }
           }
           if (nu > 0) {
