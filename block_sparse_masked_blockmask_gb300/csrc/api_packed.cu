@@ -104,6 +104,7 @@ int flex_attention_packed_fwd(const flex_tensor *q, const flex_tensor *k, const 
     if ((rc = check_tensor(v, FLEX_DTYPE_BF16, 1, plan->Hk, plan->total_k, D)) != FLEX_OK) return rc;
     if ((rc = check_tensor(out, FLEX_DTYPE_BF16, 1, plan->Hq, plan->total_q, D)) != FLEX_OK) return rc;
     if (!aligned(lse, 4) || !aligned(plan->entries, 16)) return FLEX_ERR_ALIGNMENT;
+    p.sequences = plan->sequences;
     p.Hq = plan->Hq;
     p.Hk = plan->Hk;
     p.D = (int)D;

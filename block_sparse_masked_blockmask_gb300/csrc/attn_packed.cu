@@ -7,12 +7,14 @@
 // up, and places the entries; entries of one length have no order, which no result depends on.  It
 // is made once for a batch and serves all its layers.
 #include <algorithm>
+#include <climits>
 
 #include "attn_packed_kernel.cuh"
 
 namespace flex {
 namespace {
 
+constexpr int64_t kFewKeys = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kLengths = 1024;  // lengths told apart, in kv tiles (longer ones count as the longest)
 
@@ -98,6 +100,10 @@ cudaError_t launch_attn_packed(const PackedProblem &p, cudaStream_t stream) {
     kp.lse = p.lse;
     kp.status = p.status;
     kp.wide_out = (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.out_stride[0] * 2 | (uintptr_t)p.out_stride[1] * 2) % 32 == 0;
+    // few kv tiles: at most so many keys a sequence on average, or in a window
+    int64_t keys = p.total_k / p.sequences;
+    if (p.mask.window != INT_MAX) keys = std::min<int64_t>(keys, (int64_t)p.mask.window + p.mask.sinks);
+    kp.few_tiles = keys <= kFewKeys;
     return p.D == 64 ? launch_packed_d64(p, kp, stream) : launch_packed_d128(p, kp, stream);
 }
 

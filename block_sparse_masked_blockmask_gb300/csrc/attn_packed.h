@@ -24,7 +24,7 @@ struct PackedMask {
 };
 
 struct PackedProblem {
-    int Hq, Hk, D, total_q, total_k;
+    int sequences, Hq, Hk, D, total_q, total_k;
     const void *q, *k, *v;
     int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];  // h, token (elements)
     const PlanEntry *plan;  // [0].q_row: how many entries follow

@@ -20,9 +20,9 @@
 //  * A tile of keys may reach into the next sequence: its columns are masked like
 //    those behind a row's position.  A masked column has weight 0, which a value
 //    that is not finite would turn into NaN; so in tiles that some row does not
-//    keep whole, the softmax warps look through the staged values before they hand
-//    over P (16 reads a thread at D = 128), zero what is not finite, and such an
-//    item's rows add those of them that they keep at the end.
+//    keep whole, the warp that loads the values looks through them, beside the
+//    softmax of the step, and zeroes what is not finite, and such an item's rows
+//    add those of them that they keep at the end.
 //  * lse to float32's accuracy: the row sum takes the weights before their
 //    rounding to bf16, softcap is not the hardware's tanh, and ALiBi's distances
 //    are whole numbers until they meet the slope.
@@ -46,6 +46,7 @@ struct PackedParams {
     float *lse;
     int *status;
     int wide_out;           // out rows are 32-byte aligned
+    int few_tiles;          // items have few kv tiles each, on average
 };
 
 // Kv tiles as the steps of an item that walk them: first .. last, and from `sinks`
@@ -66,14 +67,14 @@ struct PackedItem {
     int hk, q_row, q_tokens, pos, k_row, k_len;
     int has1;
     StepRange need[2];       // steps whose kv tile a Q tile needs
-    StepRange full[2];       // those whose kv tile all rows of a Q tile keep whole
-    StepRange clean;         // those that are so for both: the values of other steps are cleaned
+    StepRange full;          // steps whose kv tile all rows of both Q tiles keep whole
     volatile int odd;        // a value that is not finite was zeroed in a staged tile
 };
 
 struct PackedMisc {
     uint64_t q_full, q_empty, near_end;
     uint64_t k_full[4], v_full[4], k_empty[4], v_empty[4];
+    uint64_t v_clean[4];                       // the stage's values were looked through (steps that are not full)
     uint64_t s_full[2], p_full[2], s_free[2], pv_done[2], o_full[2], drain[2];
     uint64_t item_ready[2], item_free[2];
     uint64_t clc_bar;
@@ -106,19 +107,28 @@ __device__ __forceinline__ RowKeep packed_keep(const PackedMask &m, int pos, int
     if (r.lo <= r.sink + 1) r = {0, r.hi, -1};
     return r;
 }
+// Columns lo .. hi of 32, as bits.
+__device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
+    const uint32_t below = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u;
+    return lo <= 0 ? below : lo > 31 ? 0u : below & (~0u << lo);
+}
+// The scores of columns that a row does not keep become -inf, 32 columns at a
+// time: a warp's rows are few tokens, so most chunks are kept whole by all of
+// them, or by none.
 __device__ __forceinline__ void apply_packed_mask(const RowKeep &r, int kv0, uint64_t (&x2)[64]) {
-    const int csink = r.sink - kv0, clo = r.lo - kv0, chi = r.hi - kv0;
-    const bool sink_here = csink >= 0, main_here = clo < kBlock && chi >= 0;
-    if (!__any_sync(0xffffffffu, sink_here && main_here)) {
-        const int a = sink_here ? 0 : clo, e = sink_here ? csink : chi;
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-            x2[j] = keep_pair(x2[j], 2 * j >= a && 2 * j <= e, 2 * j + 1 >= a && 2 * j + 1 <= e);
-    } else {
+    for (int q = 0; q < 4; ++q) {
+        const int at = kv0 + 32 * q;
+        const uint32_t keep = column_bits(r.lo - at, r.hi - at) | column_bits(0, r.sink - at);
+        if (__all_sync(0xffffffffu, keep == ~0u)) continue;
+        if (__all_sync(0xffffffffu, keep == 0u)) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-            x2[j] = keep_pair(x2[j], 2 * j <= csink || (2 * j >= clo && 2 * j <= chi),
-                              2 * j + 1 <= csink || (2 * j + 1 >= clo && 2 * j + 1 <= chi));
+            for (int j = 0; j < 16; ++j) x2[16 * q + j] = f2_pack(-INFINITY, -INFINITY);
+            continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            x2[16 * q + j] = keep_pair(x2[16 * q + j], (keep >> (2 * j)) & 1u, (keep >> (2 * j + 1)) & 1u);
     }
 }
 
@@ -158,6 +168,16 @@ struct PackedScore {
     }
 };
 
+// TMEM read of 64 columns of this thread's lane, completed before returning.
+__device__ __forceinline__ void tmem_ld64_sync(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
+
 // The largest magnitude's bits of the two bf16 of each word, and whether one is
 // an infinity or NaN.
 __device__ __forceinline__ uint32_t most_bf16x2(uint32_t most, uint32_t w) { return __vmaxu2(most, w & 0x7FFF7FFFu); }
@@ -165,37 +185,36 @@ __device__ __forceinline__ bool odd_bf16x2(uint32_t most) {
     return (most & 0x7FFFu) >= 0x7F80u || (most >> 16) >= 0x7F80u;
 }
 
-// Zero what is not finite in a staged tile of values (the 128 softmax threads of
-// a Q tile; those of the other one may do the same at the same time).
+// Zero what is not finite in a staged tile of values, with the 32 lanes of a
+// warp; *odd is set where something was.
 template <int D>
-__device__ __forceinline__ void clean_values(uint8_t *tile, int t, volatile int *odd) {
-    constexpr int N = 128 * D * 2 / 16 / 128;  // 16-byte words of a thread
+__device__ __forceinline__ void clean_values(uint8_t *tile, int lane, volatile int *odd) {
     uint4 *v = reinterpret_cast<uint4 *>(tile);
-    uint32_t most = 0u;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint4 w = v[i * 128 + t];
-        most = most_bf16x2(most_bf16x2(most_bf16x2(most_bf16x2(most, w.x), w.y), w.z), w.w);
-    }
-    if (!odd_bf16x2(most)) {
-        __threadfence_block();  // a zero that the other tile's thread wrote is seen after its flag
-        if (*odd) fence_proxy_async_smem();
-        return;
-    }
-    *odd = 1;
-    __threadfence_block();
+    constexpr int N = 128 * D * 2 / 16;  // 16-byte words
+    constexpr int U = 4;                 // of a lane in flight
 #pragma unroll 1
-    for (int i = 0; i < N; ++i) {
-        uint4 w = v[i * 128 + t];
-        uint32_t *e = reinterpret_cast<uint32_t *>(&w);
+    for (int i = lane; i < N; i += 32 * U) {
+        uint4 w[U];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if ((e[j] & 0x7F80u) == 0x7F80u) e[j] &= 0xFFFF0000u;
-            if ((e[j] & 0x7F800000u) == 0x7F800000u) e[j] &= 0xFFFFu;
+        for (int k = 0; k < U; ++k) w[k] = v[i + 32 * k];
+        uint32_t most = 0u;
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            most = most_bf16x2(most_bf16x2(most_bf16x2(most_bf16x2(most, w[k].x), w[k].y), w[k].z), w[k].w);
+        if (!odd_bf16x2(most)) continue;
+        *odd = 1;
+#pragma unroll 1
+        for (int k = 0; k < U; ++k) {
+            uint32_t *e = reinterpret_cast<uint32_t *>(&v[i + 32 * k]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if ((e[j] & 0x7F80u) == 0x7F80u) e[j] &= 0xFFFF0000u;
+                if ((e[j] & 0x7F800000u) == 0x7F800000u) e[j] &= 0xFFFFu;
+            }
         }
-        v[i * 128 + t] = w;
+        fence_proxy_async_smem();  // the MMAs read these generic-proxy writes
     }
-    fence_proxy_async_smem();  // the MMAs read these generic-proxy writes
+    __syncwarp();
 }
 
 // Item `item` of the grid into `sl` (all lanes of the scheduler warp compute it).
@@ -221,20 +240,16 @@ __device__ __forceinline__ void build_packed(const PackedParams &p, PackedItem &
         sl.k_len = k_len;
         sl.has1 = tokens > p.tokens;
         const int nu = t.n_main + t.n_sink;
-        for (int i = 0; i < 2; ++i) {
-            const int first = i * p.tokens, last = min(first + p.tokens, tokens) - 1;
-            sl.need[i] = step_range(t.range[i], t.hi, nu);
-            sl.full[i] = i == 1 && tokens <= p.tokens ? sl.full[0]
-                                                      : step_range(packed_full(p.mask, pos + first, pos + last, k_len), t.hi, nu);
-        }
-        sl.clean = {max(sl.full[0].first, sl.full[1].first), min(sl.full[0].last, sl.full[1].last),
-                    max(sl.full[0].sinks, sl.full[1].sinks), 0};
+        sl.need[0] = step_range(t.range[0], t.hi, nu);
+        sl.need[1] = step_range(t.range[1], t.hi, nu);
+        sl.full = step_range(packed_full(p.mask, pos, pos + tokens - 1, k_len), t.hi, nu);
         sl.odd = 0;
     }
     __syncwarp();
 }
 
-template <int D, int SCORE>
+// SHORT: compiled for items of few kv tiles, see the softmax.
+template <int D, int SCORE, bool SHORT>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const PackedParams p) {
@@ -256,6 +271,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(&ms.v_full[s], 1);
             mbar_init(&ms.k_empty[s], C::kIssuers);
             mbar_init(&ms.v_empty[s], C::kIssuers);
+            mbar_init(&ms.v_clean[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms.s_full[i], 1);
@@ -350,59 +366,83 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
     } else if (warp == kTmaWarp || (!C::kSepP && warp == kTmaVWarp)) {
         // ----------------------------------------------------- TMA producers
-        // D = 128: warp 8 loads K, warp 10 V; D = 64: warp 8 both
-        if (lane == 0) {
-            const bool does_k = warp == kTmaWarp, does_v = C::kSepP || warp == kTmaVWarp;
-            if (does_k) prefetch_tensormap(&tmap_k);
-            if (does_v) prefetch_tensormap(&tmap_v);
-            uint32_t g = 0;  // steps issued over all items
-            bool ok = true;
-            for (uint32_t n = 0; ok; ++n) {
-                const int k = (int)(n & 1u);
-                const PackedItem &sl = ms.slot[k];
-                if (!mbar_wait(&ms.item_ready[k], (n >> 1) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                const int nu = sl.nu;
-                if (nu < 0) break;
-                const int hk = sl.hk, k_row = sl.k_row, hi = sl.hi, n_main = sl.n_main;
-                for (int u = 0; u < nu; ++u, ++g) {
-                    const int s = (int)(g % NS);
-                    const uint32_t use = g / NS;
-                    const int row = k_row + (u < n_main ? hi - u : nu - 1 - u) * kBlock;
-                    uint8_t *dst = smem + C::kKvOff + s * C::kStageBytes;
-                    if (does_k) {
-                        if (use > 0 && !mbar_wait(&ms.k_empty[s], (use - 1) & 1u, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
+        // D = 128: warp 8 loads K, warp 10 V; D = 64: warp 8 both.  The loads are
+        // lane 0's; the warp that loads V looks through the values of a step that
+        // is not full once the next step's loads are on the way.
+        const bool does_k = warp == kTmaWarp, does_v = C::kSepP || warp == kTmaVWarp;
+        if (lane == 0 && does_k) prefetch_tensormap(&tmap_k);
+        if (lane == 0 && does_v) prefetch_tensormap(&tmap_v);
+        uint32_t g = 0;  // steps issued over all items
+        bool ok = true, half = false;  // half: a step's K was issued and its V was not
+        int left = -1;                 // the step whose values are still to be looked through, over all items
+        auto look = [&](PackedItem &sl) -> bool {
+            if (left < 0) return true;
+            const int s = (int)((uint32_t)left % NS);
+            if (!warp_wait(&ms.v_full[s], ((uint32_t)left / NS) & 1u, abort_flag)) return false;
+            clean_values<D>(smem + C::kKvOff + s * C::kStageBytes + C::kTileBytes, lane, &sl.odd);
+            if (lane == 0) mbar_arrive(&ms.v_clean[s]);
+            left = -1;
+            return true;
+        };
+        for (uint32_t n = 0; ok; ++n) {
+            const int k = (int)(n & 1u);
+            PackedItem &sl = ms.slot[k];
+            if (!warp_wait(&ms.item_ready[k], (n >> 1) & 1u, abort_flag)) {
+                ok = false;
+                break;
+            }
+            const int nu = sl.nu;
+            if (nu < 0) break;
+            const int hk = sl.hk, k_row = sl.k_row, hi = sl.hi, n_main = sl.n_main;
+            for (int u = 0; u < nu; ++u, ++g) {
+                const int s = (int)(g % NS);
+                const uint32_t use = g / NS;
+                const int row = k_row + (u < n_main ? hi - u : nu - 1 - u) * kBlock;
+                uint8_t *dst = smem + C::kKvOff + s * C::kStageBytes;
+                if (does_k) {
+                    if (use > 0 && !warp_wait(&ms.k_empty[s], (use - 1) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
                         mbar_arrive_expect_tx(&ms.k_full[s], C::kTileBytes);
                         for (int a = 0; a < C::kAtoms; ++a)
                             tma_load_3d(dst + a * C::kAtomBytes, &tmap_k, &ms.k_full[s], 64 * a, row, hk);
                     }
-                    if (does_v) {
-                        if (use > 0 && !mbar_wait(&ms.v_empty[s], (use - 1) & 1u, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
+                }
+                if (does_v) {
+                    if (use > 0 && !warp_wait(&ms.v_empty[s], (use - 1) & 1u, abort_flag)) {
+                        ok = false;
+                        half = does_k;
+                        break;
+                    }
+                    if (lane == 0) {
                         mbar_arrive_expect_tx(&ms.v_full[s], C::kTileBytes);
                         for (int a = 0; a < C::kAtoms; ++a)
                             tma_load_3d(dst + C::kTileBytes + a * C::kAtomBytes, &tmap_v, &ms.v_full[s], 64 * a, row, hk);
                     }
+                    if (!look(sl)) {
+                        ok = false;
+                        ++g;
+                        break;
+                    }
+                    if (!sl.full.has(u)) left = (int)g;
                 }
-                if (ok && does_k && nu > 0) mbar_arrive(&ms.near_end);
-                if (ok) mbar_arrive(&ms.item_free[k]);
             }
-            if (!ok) record_failure(ms, p.status);
-            // Drain: every copy issued above lands before the CTA exits (a step
-            // that gave up between its K and its V has none of the latter).
+            if (ok && does_k && nu > 0 && lane == 0) mbar_arrive(&ms.near_end);
+            if (ok && does_v) ok = look(sl);
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&ms.item_free[k]);
+        }
+        if (!ok && lane == 0) record_failure(ms, p.status);
+        // Drain: every copy issued above lands before the CTA exits.
+        if (lane == 0) {
             for (uint32_t s = 0; s < (uint32_t)NS && s < g; ++s) {
                 const uint32_t last = s + ((g - 1 - s) / NS) * NS;
                 if (does_k) drain_wait(&ms.k_full[s], (last / NS) & 1u);
                 if (does_v) drain_wait(&ms.v_full[s], (last / NS) & 1u);
             }
-            if (!ok && C::kSepP) drain_wait(&ms.k_full[g % NS], (g / NS) & 1u);
+            if (half) drain_wait(&ms.k_full[g % NS], (g / NS) & 1u);
         }
         __syncwarp();
     } else if (C::kSepP && (warp == kMmaWarp || warp == kTmaVWarp)) {
@@ -578,11 +618,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             ok = false;
                             break;
                         }
+                        if (!nxt) mma_commit(&ms.o_full[0]);
                         if (f1 & 1u) issue_s(0, s1);
                         if ((f & 2u) && !issue_pv(1, s)) {
                             ok = false;
                             break;
                         }
+                        if (!nxt) mma_commit(&ms.o_full[1]);
                         mma_commit(&ms.v_empty[s]);
                         if (nxt) {
                             if (f1 & 2u) issue_s(1, s1);
@@ -592,7 +634,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         f = f1;
                     }
                     if (!ok) break;
-                    mma_commit(&ms.o_full[0]);
                     g += (uint32_t)nu;
                     ++nq;
                 }
@@ -612,8 +653,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t s_addr = tmem + lane_base + C::s_col(i);
         const uint32_t p_addr = tmem + lane_base + C::p_col(i);
         const uint32_t o_addr = tmem + lane_base + C::o_col(i);
-        const int token_in = t / p.G, head_in = t % p.G;  // of this thread's row
-        uint32_t cnt_total = 0, g = 0, nq = 0;
+        // This thread's row of an item.  Worked out from the thread's index where it is
+        // needed (volatile, so that no register keeps it): the loop over full tiles
+        // has none to spare.
+        struct Row {
+            int token, h, pos;
+            bool live;
+        };
+        auto row_of = [&](const PackedItem &sl) {
+            uint32_t tid;
+            asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+            const int r = (int)(tid % 128u), in = r / p.G;
+            Row row;
+            row.token = i * p.tokens + in;
+            row.h = sl.hk * p.G + r % p.G;
+            row.pos = sl.pos + row.token;
+            row.live = in < p.tokens && row.token < sl.q_tokens;
+            return row;
+        };
+        uint32_t cnt_total = 0, g = 0, nq = 0, cleaned = 0u;  // cleaned: parity of each stage's v_clean
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
           const int k = (int)(n & 1u);
@@ -624,131 +682,201 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           const int nu = sl.nu;
           if (nu < 0) break;
-          const bool valid = i == 0 || sl.has1;
-          const int token = i * p.tokens + token_in, h = sl.hk * p.G + head_in;
-          const bool live_row = token_in < p.tokens && token < sl.q_tokens;
-          const int pos = sl.pos + token, k_len = sl.k_len;
-          // what the row keeps: worked out where it is needed, which few steps do
-          auto kept_columns = [&]() { return live_row ? packed_keep(p.mask, pos, k_len) : RowKeep{0, -1, -1}; };
-          const int hi = sl.hi, n_main = sl.n_main;
           PackedScore<SCORE> score;
-          score.init(p, h);
+          int pos = 0;
+          if constexpr (SCORE == FLEX_SCORE_ALIBI) {
+              const Row row = row_of(sl);
+              score.init(p, row.h);
+              pos = row.pos;
+          } else {
+              score.init(p, 0);
+          }
           // see attn_bf16_kernel.cuh for the finite floor of the running max and
           // the shift that the scores carry
           float m_run = -FLT_MAX, l_run = 0.f;
           uint32_t cnt = 0;
-          if (valid) {
+            // the running max trails by 2^8 at most
+            auto raise = [&](float m_tile, float &alpha) {
+                alpha = 1.f;
+                if (m_tile > m_run + kRescaleThreshold) {  // always taken at the row's first live tile
+                    alpha = ex2_approx(m_run - m_tile);
+                    m_run = m_tile;
+                }
+            };
+            auto rescale_o = [&](float alpha) {
+                if (cnt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32_sync(o_addr + c0, o);
+                        const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float lo, hi;
+                            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1])), a2),
+                                      lo, hi);
+                            o[2 * j] = __float_as_uint(lo);
+                            o[2 * j + 1] = __float_as_uint(hi);
+                        }
+                        tmem_st32(o_addr + c0, o);
+                    }
+                }
+            };
             for (int u = 0; u < nu; ++u) {
+                const bool full = sl.full.has(u);
+                const uint32_t stage = (g + (uint32_t)u) % NS, clean = cleaned >> stage;
+                if (!full) cleaned ^= 1u << stage;
                 if (!sl.need[i].has(u)) continue;
-                const bool full = sl.full[i].has(u), clean = sl.clean.has(u);
-                const int kv0 = (u < n_main ? hi - u : nu - 1 - u) * kBlock;
+                const int kv0 = (u < sl.n_main ? sl.hi - u : nu - 1 - u) * kBlock;
                 if (!warp_wait(&ms.s_full[i], cnt_total & 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
-                const float a_shift = m_run > -FLT_MAX ? -m_run : 0.f;
-                uint64_t x2[64];
-                {
-                    uint32_t r[128];
-                    tmem_ld128_sync(s_addr, r);
+                float alpha;
+                uint64_t rsum2[2] = {0, 0};
+                if constexpr (SHORT) {
+                    // 32 columns at a time, read twice (for the maximum, then for the weights), those that no row of
+                    // the warp keeps left out
+                    const Row row = row_of(sl);
+                    const RowKeep keep = row.live ? packed_keep(p.mask, row.pos, sl.k_len) : RowKeep{0, -1, -1};
+                    auto columns = [&](int at) {
+                        return column_bits(keep.lo - at, keep.hi - at) | column_bits(0, keep.sink - at);
+                    };
+                    auto scores = [&](int q, float a, uint32_t bits, auto &&f) {  // f(j, columns 2j and 2j + 1 of chunk q)
+                        uint32_t r[32];
+                        tmem_ld32_sync(s_addr + 32 * q, r);
+                        score.tile(kv0 + 32 * q, pos, a);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            f(j, keep_pair(score.pair(f2_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]))),
+                                           (bits >> (2 * j)) & 1u, (bits >> (2 * j + 1)) & 1u));
+                    };
+                    float m_tile = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t bits = columns(kv0 + 32 * q);
+                        if (!__any_sync(0xffffffffu, bits != 0u)) continue;
+                        scores(q, 0.f, bits, [&](int, uint64_t x) {
+                            float lo, hi;
+                            f2_unpack(x, lo, hi);
+                            m_tile = fmax3(m_tile, lo, hi);
+                        });
+                    }
+                    raise(m_tile, alpha);
+                    if constexpr (C::kSepP) {
+                        if (cnt_total > 0 && !warp_wait(&ms.pv_done[i], (cnt_total - 1) & 1u, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                    }
+                    rescale_o(alpha);
+                    // P of a chunk goes where the scores of it or of the chunk before it were (D = 128)
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t bits = columns(kv0 + 32 * q);
+                        if (!__any_sync(0xffffffffu, bits != 0u)) {
+                            uint32_t none[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) none[j] = 0u;
+                            tmem_st16(p_addr + 16 * q, none);
+                            continue;
+                        }
+                        uint32_t pk[16];
+                        scores(q, m_run > -FLT_MAX ? -m_run : 0.f, bits, [&](int j, uint64_t x) {
+                            float d0, d1;
+                            f2_unpack(x, d0, d1);
+                            d0 = ex2_approx(d0);
+                            d1 = ex2_approx(d1);
+                            rsum2[j & 1] = f2_add(rsum2[j & 1], f2_pack(d0, d1));
+                            pk[j] = pack_bf16x2(d0, d1);
+                        });
+                        tmem_st16(p_addr + 16 * q, pk);
+                    }
                     if constexpr (C::kSepP) {
                         tc_fence_before_sync();
                         mbar_arrive(&ms.s_free[i]);  // S_i may be overwritten by the next S MMA
                     }
-                    score.tile(kv0, pos, a_shift);
-#pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        x2[j] = score.pair(f2_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
-                }
-                if (!full) apply_packed_mask(kept_columns(), kv0, x2);
-                float mx[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float lo, hi;
-                    f2_unpack(x2[k], lo, hi);
-                    mx[k] = fmaxf(lo, hi);
-                }
-#pragma unroll
-                for (int j = 8; j < 64; ++j) {
-                    float lo, hi;
-                    f2_unpack(x2[j], lo, hi);
-                    mx[j & 7] = fmax3(mx[j & 7], lo, hi);
-                }
-                const float m_tile =
-                    fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) - a_shift;
-                float alpha = 1.f;
-                if (m_tile > m_run + kRescaleThreshold) {  // always taken at the row's first live tile
-                    alpha = ex2_approx(m_run - m_tile);
-                    m_run = m_tile;
-                }
-                const float shift = -m_run - a_shift;
-                if (__any_sync(0xffffffffu, shift != 0.f)) {
-                    const uint64_t shift2 = f2_pack(shift, shift);
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) x2[j] = f2_add(x2[j], shift2);
-                }
-                if (!clean) {  // masked columns meet no value that is not finite
-                    const uint32_t gu = g + (uint32_t)u;
-                    const int stage = (int)(gu % NS);
-                    if (!warp_wait(&ms.v_full[stage], (gu / NS) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    clean_values<D>(smem + C::kKvOff + stage * C::kStageBytes + C::kTileBytes, t, &sl.odd);
-                }
-                auto rescale_o = [&]() {
-                    if (cnt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            tmem_ld32_sync(o_addr + c0, o);
-                            const uint64_t a2 = f2_pack(alpha, alpha);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                float lo, hi;
-                                f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1])), a2),
-                                          lo, hi);
-                                o[2 * j] = __float_as_uint(lo);
-                                o[2 * j + 1] = __float_as_uint(hi);
-                            }
-                            tmem_st32(o_addr + c0, o);
-                        }
-                    }
-                };
-                uint64_t rsum2[2] = {0, 0};
-                auto weights = [&](int j) {
-                    float d0, d1;
-                    f2_unpack(x2[j], d0, d1);
-                    d0 = ex2_approx(d0);
-                    d1 = ex2_approx(d1);
-                    rsum2[j & 1] = f2_add(rsum2[j & 1], f2_pack(d0, d1));
-                    return pack_bf16x2(d0, d1);
-                };
-                if constexpr (C::kSepP) {
-                    uint32_t pk[64];
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) pk[j] = weights(j);
-                    if (cnt_total > 0 && !warp_wait(&ms.pv_done[i], (cnt_total - 1) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    rescale_o();
-#pragma unroll
-                    for (int gq = 0; gq < 4; ++gq)
-                        tmem_st16(p_addr + 16 * gq, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * gq]));
                 } else {
-                    rescale_o();
+                    const float a_shift = m_run > -FLT_MAX ? -m_run : 0.f;
+                    uint64_t x2[64];
+                    {
+                        uint32_t r[128];
+                        tmem_ld128_sync(s_addr, r);
+                        if constexpr (C::kSepP) {
+                            tc_fence_before_sync();
+                            mbar_arrive(&ms.s_free[i]);  // S_i may be overwritten by the next S MMA
+                        }
+                        score.tile(kv0, pos, a_shift);
 #pragma unroll
-                    for (int gq = 0; gq < 4; ++gq) {
-                        uint32_t pk[16];
+                        for (int j = 0; j < 64; ++j)
+                            x2[j] = score.pair(f2_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+                    }
+                    if (!full) {
+                        const Row row = row_of(sl);
+                        apply_packed_mask(row.live ? packed_keep(p.mask, row.pos, sl.k_len) : RowKeep{0, -1, -1}, kv0, x2);
+                    }
+                    float mx[8];
 #pragma unroll
-                        for (int t2 = 0; t2 < 16; ++t2) pk[t2] = weights(16 * gq + t2);
-                        tmem_st16(p_addr + 16 * gq, pk);
+                    for (int k = 0; k < 8; ++k) {
+                        float lo, hi;
+                        f2_unpack(x2[k], lo, hi);
+                        mx[k] = fmaxf(lo, hi);
+                    }
+#pragma unroll
+                    for (int j = 8; j < 64; ++j) {
+                        float lo, hi;
+                        f2_unpack(x2[j], lo, hi);
+                        mx[j & 7] = fmax3(mx[j & 7], lo, hi);
+                    }
+                    const float m_tile =
+                        fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) - a_shift;
+                    raise(m_tile, alpha);
+                    const float shift = -m_run - a_shift;
+                    if (__any_sync(0xffffffffu, shift != 0.f)) {
+                        const uint64_t shift2 = f2_pack(shift, shift);
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) x2[j] = f2_add(x2[j], shift2);
+                    }
+                    auto weights = [&](int j) {
+                        float d0, d1;
+                        f2_unpack(x2[j], d0, d1);
+                        d0 = ex2_approx(d0);
+                        d1 = ex2_approx(d1);
+                        rsum2[j & 1] = f2_add(rsum2[j & 1], f2_pack(d0, d1));
+                        return pack_bf16x2(d0, d1);
+                    };
+                    if constexpr (C::kSepP) {
+                        uint32_t pk[64];
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) pk[j] = weights(j);
+                        if (cnt_total > 0 && !warp_wait(&ms.pv_done[i], (cnt_total - 1) & 1u, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        rescale_o(alpha);
+#pragma unroll
+                        for (int gq = 0; gq < 4; ++gq)
+                            tmem_st16(p_addr + 16 * gq, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * gq]));
+                    } else {
+                        rescale_o(alpha);
+#pragma unroll
+                        for (int gq = 0; gq < 4; ++gq) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int t2 = 0; t2 < 16; ++t2) pk[t2] = weights(16 * gq + t2);
+                            tmem_st16(p_addr + 16 * gq, pk);
+                        }
                     }
                 }
                 tmem_wait_st();
+                // PV waits for P alone: P says that the values were looked through as well
+                if (!full && !warp_wait(&ms.v_clean[stage], clean & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_before_sync();
                 mbar_arrive(&ms.p_full[i]);
                 float r0, r1, r2, r3;
@@ -760,54 +888,54 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             // ---------------------------------------------------- epilogue
             bool have = ok && cnt > 0;
-            if (have && !warp_wait(&ms.o_full[C::kSepP ? i : 0], nq & 1u, abort_flag)) {
+            if (have && !warp_wait(&ms.o_full[i], nq & 1u, abort_flag)) {
                 have = false;
                 ok = false;
             }
             if (!ok) record_failure(ms, p.status);
             if (ok) {
                 tc_fence_after_sync();
-                __threadfence_block();
                 const bool odd = sl.odd != 0;
-                const int64_t row = sl.q_row + token;
-                uint16_t *dst = p.out + h * p.out_stride[0] + row * p.out_stride[1];
+                const Row row = row_of(sl);
+                const int64_t token = sl.q_row + row.token;
+                uint16_t *dst = p.out + row.h * p.out_stride[0] + token * p.out_stride[1];
                 const bool kept = have && l_run != 0.f;  // NaN stays
                 const float inv = kept ? 1.f / l_run : 0.f;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    uint32_t o[64];
                     if (have) {
-                        tmem_ld32_sync(o_addr + c0, o);
+                        tmem_ld64_sync(o_addr + c0, o);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+                        for (int j = 0; j < 64; ++j) o[j] = 0u;
                     }
-                    uint32_t pk[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        pk[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-                        if (!kept) pk[j] = 0u;
-                    }
-                    if (live_row) {
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            pk[j] = pack_bf16x2(__uint_as_float(o[c + 2 * j]) * inv, __uint_as_float(o[c + 2 * j + 1]) * inv);
+                            if (!kept) pk[j] = 0u;
+                        }
+                        if (!row.live) continue;
                         if (p.wide_out) {  // whole 32-byte sectors per store
-                            st_global_32B(dst + c0, &pk[0]);
-                            st_global_32B(dst + c0 + 16, &pk[8]);
+                            st_global_32B(dst + c0 + c, pk);
                         } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                *reinterpret_cast<uint4 *>(dst + c0 + 8 * j) =
-                                    make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                            *reinterpret_cast<uint4 *>(dst + c0 + c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            *reinterpret_cast<uint4 *>(dst + c0 + c + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                         }
                     }
                 }
-                if (live_row) p.lse[(int64_t)h * p.total_q + row] = kept ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
-                if (odd && live_row) {
+                if (row.live) p.lse[(int64_t)row.h * p.total_q + token] = kept ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+                if (odd && row.live) {
                     // the values that were zeroed, of the columns that this row keeps, on top of what was stored
-                    const RowKeep keep = kept_columns();
+                    const int k_len = sl.k_len;
+                    const RowKeep keep = packed_keep(p.mask, row.pos, k_len);
 #pragma unroll 1
                     for (int u = 0; u < nu; ++u) {
-                        if (!sl.need[i].has(u) || sl.clean.has(u)) continue;
-                        const int kv0 = (u < n_main ? hi - u : nu - 1 - u) * kBlock;
+                        if (!sl.need[i].has(u) || sl.full.has(u)) continue;
+                        const int kv0 = (u < sl.n_main ? sl.hi - u : nu - 1 - u) * kBlock;
 #pragma unroll 1
                         for (int kv = kv0; kv < kv0 + kBlock && kv < k_len; ++kv) {
                             if (!((kv >= keep.lo && kv <= keep.hi) || kv <= keep.sink)) continue;
@@ -821,7 +949,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
             }
-          }
           if (nu > 0) {
               g += (uint32_t)nu;
               ++nq;
@@ -841,7 +968,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 }
 
-template <int D, int SCORE>
+template <int D, int SCORE, bool SHORT>
 cudaError_t launch_packed_kernel(const PackedProblem &p, const PackedParams &kp, cudaStream_t stream) {
     using C = PackedCfg<D>;
     CUtensorMap tq, tk, tv;
@@ -854,7 +981,7 @@ cudaError_t launch_packed_kernel(const PackedProblem &p, const PackedParams &kp,
         !make_tile_map_3d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_tile_map_3d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kd, vs, kb, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    auto kernel = attn_packed_kernel<D, SCORE>;
+    auto kernel = attn_packed_kernel<D, SCORE, SHORT>;
     // the register split assumes exactly kRegsAtLaunch registers at launch
     cudaFuncAttributes attr;
     cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
@@ -866,16 +993,21 @@ cudaError_t launch_packed_kernel(const PackedProblem &p, const PackedParams &kp,
     return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_packed_dim(const PackedProblem &p, const PackedParams &kp, cudaStream_t stream) {
+template <int D, bool SHORT>
+cudaError_t launch_packed_score(const PackedProblem &p, const PackedParams &kp, cudaStream_t stream) {
     switch (p.score_kind) {
         case FLEX_SCORE_SOFTCAP:
-            return launch_packed_kernel<D, FLEX_SCORE_SOFTCAP>(p, kp, stream);
+            return launch_packed_kernel<D, FLEX_SCORE_SOFTCAP, SHORT>(p, kp, stream);
         case FLEX_SCORE_ALIBI:
-            return launch_packed_kernel<D, FLEX_SCORE_ALIBI>(p, kp, stream);
+            return launch_packed_kernel<D, FLEX_SCORE_ALIBI, SHORT>(p, kp, stream);
         default:
-            return launch_packed_kernel<D, FLEX_SCORE_IDENTITY>(p, kp, stream);
+            return launch_packed_kernel<D, FLEX_SCORE_IDENTITY, SHORT>(p, kp, stream);
     }
+}
+
+template <int D>
+cudaError_t launch_packed_dim(const PackedProblem &p, const PackedParams &kp, cudaStream_t stream) {
+    return kp.few_tiles ? launch_packed_score<D, true>(p, kp, stream) : launch_packed_score<D, false>(p, kp, stream);
 }
 
 cudaError_t launch_packed_d64(const PackedProblem &p, const PackedParams &kp, cudaStream_t stream);

@@ -18,7 +18,7 @@ BF16 = torch.bfloat16
 MASKS = [(fa.FLEX_MASK_CAUSAL, 0, 0), (fa.FLEX_MASK_SLIDING_WINDOW, 5, 0), (fa.FLEX_MASK_SLIDING_WINDOW, 0, 0),
          (fa.FLEX_MASK_SLIDING_WINDOW, 200, 0), (fa.FLEX_MASK_WINDOW_SINKS, 33, 4), (fa.FLEX_MASK_WINDOW_SINKS, 1, 170),
          (fa.FLEX_MASK_WINDOW_SINKS, 0, 3), (fa.FLEX_MASK_WINDOW_SINKS, 2**31 - 1, 2**31 - 1),
-         (fa.FLEX_MASK_WINDOW_SINKS, 130, 129), (fa.FLEX_MASK_ALL, 0, 0)]
+         (fa.FLEX_MASK_WINDOW_SINKS, 130, 129), (fa.FLEX_MASK_ALL, 0, 0), (fa.FLEX_MASK_WINDOW_SINKS, 300, 20)]
 SCORES = (fa.FLEX_SCORE_IDENTITY, fa.FLEX_SCORE_SOFTCAP, fa.FLEX_SCORE_ALIBI)
 
 
@@ -109,12 +109,12 @@ def running(lens, first=0):
 def test_masks_and_lengths(D, Hk, G, order):
     """Ragged prompts (empty, one token, tile ends) at every mask and score; tokens before and behind all of them."""
     gen = torch.Generator().manual_seed(D + 10 * G)
-    lens = [5, 0, 1, 128, 300, 127, 129, 2, 33]
-    qs = running(lens, 3)
-    q = tokens(gen, qs[-1] + 9, Hk * G, D, order)
-    k, v = (tokens(gen, qs[-1] + 9, Hk, D, order) for _ in range(2))
-    for i, (kind, window, sinks) in enumerate(MASKS):
-        compare(q, k, v, qs, qs, kind, window, sinks, SCORES[i % 3])
+    for lens in ([5, 0, 1, 128, 300, 127, 129, 2, 33], [700, 1, 384]):  # few kv tiles a sequence, and more
+        qs = running(lens, 3)
+        q = tokens(gen, qs[-1] + 9, Hk * G, D, order)
+        k, v = (tokens(gen, qs[-1] + 9, Hk, D, order) for _ in range(2))
+        for i, (kind, window, sinks) in enumerate(MASKS):
+            compare(q, k, v, qs, qs, kind, window, sinks, SCORES[i % 3])
 
 
 @pytest.mark.parametrize("D,Hk,G", [(64, 2, 4), (128, 1, 6), (128, 2, 1), (64, 1, 20)])
@@ -160,12 +160,13 @@ def test_large_scores(score, cap):
 
 @pytest.mark.parametrize("D,G", [(64, 4), (128, 4), (128, 1), (64, 1)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (70, 2)])
-@pytest.mark.parametrize("at", [10, 200, 259])
-def test_not_finite_where_masked(D, G, window, sinks, at):
+@pytest.mark.parametrize("at,last", [(10, 50), (200, 50), (259, 50), (10, 1500), (200, 1500), (259, 1500)])
+def test_not_finite_where_masked(D, G, window, sinks, at, last):
     """A value or key that is not finite reaches exactly the rows of its sequence that keep it."""
     gen = torch.Generator().manual_seed(D + G)
     kind = fa.FLEX_MASK_WINDOW_SINKS if window else fa.FLEX_MASK_CAUSAL
-    lens = [37, 260, 50]
+    lens = [37, 260, last]  # the longer last one: kernels of many kv tiles
+    window += last if window and last > 50 else 0
     qs = running(lens)
     q, k, v = (tokens(gen, qs[-1], h, D, "thd") for h in (2 * G, 2, 2))
     plan = fa.flex_packed_plan_create(ints(qs), None, qs[-1], None, 2 * G, 2, kind, window, sinks)
