@@ -20,7 +20,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kJoinThreads = 512;
 constexpr int kJoinMany = 8;       // warps of the main launch per pair, from which CTAs join a row
-constexpr int kMaxCtas = 152 * 2;  // of the main launch: two on every SM
+constexpr int kSms = 152, kMostPerSm = 4;  // CTAs of the main launch on every SM: two to four
 constexpr float kLog2e = kLog2eF;
 constexpr float kLn2 = 0.6931471805599453f;
 // Entering and finishing a (sequence, head, row tile) costs a warp the time of
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(32 * ROWS) cache_attention_join_few_kernel(con
 template <int D, int ROWS, int TOKENS>
 __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(const CacheAttnProblem p, int row_tiles) {
     constexpr int kColumns = 16, kGroups = kJoinThreads / kColumns, kJoinWarps = kJoinThreads / 32;
-    __shared__ float top_s[kJoinWarps], sum_s[kJoinWarps], factor[kMaxCtas * kWarps];
+    __shared__ float top_s[kJoinWarps], sum_s[kJoinWarps], factor[kSms * kMostPerSm * kWarps];
     __shared__ float2 value_s[kJoinWarps][kColumns];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int pairs_per_seq = p.cache.H * row_tiles, warp = threadIdx.x / 32;
@@ -371,7 +371,7 @@ int tile_rows(const CacheAttnProblem &p) { return (int64_t)p.Q * p.G <= 8 ? 8 : 
 
 // CTAs of the main launch: one wave, or as many as there can be steps, from
 // what the host knows of the lengths.
-int64_t main_ctas(const CacheAttnProblem &p, int tokens) {
+int64_t main_ctas(const CacheAttnProblem &p, int tokens, int per_sm = 2) {
     const int rows = tile_rows(p);
     const int64_t pairs = (int64_t)p.B * p.cache.H * (((int64_t)p.Q * p.G + rows - 1) / rows);
     int64_t most = (int64_t)p.max_pages * p.cache.page;
@@ -379,16 +379,16 @@ int64_t main_ctas(const CacheAttnProblem &p, int tokens) {
         const int64_t w = (int64_t)p.window + p.sinks + p.Q + 2 * tokens;
         most = most < w ? most : w;
     }
-    const int64_t steps = pairs * ((most + tokens - 1) / tokens + 1), wave = kMaxCtas;
+    const int64_t steps = pairs * ((most + tokens - 1) / tokens + 1), wave = kSms * per_sm;
     return steps < wave ? steps : wave;
 }
 
 template <int D, int ROWS, int TOKENS>
-cudaError_t launch_join(const CacheAttnProblem &p, int row_tiles, int64_t pairs, cudaStream_t stream) {
+cudaError_t launch_join(const CacheAttnProblem &p, int row_tiles, int64_t pairs, cudaStream_t stream, int per_sm = 2) {
     // the join is launched while the main kernel runs and waits for its end on
     // the device, which hides its launch
     cudaLaunchConfig_t cfg = {};
-    const bool many = main_ctas(p, TOKENS) * kWarps >= pairs * kJoinMany;
+    const bool many = main_ctas(p, TOKENS, per_sm) * kWarps >= pairs * kJoinMany;
     const int live = (int)((int64_t)p.Q * p.G < ROWS ? (int64_t)p.Q * p.G : ROWS);
     cfg.gridDim = dim3((unsigned)pairs, many ? live : 1, many ? D / 32 : 1);
     cfg.blockDim = dim3(many ? kJoinThreads : 32 * ROWS);

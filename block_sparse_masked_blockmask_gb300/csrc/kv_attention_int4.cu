@@ -35,45 +35,62 @@ namespace {
 
 constexpr float kLeastRef = 0x1p-60f;
 
-// fp16x2 of the codes at nibble N of both halves of a word, less 8, exactly.
+// The codes at nibble N of both halves of a word as fp16x2: their bits alone are
+// subnormal numbers.  The tensor core cuts products off some 2^-24 below what a
+// number of that exponent could be at most, so the higher a code's bits lie, the
+// more is left.  Values: where the nibble lies in its byte, code 2^-24 (N even,
+// off by 2^-17 of the largest product) or code 2^-20 (N odd): what counts is their
+// sum, and its last place soon outweighs that.  Keys: two bits further up, code
+// 2^-22 or code 2^-18 (2^-19 and 2^-23), since a score's error stays in lse however
+// short a sequence is.
 template <int N>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
-    const uint32_t x = N >= 2 ? w >> 8 : w;
-    uint32_t r;
-    if constexpr (N % 2 == 0)
-        asm("{\n\t.reg .b32 h;\n\tlop3.b32 h, %1, 0x000F000F, 0x64006400, 0xEA;\n\t"
-            "add.rn.f16x2 %0, h, %2;\n\t}" : "=r"(r) : "r"(x), "r"(0xE408E408u));  // - 1032
-    else
-        asm("{\n\t.reg .b32 h;\n\tlop3.b32 h, %1, 0x00F000F0, 0x64006400, 0xEA;\n\t"
-            "fma.rn.f16x2 %0, h, %2, %3;\n\t}" : "=r"(r) : "r"(x), "r"(0x2C002C00u), "r"(0xD480D480u));  // / 16, - 72
-    return r;
+__device__ __forceinline__ uint32_t value_codes(uint32_t w) {
+    return (N >= 2 ? w >> 8 : w) & (N % 2 ? 0x00F000F0u : 0x000F000Fu);
+}
+template <int N>
+__device__ __forceinline__ uint32_t key_codes(uint32_t w) {
+    return (N >= 2 ? w >> 6 : w << 2) & (N % 2 ? 0x03C003C0u : 0x003C003Cu);
+}
+constexpr uint32_t kEight = 0x00800080u;  // the code 8 as code 2^-20, in both halves
+// query rows are scaled to below 2^11, and 16 times that where they meet codes of even nibbles
+constexpr int kQueryUp = 10;
+constexpr float kScoreUnit = 0x1p8f;      // products of codes and such queries are in units of 2^-8
+
+// c + a b: the same products with sums of their own.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                              float c1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
 template <int D, int NT>
 struct Cfg4 {
     static constexpr int kRowBytes = D / 2;             // of codes; TMA swizzle span
     static constexpr int kGroups = D / 32;
-    static constexpr int kTokens = 64;                  // of a step
+    static constexpr int kTokens = 32;                  // of a step
     static constexpr int kSub = kTokens / 16;
-    static constexpr int kStages = 2;
+    static_assert(kSub == 2, "a step's info has bits for two groups, and its first token leaves five free");
+    static constexpr int kStages = 3;
+    static constexpr int kPerSm = NT == 1 ? 3 : 2;      // CTAs
     static constexpr int kSteps = D / 16;               // k16 steps of S, m16 tiles of O
     static constexpr int kRows = 8 * NT;
     static constexpr int kCodes = kTokens * kRowBytes;  // bytes of a step's keys, or values
     static constexpr int kKeyScales = kTokens * kGroups * 2, kValueScales = kTokens * 2;
     static constexpr int kSlot = (2 * kCodes + kKeyScales + kValueScales + 511) / 512 * 512;
     static constexpr int kRing = kStages * kSlot;
-    static constexpr int kQBytes = NT * kSteps * 32 * 8;
-    static constexpr int kSmem = 1024 + kWarps * (kRing + kQBytes);
+    static constexpr int kSmem = 1024 + kWarps * kRing;
 };
 
 struct Misc4 {
-    uint64_t k_full[kWarps][2], v_full[kWarps][2];
+    uint64_t full[kWarps][4];
     int64_t sums[kWarps];
     int abort;
 };
 
 template <int D, int NT, bool CAP>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
     cache_attention_int4_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                                 const CacheAttnProblem p, int row_tiles, int box_rows) {
     using C = Cfg4<D, NT>;
@@ -90,10 +107,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
         for (int w = 0; w < kWarps; ++w)
-            for (int s = 0; s < ST; ++s) {
-                mbar_init(&ms.k_full[w][s], 1);
-                mbar_init(&ms.v_full[w][s], 1);
-            }
+            for (int s = 0; s < ST; ++s) mbar_init(&ms.full[w][s], 1);
         ms.abort = 0;
         fence_barrier_init();
     }
@@ -104,13 +118,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!take_share<C::kTokens>(p, pairs_per_seq, ms.sums, b, off, steps, worker)) return;
 
     // ---- steps ahead of the computation.  Lane i looks up the warp's step
-    // 32 k + i: its first token, and of its 16-token groups page * heads + head,
-    // or -1 where there is nothing that a row keeps.  The groups of one box share
-    // a page.
+    // 32 k + i and asks for its copies when its turn comes: of its 16-token groups
+    // page * heads + head, or -1 where there is nothing that a row keeps (the groups of
+    // one box share a page).  The others get its first token, a multiple of 32, and
+    // in the low bits which groups are there (1, 2), and whether every row keeps all of it (4).
     int look_b = b;
     int64_t look_off = off;
     int looked = 0;
-    int base_lane = 0, ph_lane[SUB];
+    int info_lane = 0, ph_lane[SUB];
     auto lookup = [&]() {
         int lb = look_b;
         int64_t lo_ = look_off + lane;
@@ -122,61 +137,60 @@ __global__ void __launch_bounds__(kThreads, 2)
         const bool live = looked + lane < steps;
         const int pair = (int)(lo_ / sq.count), hk = pair / row_tiles, r0 = pair % row_tiles * C::kRows;
         const int tmin = r0 / p.G, tmax = (min(r0 + C::kRows, p.Q * p.G) - 1) / p.G;
+        // what any row of the tile keeps, [0, send) and [lo_min, hi), and what every row does
         const int hi = p.causal ? max(sq.n - p.Q + tmax + 1, 0) : sq.n;
         const int64_t lo_min = p.causal ? max((int64_t)sq.n - p.Q + tmin - p.window + 1, (int64_t)0) : 0;
         const int send = min(p.sinks, hi);
-        base_lane = sq.base((int)(lo_ % sq.count), C::kTokens);
+        const int all_hi = p.causal ? sq.n - p.Q + tmin + 1 : (sq.n - p.Q + tmin >= 0 ? sq.n : 0);
+        const int64_t all_lo = p.causal ? max((int64_t)sq.n - p.Q + tmax - p.window + 1, (int64_t)0) : 0;
+        const int base = sq.base((int)(lo_ % sq.count), C::kTokens);
         const int *table = p.page_table + (int64_t)lb * p.max_pages;
+        bool whole = base + C::kTokens <= all_hi && (base >= all_lo || base + C::kTokens <= p.sinks);
+        info_lane = base;
 #pragma unroll
         for (int j = 0; j < SUB; ++j) {
-            const int at = base_lane + 16 * j, box = at & ~(box_rows - 1);
+            const int at = base + 16 * j, box = at & ~(box_rows - 1);
             ph_lane[j] = -1;
             if (live && box < hi && (box + box_rows > lo_min || box < send)) {
                 const int id = __ldg(table + (at >> p.cache.page_shift));
                 if (id >= 0 && id < p.cache.num_pages) ph_lane[j] = id * p.cache.H + hk;
             }
+            whole = whole && ph_lane[j] >= 0;
+            info_lane |= ph_lane[j] >= 0 ? 1 << j : 0;
         }
+        info_lane |= whole ? 4 : 0;
         // the next batch begins where lane 31's successor would be
         look_b = __shfl_sync(0xffffffffu, lb, 31);
         look_off = __shfl_sync(0xffffffffu, lo_, 31) + 1;
         looked += 32;
     };
-    // one step's keys (or values) and their scales into ring slot `slot` (lane 0); `after` is 0
-    auto fetch = [&](bool is_v, int slot, uint32_t after, int base, const int (&ph)[SUB]) {
-        if (lane == 0) {
-            uint8_t *codes = ring + slot * C::kSlot + (is_v ? C::kCodes : 0) + after;
-            uint8_t *scales = ring + slot * C::kSlot + 2 * C::kCodes + (is_v ? C::kKeyScales : 0) + after;
-            uint64_t *bar = is_v ? &ms.v_full[warp][slot] : &ms.k_full[warp][slot];
-            const int row = is_v ? 2 : 2 * J;  // bytes of a token's scales
-            const uint8_t *from = reinterpret_cast<const uint8_t *>(is_v ? p.cache.v_scale : p.cache.k_scale);
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int j = 0; j < SUB; ++j) bytes += ph[j] >= 0 ? 16u * (C::kRowBytes + row) : 0u;
-            mbar_arrive_expect_tx(bar, bytes);
+    // the warp's step i, its keys, values and their scales, into ring slot `slot`; `after` is 0
+    auto fetch = [&](int i, int slot, uint32_t after) {
+        if (lane == i % 32) {
+            uint8_t *dst = ring + slot * C::kSlot + after;
+            uint64_t *bar = &ms.full[warp][slot];
+            constexpr uint32_t kGroup = 16u * (2 * C::kRowBytes + 2 * J + 2);
+            mbar_arrive_expect_tx(bar, kGroup * (uint32_t)__popc(info_lane & 3));
 #pragma unroll
             for (int j = 0; j < SUB; ++j)
-                if (ph[j] >= 0 && ((16 * j) & (box_rows - 1)) == 0) {
-                    const int at = (base + 16 * j) & (page - 1);
-                    tma_load_3d(codes + 16 * j * C::kRowBytes, is_v ? &map_v : &map_k, bar, 0, at, ph[j]);
-                    bulk_load(scales + 16 * j * row, from + ((int64_t)ph[j] * page + at) * row, box_rows * row, bar);
+                if (ph_lane[j] >= 0 && (j == 0 || box_rows == 16)) {
+                    const int at = ((info_lane & ~(C::kTokens - 1)) + 16 * j) & (page - 1);
+                    const int64_t row = (int64_t)ph_lane[j] * page + at;
+                    tma_load_3d(dst + 16 * j * C::kRowBytes, &map_k, bar, 0, at, ph_lane[j]);
+                    bulk_load(dst + 2 * C::kCodes + 16 * j * 2 * J,
+                              reinterpret_cast<const uint8_t *>(p.cache.k_scale) + row * 2 * J, box_rows * 2 * J, bar);
+                    tma_load_3d(dst + C::kCodes + 16 * j * C::kRowBytes, &map_v, bar, 0, at, ph_lane[j]);
+                    bulk_load(dst + 2 * C::kCodes + C::kKeyScales + 16 * j * 2,
+                              reinterpret_cast<const uint8_t *>(p.cache.v_scale) + row * 2, box_rows * 2, bar);
                 }
         }
     };
-    // of the current step and the ST - 1 behind it
-    int base_of[ST], ph[ST][SUB];
-    auto take_place = [&](int i, int &base, int (&to)[SUB]) {
-        base = __shfl_sync(0xffffffffu, base_lane, i);
-#pragma unroll
-        for (int j = 0; j < SUB; ++j) to[j] = __shfl_sync(0xffffffffu, ph_lane[j], i);
-    };
+    int info[ST];  // of the current step and the ST - 1 behind it
     lookup();
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
-        take_place(s, base_of[s], ph[s]);
-        if (s < steps) {
-            fetch(false, s, 0u, base_of[s], ph[s]);
-            fetch(true, s, 0u, base_of[s], ph[s]);
-        }
+        info[s] = __shfl_sync(0xffffffffu, info_lane, s);
+        if (s < steps) fetch(s, s, 0u);
     }
 
     const uint32_t nothing = (uint32_t)p.cache.page & 1u;  // 0, which the compiler does not know
@@ -196,11 +210,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     int pair = (int)(off / sq.count), at_step = (int)(off % sq.count);
     bool entering = true, whole_start = false;
     int hk = 0, r0 = 0, r1 = 0, n = 0;
-    int all_hi = 0, all_lo = 0;
     float slope[NT][2], qscale[NT][2];  // of this thread's rows, columns 2t and 2t + 1 of each row tile (base-2 units)
     int pos[NT][2], seen[NT][2];        // position, and the last kv it keeps (-1: nothing)
-    float m[NT][2], l[NT][2], acc[NT][KS][4];
-    uint2 *qs = reinterpret_cast<uint2 *>(smem + kWarps * C::kRing + warp * C::kQBytes);
+    float m[NT][2], l[NT][2], acc[NT][KS][4], eights[NT][4];
+    uint2 q[NT][KS];                    // Q operand
+    float less[NT][J][2];               // -8 2^-18 times the sum of a row's values of each group
 
     // ---- the end of a piece: the pair's rows where the warp covered all of its
     // steps, else a partial result
@@ -223,10 +237,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
                     const int d = 32 * (i / 2) + 4 * g + 2 * (i % 2);
+                    const float a = (acc[nt][i][u] - eights[nt][u] * 0.0625f) * 0x1p24f,
+                                z = (acc[nt][i][u + 2] - eights[nt][u]) * 0x1p20f;
                     if (whole_start && whole_end)
-                        store_pair<D>(p, b, hk, r0 + r, d, acc[nt][i][u], acc[nt][i][u + 2], m[nt][u], l[nt][u]);
+                        store_pair<D>(p, b, hk, r0 + r, d, a, z, m[nt][u], l[nt][u]);
                     else
-                        *reinterpret_cast<float2 *>(part + r * D + d) = make_float2(acc[nt][i][u], acc[nt][i][u + 2]);
+                        *reinterpret_cast<float2 *>(part + r * D + d) = make_float2(a, z);
                 }
                 if (!(whole_start && whole_end) && g == 0)
                     *reinterpret_cast<float2 *>(part + C::kRows * D + 2 * r) = make_float2(m[nt][u], l[nt][u]);
@@ -235,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     int slot = 0;
     uint32_t phase = 0;
-    bool ok = true, refetched = false;  // refetched: this slot's next keys were already asked for
+    bool ok = true;
     int it = 0;
     for (; it < steps; ++it) {
         if (entering) {
@@ -246,10 +262,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             // rows of this tile: r = query token * G + head within the group
             r0 = pair % row_tiles * C::kRows;
             r1 = min(r0 + C::kRows, p.Q * p.G) - 1;
-            const int tmin = r0 / p.G, tmax = r1 / p.G;
-            // what every row keeps, for steps without mask work
-            all_hi = p.causal ? n - p.Q + tmin + 1 : (n - p.Q + tmin >= 0 ? n : 0);
-            all_lo = p.causal ? (int)max((int64_t)n - p.Q + tmax - p.window + 1, (int64_t)0) : 0;
             // Q operand: lane (g, t) takes row g at the head dims of its key pieces
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -271,23 +283,32 @@ __global__ void __launch_bounds__(kThreads, 2)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // rows are divided by the power of two of their largest magnitude, so
                 // that they fit fp16 (bf16 values keep all their bits down to 2^-14
-                // of it); by 1 where they are zero or not finite
+                // of it and further); by 1 where they are zero or not finite
                 const uint32_t e = top >> 7;
-                const float qf = e == 0u || e == 255u ? 1.f : __uint_as_float(e << 23), f = 1.f / qf;
+                const float qf = e == 0u || e == 255u ? 1.f : __uint_as_float(e << 23);
+                const float f = 1.f / qf * (float)(1 << kQueryUp);
+                float sum[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     // values 0 .. 7 as the pairs (0, 4), (1, 5), (2, 6), (3, 7)
                     const uint32_t lo[2] = {w[j].x, w[j].y}, hi[2] = {w[j].z, w[j].w};
                     uint32_t r[4];
+                    sum[j] = 0.f;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const uint32_t a = lo[c / 2], z = hi[c / 2];
-                        r[c] = pack_f16x2(__uint_as_float(c % 2 ? a & 0xFFFF0000u : a << 16) * f,
-                                          __uint_as_float(c % 2 ? z & 0xFFFF0000u : z << 16) * f);
+                        const float up = c % 2 ? f : f * 16.f;
+                        r[c] = pack_f16x2(__uint_as_float(c % 2 ? a & 0xFFFF0000u : a << 16) * up,
+                                          __uint_as_float(c % 2 ? z & 0xFFFF0000u : z << 16) * up);
+                        const __half2 h = *reinterpret_cast<const __half2 *>(&r[c]);
+                        sum[j] += (__low2float(h) + __high2float(h)) * (c % 2 ? 1.f : 0.0625f);
                     }
-                    // read back by this lane alone
-                    qs[(nt * KS + 2 * j) * 32 + lane] = make_uint2(r[0], r[1]);
-                    qs[(nt * KS + 2 * j + 1) * 32 + lane] = make_uint2(r[2], r[3]);
+                    q[nt][2 * j] = make_uint2(r[0], r[1]);
+                    q[nt][2 * j + 1] = make_uint2(r[2], r[3]);
+                    sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
+                    sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) less[nt][j][u] = -0x1p-15f * __shfl_sync(0xffffffffu, sum[j], (2 * t + u) * 4);
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -295,225 +316,185 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const bool in = rw <= r1;
                     pos[nt][u] = n - p.Q + (in ? rw / p.G : 0);
                     seen[nt][u] = in && pos[nt][u] >= 0 ? (p.causal ? pos[nt][u] : n - 1) : -1;
-                    qscale[nt][u] = p.scale * __shfl_sync(0xffffffffu, qf, (2 * t + u) * 4) * (CAP ? 1.f : kLog2e);
+                    qscale[nt][u] = p.scale * kScoreUnit * (CAP ? 1.f : kLog2e) * __shfl_sync(0xffffffffu, qf, (2 * t + u) * 4);
                     slope[nt][u] = exp2f(-8.f * (float)(hk * p.G + (in ? rw % p.G : 0) + 1) / (float)p.Hq) * kLog2e;
                     m[nt][u] = -FLT_MAX;
                     l[nt][u] = 0.f;
                 }
 #pragma unroll
                 for (int i = 0; i < KS; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+                eights[nt][0] = eights[nt][1] = eights[nt][2] = eights[nt][3] = 0.f;
             }
         }
-        const int base = base_of[0];
-        const bool more = it + ST < steps;
-        int base_next, ph_next[SUB];
-        if (more && it + ST == looked) lookup();
-        take_place((it + ST) % 32, base_next, ph_next);
-        bool whole = base + C::kTokens <= all_hi && (base >= all_lo || base + C::kTokens <= p.sinks);
-#pragma unroll
-        for (int j = 0; j < SUB; ++j) whole = whole && ph[0][j] >= 0;
+        const int base = info[0] & ~(C::kTokens - 1);
+        const bool whole = info[0] & 4;
         const uint32_t k_at = ring_at + slot * C::kSlot, v_at = k_at + C::kCodes, ks_at = k_at + 2 * C::kCodes,
                        vs_at = ks_at + C::kKeyScales;
-        // ---- S^T = K Q^T
-        if (!__all_sync(0xffffffffu, mbar_wait(&ms.k_full[warp][slot], phase, &ms.abort))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ms.full[warp][slot], phase, &ms.abort))) {
             ok = false;
             break;
         }
-        uint32_t kw[SUB][2][J], kscale[SUB][2][J / 2];
-#pragma unroll
-        for (int j = 0; j < SUB; ++j)
+        uint32_t last = 0u;
+        // 16 tokens at a time; more at once and the loop outgrows the instruction cache
+#pragma unroll 1
+        for (int j = 0; j < SUB; ++j) {
+            // ---- S^T = K Q^T
+            uint32_t kw[2][J], kscale[2][J / 2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                load_shared<4 * J>(kw[j][r], k_at + koff + (16 * j + 8 * r) * C::kRowBytes);
-                load_words<J / 2>(kscale[j][r], ks_at + (16 * j + 8 * r + g) * 2 * J);
+                load_shared<4 * J>(kw[r], k_at + koff + (16 * j + 8 * r) * C::kRowBytes);
+                load_words<J / 2>(kscale[r], ks_at + (16 * j + 8 * r + g) * 2 * J);
             }
-        __syncwarp();
-        if (more)  // the slot is free as soon as its words are in registers
-            fetch(false, slot, zero_after(kscale[SUB - 1][1][J / 2 - 1] ^ kw[SUB - 1][1][J - 1], nothing),
-                  base_next, ph_next);
-        float x[NT][SUB][4];
+            uint32_t v[4][J / 2];
+            float vs[2];  // of tokens g and g + 8
 #pragma unroll
-        for (int i = 0; i < J; ++i) {
-            uint2 q[2][NT];
+            for (int r = 0; r < 4; ++r)
+                load_words<J / 2>(v[r], v_at + voff + ((r & 1) + 8 * (r >> 1) + 16 * j) * C::kRowBytes);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                q[0][nt] = qs[(nt * KS + 2 * i) * 32 + lane];
-                q[1][nt] = qs[(nt * KS + 2 * i + 1) * 32 + lane];
-            }
+            for (int r = 0; r < 2; ++r) vs[r] = __uint_as_float(load_u16(vs_at + (16 * j + 8 * r + g) * 2) << 16);
+            last = __float_as_uint(vs[1]);
+            float x[NT][4];
 #pragma unroll
-            for (int j = 0; j < SUB; ++j) {
+            for (int i = 0; i < J; ++i) {
                 uint32_t w[2];  // the group's eight codes of keys g and g + 8
                 float s[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint32_t sel = i % 2 ? 0x7632u : 0x5410u;
-                    w[r] = prmt(kw[j][r][i / 2], kw[j][r][J / 2 + i / 2], sel);
-                    s[r] = __uint_as_float(i % 2 ? kscale[j][r][i / 2] & 0xFFFF0000u : kscale[j][r][i / 2] << 16);
+                    w[r] = prmt(kw[r][i / 2], kw[r][J / 2 + i / 2], i % 2 ? 0x7632u : 0x5410u);
+                    s[r] = __uint_as_float(i % 2 ? kscale[r][i / 2] & 0xFFFF0000u : kscale[r][i / 2] << 16);
                 }
-                const uint32_t a0[4] = {codes_f16<0>(w[0]), codes_f16<0>(w[1]), codes_f16<1>(w[0]), codes_f16<1>(w[1])};
-                const uint32_t a1[4] = {codes_f16<2>(w[0]), codes_f16<2>(w[1]), codes_f16<3>(w[0]), codes_f16<3>(w[1])};
+                const uint32_t a0[4] = {key_codes<0>(w[0]), key_codes<0>(w[1]), key_codes<1>(w[0]), key_codes<1>(w[1])};
+                const uint32_t a1[4] = {key_codes<2>(w[0]), key_codes<2>(w[1]), key_codes<3>(w[0]), key_codes<3>(w[1])};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16816<true>(d, a0, q[0][nt].x, q[0][nt].y);
-                    mma16816<true>(d, a1, q[1][nt].x, q[1][nt].y);
+                    float d[4];
+                    mma16816_from(d, a0, q[nt][2 * i].x, q[nt][2 * i].y, less[nt][i][0], less[nt][i][1]);
+                    mma16816<true>(d, a1, q[nt][2 * i + 1].x, q[nt][2 * i + 1].y);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[nt][j][e] = i == 0 ? d[e] * s[e >> 1] : fmaf(d[e], s[e >> 1], x[nt][j][e]);
+                    for (int e = 0; e < 4; ++e) x[nt][e] = i == 0 ? d[e] * s[e >> 1] : fmaf(d[e], s[e >> 1], x[nt][e]);
                 }
             }
-        }
-        // ---- the values into registers, and their slot free again
-        if (!__all_sync(0xffffffffu, mbar_wait(&ms.v_full[warp][slot], phase, &ms.abort))) {
-            ok = false;
-            refetched = more;
-            break;
-        }
-        uint32_t v[SUB][4][J / 2];
-        float vs[SUB][2];  // of tokens g and g + 8
-#pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                load_words<J / 2>(v[j][r], v_at + voff + ((r & 1) + 8 * (r >> 1) + 16 * j) * C::kRowBytes);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) vs[j][r] = __uint_as_float(load_u16(vs_at + (16 * j + 8 * r + g) * 2) << 16);
-        }
-        __syncwarp();
-        if (more)
-            fetch(true, slot, zero_after(__float_as_uint(vs[SUB - 1][1]), nothing), base_next, ph_next);
-
-        // ---- scores in base-2 units, masked
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < SUB; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[nt][j][e] *= qscale[nt][e & 1];
-        if constexpr (CAP) {
-            const float cap_in = fminf(2.f * kLog2e / p.score_param, FLT_MAX),
-                        cap_out = fminf(p.score_param * kLog2e, FLT_MAX);
+            // ---- scores in base-2 units, masked
+            const int kv0 = base + 16 * j + g;
+            // (rounded before the reference is taken off, as they are when one becomes the
+            // reference: fused, what is left of a score of 2^30 is its rounding)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < SUB; ++j)
+                for (int e = 0; e < 4; ++e) {
+                    x[nt][e] = __fmul_rn(x[nt][e], qscale[nt][e & 1]);
+                    if constexpr (CAP)
+                        x[nt][e] = softcap_log2(x[nt][e], fminf(2.f * kLog2e / p.score_param, FLT_MAX),
+                                                fminf(p.score_param * kLog2e, FLT_MAX));
+                }
+            if (!CAP && p.score_kind == FLEX_SCORE_ALIBI) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        x[nt][j][e] = softcap_log2(x[nt][j][e], cap_in, cap_out);
-        } else if (p.score_kind == FLEX_SCORE_ALIBI) {
+                        x[nt][e] = fmaf(-slope[nt][e & 1], (float)(pos[nt][e & 1] - (kv0 + (e >> 1) * 8)), x[nt][e]);
+            }
+            if (!whole) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < SUB; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[nt][j][e] -= slope[nt][e & 1] * (float)(pos[nt][e & 1] - (base + 16 * j + g + (e >> 1) * 8));
-        }
-        if (!whole) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < SUB; ++j)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int u = e & 1, kv = base + 16 * j + g + (e >> 1) * 8;
-                        const bool keep = ph[0][j] >= 0 && kv <= seen[nt][u] &&
+                        const int u = e & 1, kv = kv0 + (e >> 1) * 8;
+                        const bool keep = (info[0] >> j & 1) && kv <= seen[nt][u] &&
                                           (pos[nt][u] - kv < p.window || kv < p.sinks);
-                        if (!keep) x[nt][j][e] = -INFINITY;
+                        if (!keep) x[nt][e] = -INFINITY;
                     }
-        }
-        // ---- weights, and whether one exceeds what the reference allows
-        float ref[SUB][2];
+            }
+            // ---- w: weights, which the row's sum takes; y: times the value's scale
+            float w[NT][4], y[NT][4];
+            auto exponentials = [&]() {
 #pragma unroll
-        for (int j = 0; j < SUB; ++j)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) ref[j][r] = fmaxf(vs[j][r], kLeastRef);  // NaN: counts as the least
-        float w[NT][SUB][4];
-        bool raise = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < SUB; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[nt][j][e] = ex2_approx(x[nt][j][e] - m[nt][e & 1]);
-                    raise |= w[nt][j][e] * ref[j][e >> 1] > 0x1p15f;
-                }
-        if (__any_sync(0xffffffffu, raise)) {
-            float lr[SUB][2];
-#pragma unroll
-            for (int j = 0; j < SUB; ++j)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) lr[j][r] = log2f(ref[j][r]);
+                    for (int e = 0; e < 4; ++e) {
+                        w[nt][e] = ex2_approx(x[nt][e] - m[nt][e & 1]);
+                        y[nt][e] = w[nt][e] * vs[e >> 1];
+                    }
+            };
+            exponentials();
+            float most_y = 0.f, most_w = 0.f;  // NaN: passed over
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float alpha[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < SUB; ++j)
-                        top = fmax3(top, x[nt][j][u] + lr[j][0], x[nt][j][u + 2] + lr[j][1]);
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float now = top > m[nt][u] + kRaise - 0.0625f ? top - kTop : m[nt][u];
-                    alpha[u] = exp2f(m[nt][u] - now);
-                    m[nt][u] = now;
-                    l[nt][u] *= alpha[u];
-                }
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    acc[nt][i][0] *= alpha[0];
-                    acc[nt][i][1] *= alpha[1];
-                    acc[nt][i][2] *= alpha[0];
-                    acc[nt][i][3] *= alpha[1];
-                }
-#pragma unroll
-                for (int j = 0; j < SUB; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[nt][j][e] = ex2_approx(x[nt][j][e] - m[nt][e & 1]);
+                most_y = fmax3(fmax3(most_y, y[nt][0], y[nt][1]), y[nt][2], y[nt][3]);
+                most_w = fmax3(fmax3(most_w, w[nt][0], w[nt][1]), w[nt][2], w[nt][3]);
             }
-        }
-        // ---- P, the sum of weights, and P^T as operand
-        uint32_t pb[NT][SUB][2];
+            if (__any_sync(0xffffffffu, most_y > 0x1p15f || most_w > 0x1p15f / kLeastRef)) {
+                const float lr[2] = {log2f(fmaxf(vs[0], kLeastRef)), log2f(fmaxf(vs[1], kLeastRef))};
 #pragma unroll
-        for (int j = 0; j < SUB; ++j)
+                for (int nt = 0; nt < NT; ++nt) {
+                    float alpha[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float top = fmaxf(x[nt][u] + lr[0], x[nt][u + 2] + lr[1]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const float now = top > m[nt][u] + kRaise - 0.0625f ? top - kTop : m[nt][u];
+                        alpha[u] = exp2f(m[nt][u] - now);
+                        m[nt][u] = now;
+                        l[nt][u] *= alpha[u];
+                    }
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        acc[nt][i][0] *= alpha[0];
+                        acc[nt][i][1] *= alpha[1];
+                        acc[nt][i][2] *= alpha[0];
+                        acc[nt][i][3] *= alpha[1];
+                    }
+                    eights[nt][0] *= alpha[0];
+                    eights[nt][1] *= alpha[1];
+                }
+                exponentials();
+            }
+            if (!whole) {  // a token that the row does not keep, whatever its scale
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (w[nt][e] == 0.f) y[nt][e] = 0.f;
+            }
+            // ---- the sum of weights, and P^T as operand
+            uint32_t pb[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    l[nt][e & 1] += w[nt][j][e];
-                    y[e] = w[nt][j][e] * vs[j][e >> 1];
-                    // a token that the row does not keep, whatever its scale
-                    if (!whole && x[nt][j][e] == -INFINITY) y[e] = 0.f;
-                }
-                pb[nt][j][0] = transpose8(pack_f16x2(y[0], y[1]));
-                pb[nt][j][1] = transpose8(pack_f16x2(y[2], y[3]));
+                for (int e = 0; e < 4; ++e) l[nt][e & 1] += w[nt][e];
+                pb[nt][0] = transpose8(pack_f16x2(y[nt][0], y[nt][1]));
+                pb[nt][1] = transpose8(pack_f16x2(y[nt][2], y[nt][3]));
             }
-        // ---- O^T += V^T P^T
+            // ---- O^T += V^T P^T, and what the codes' 8 adds to every value
+            {
+                const uint32_t a[4] = {kEight, kEight, kEight, kEight};
 #pragma unroll
-        for (int j = 0; j < SUB; ++j)
+                for (int nt = 0; nt < NT; ++nt) mma16816<true>(eights[nt], a, pb[nt][0], pb[nt][1]);
+            }
 #pragma unroll
             for (int i = 0; i < J; ++i) {
                 const uint32_t sel = i % 2 ? 0x7632u : 0x5410u;
-                const uint32_t lo = prmt(v[j][0][i / 2], v[j][1][i / 2], sel), hi = prmt(v[j][2][i / 2], v[j][3][i / 2], sel);
-                const uint32_t a0[4] = {codes_f16<0>(lo), codes_f16<1>(lo), codes_f16<0>(hi), codes_f16<1>(hi)};
-                const uint32_t a1[4] = {codes_f16<2>(lo), codes_f16<3>(lo), codes_f16<2>(hi), codes_f16<3>(hi)};
+                const uint32_t lo = prmt(v[0][i / 2], v[1][i / 2], sel), hi = prmt(v[2][i / 2], v[3][i / 2], sel);
+                const uint32_t a0[4] = {value_codes<0>(lo), value_codes<1>(lo), value_codes<0>(hi), value_codes<1>(hi)};
+                const uint32_t a1[4] = {value_codes<2>(lo), value_codes<3>(lo), value_codes<2>(hi), value_codes<3>(hi)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma16816<true>(acc[nt][2 * i], a0, pb[nt][j][0], pb[nt][j][1]);
-                    mma16816<true>(acc[nt][2 * i + 1], a1, pb[nt][j][0], pb[nt][j][1]);
+                    mma16816<true>(acc[nt][2 * i], a0, pb[nt][0], pb[nt][1]);
+                    mma16816<true>(acc[nt][2 * i + 1], a1, pb[nt][0], pb[nt][1]);
                 }
             }
-#pragma unroll
-        for (int s = 0; s + 1 < ST; ++s) {
-            base_of[s] = base_of[s + 1];
-#pragma unroll
-            for (int j = 0; j < SUB; ++j) ph[s][j] = ph[s + 1][j];
         }
-        base_of[ST - 1] = base_next;
+        // ---- the slot is free: the step ST further on goes there
+        const uint32_t after = zero_after(last, nothing);
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < SUB; ++j) ph[ST - 1][j] = ph_next[j];
+        for (int i = 0; i + 1 < ST; ++i) info[i] = info[i + 1];
+        if (it + ST < steps) {
+            if (it + ST == looked) lookup();
+            info[ST - 1] = __shfl_sync(0xffffffffu, info_lane, (it + ST) % 32);
+            fetch(it + ST, slot, after);
+        }
         if (++slot == ST) {
             slot = 0;
             phase ^= 1u;
@@ -540,10 +521,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int s = 0; s < ST && it + s < steps; ++s) {
             const int at = (slot + s) % ST;
             const uint32_t par = phase ^ (slot + s >= ST ? 1u : 0u);
-            mbar_wait(&ms.k_full[warp][at], par, &keep_waiting);
-            mbar_wait(&ms.v_full[warp][at], par, &keep_waiting);
+            mbar_wait(&ms.full[warp][at], par, &keep_waiting);
         }
-        if (refetched) mbar_wait(&ms.k_full[warp][slot], phase ^ 1u, &keep_waiting);
     }
 }
 
@@ -571,9 +550,9 @@ cudaError_t launch_cache4(const CacheAttnProblem &p, cudaStream_t stream) {
     CUtensorMap map_k, map_v;
     if (!make_codes_map<D>(&map_k, p.cache.k, p.cache, box_rows) || !make_codes_map<D>(&map_v, p.cache.v, p.cache, box_rows))
         return cudaErrorInvalidValue;
-    kernel<<<(unsigned)main_ctas(p, C::kTokens), kThreads, C::kSmem, stream>>>(map_k, map_v, p, row_tiles, box_rows);
+    kernel<<<(unsigned)main_ctas(p, C::kTokens, C::kPerSm), kThreads, C::kSmem, stream>>>(map_k, map_v, p, row_tiles, box_rows);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_join<D, C::kRows, C::kTokens>(p, row_tiles, pairs, stream);
+    return launch_join<D, C::kRows, C::kTokens>(p, row_tiles, pairs, stream, C::kPerSm);
 }
 
 template <int D>
@@ -586,8 +565,9 @@ cudaError_t launch_cache4_rows(const CacheAttnProblem &p, cudaStream_t stream) {
 }  // namespace
 
 int64_t cache_attention_int4_workspace(const CacheAttnProblem &p) {
-    return workspace_partials(p.B) +
-           2 * kWarps * main_ctas(p, Cfg4<128, 1>::kTokens) * partial_floats(tile_rows(p), p.cache.D) * 4;
+    const bool one = tile_rows(p) == 8;
+    const int64_t ctas = main_ctas(p, Cfg4<128, 1>::kTokens, one ? Cfg4<128, 1>::kPerSm : Cfg4<128, 2>::kPerSm);
+    return workspace_partials(p.B) + 2 * kWarps * ctas * partial_floats(tile_rows(p), p.cache.D) * 4;
 }
 
 cudaError_t launch_cache_attention_int4(const CacheAttnProblem &p, cudaStream_t stream) {

@@ -4,7 +4,12 @@ Bounds.  A score is a float32 sum of D exact products, group by group, each grou
 (D + 16) 2^-24 scale sum |q k|; a query value below 2^-14 of its row's largest keeps fp16's smallest step, 2^-24 of
 that one, half of it off.  lse is off by as much, plus 2^-19 for exponentials and sums.  A weight times its value's scale
 is rounded to fp16: off by 2^-11 of itself, or by half of fp16's smallest step, 2^-25, in units in which the row's
-largest is at least 2^7 (scales below 2^-60 count as 2^-60 there); codes are 8 at most.  out is rounded once, 2^-8.
+largest is at least 2^7 (scales below 2^-60 count as 2^-60 there); codes are 8 at most.  The sums of codes (up to 15)
+and of the 8 that is taken off afterwards are float32 sums over steps of 16 tokens, each of which cuts off less than
+2^-22 of what is summed, and products of numbers that keep 4 of 11 bits, cut off 2^-24 below what 11 bits would make, 2^-17
+of the largest, twice: 2^-16 + (n / 16 + 2) 2^-22 times 24 times the sum of weights and scales.  out is rounded once, 2^-8.
+That bound is of the worst case, and loose for long sequences: all rows together are off by 2^-8 / sqrt(3) (2-norm) of the
+last rounding, 2^-11 of the weights'.
 """
 import math
 
@@ -83,7 +88,9 @@ def reference(q, cache, table, lens, kind, window, sinks, score, cap, scale):
             absolute = torch.einsum("hgn,hnd->hgd", p, v.abs()).reshape(Hq, D)
             ref = cache.v_scale[ids[idx], :, idx % page].double().clamp(min=2.0**-60).t()        # [H, n]
             least = 2.0**-32 * 8 * len(idx) * (p * ref[:, None]).amax(-1).reshape(-1)
-            bo[b, :, t] = (2.0**-11 + 2 * e_s[:, None] + 2.0**-18) * absolute + 2.0**-8 * out[b, :, t].abs() + least[:, None]
+            sums = (2.0**-16 + (len(idx) / 16 + 2) * 2.0**-22) * 24 * (p * ref[:, None]).sum(-1).reshape(-1)
+            bo[b, :, t] = (2.0**-11 + 2 * e_s[:, None] + 2.0**-18) * absolute + 2.0**-8 * out[b, :, t].abs() + \
+                (least + sums)[:, None]
     return out, lse, bo, bl
 
 
@@ -98,6 +105,8 @@ def compare(q, cache, table, lens, kind=fa.FLEX_MASK_CAUSAL, window=0, sinks=0, 
     assert (off <= bl).all(), float((off - bl).max())
     diff = (out.double() - ro).abs()
     assert (diff <= bo).all(), float((diff - bo).max())
+    if ro.count_nonzero() >= 4096 and abs(scale) * float(q.abs().max()) < 1.0:
+        assert float(diff.norm()) <= (2.0**-8 / math.sqrt(3) + 2.0**-11) * float(ro.norm())
     return out, lse
 
 
