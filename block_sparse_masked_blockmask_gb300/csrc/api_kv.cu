@@ -275,10 +275,13 @@ int flex_kv_cache_read(const flex_kv_cache *cache, const int32_t *page_table, in
     p.max_pages = max_pages;
     p.starts = starts;
     const flex_tensor *out[2] = {k_out, v_out};
+    const int64_t elem = k_out->dtype == FLEX_DTYPE_BF16 ? 2 : 4;
+    p.wide = 1;
     for (int w = 0; w < 2; ++w) {
         p.out[w] = const_cast<void *>(out[w]->data);
         p.out_stride[w][0] = out[w]->stride[1];
         p.out_stride[w][1] = out[w]->stride[2];
+        if (!aligned(p.out[w], 32) || out[w]->stride[1] * elem % 32 != 0 || out[w]->stride[2] * elem % 32 != 0) p.wide = 0;
     }
     return launch_kv_read(p, cache->dtype, k_out->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FLEX_OK
                                                                                                          : FLEX_ERR_CUDA;

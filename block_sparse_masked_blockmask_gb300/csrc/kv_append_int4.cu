@@ -50,20 +50,27 @@ __device__ __forceinline__ float reciprocal_up(float scale) {
 // at a time x D / 32.
 template <typename T, int D, bool IS_V>
 __device__ __forceinline__ void append_rows(const AppendProblem &p, int64_t token0, int tokens, int h_first, int h_last,
-                                            float2 *table, uint64_t *turns) {
+                                            float2 *table, uint64_t *turns, int32_t (&starts_here)[kStartsHere + 1]) {
     constexpr int P = D / 32, J = D / 32, R = 1024 / D, RUNS = 4;  // threads; groups; values of a run; 8-value pieces
     const int part = threadIdx.x % P, slot = threadIdx.x / P, heads = kThreads / P / tokens;
     const int tok = slot % tokens, h0 = h_first + slot / tokens;
-    // this thread's token
+    // this thread's token, and its first head's values: they are on the way while its
+    // place is looked up
     const int64_t token = token0 + tok;
+    const int64_t *st = IS_V ? p.v_stride : p.k_stride;
+    const int32_t *starts = nullptr;
+    if (p.starts) {
+        starts = stage_starts(p.starts, p.B, starts_here);
+        __syncthreads();
+    }
     int b, t;
     int64_t row;  // of the source: the batch entry's token, or the packed token
     bool live;
     if (p.starts) {
         live = token < p.S;
-        b = live ? sequence_of(p.starts, p.B, (int)token) : -1;
+        b = live ? sequence_of(starts, p.B, (int)token) : -1;
         live = b >= 0;
-        t = live ? (int)token - __ldg(p.starts + b) : 0;
+        t = live ? (int)token - starts[b] : 0;
         row = token;
     } else {
         live = token < (int64_t)p.B * p.S;
@@ -72,6 +79,13 @@ __device__ __forceinline__ void append_rows(const AppendProblem &p, int64_t toke
         row = t;
         live = live && t < (p.new_lens ? __ldg(p.new_lens + b) : p.S);
     }
+    const T *src = static_cast<const T *>(IS_V ? p.v : p.k) + (p.starts ? 0 : b * st[0]) + row * st[2];
+    Raw8<T> raw[RUNS];  // a head's values, loaded one head ahead
+    auto load = [&](int h) {
+#pragma unroll
+        for (int k = 0; k < RUNS; ++k) raw[k].load(src + h * st[1] + 32 * (k * J / RUNS) + R * part + 8 * (k % (RUNS / J)));
+    };
+    if (live && h0 < h_last) load(h0);
     int64_t position = 0, at = 0;
     if (live) {
         const int first = __ldg(p.cache_lens + b);
@@ -101,19 +115,15 @@ __device__ __forceinline__ void append_rows(const AppendProblem &p, int64_t toke
         }
         __syncthreads();
     }
-    const int64_t *st = IS_V ? p.v_stride : p.k_stride;
-    const T *src = static_cast<const T *>(IS_V ? p.v : p.k) + (p.starts ? 0 : b * st[0]) + row * st[2];
     const float2 *cs = table + tok * pairs;
     for (int h = h0; h - slot / tokens < h_last; h += heads) {
         const bool mine = live && h < h_last;
         float x[RUNS][8];
         uint32_t most[J];
         if (mine) {
-            Raw8<T> raw[RUNS];
-#pragma unroll
-            for (int k = 0; k < RUNS; ++k) raw[k].load(src + h * st[1] + 32 * (k * J / RUNS) + R * part + 8 * (k % (RUNS / J)));
 #pragma unroll
             for (int k = 0; k < RUNS; ++k) raw[k].unpack(x[k]);
+            if (h + heads < h_last) load(h + heads);
             if (pairs && p.layout == FLEX_ROPE_HALF) {
                 if (p.rotary == D) {  // a run's partner is the thread's own, two further on
 #pragma unroll
@@ -220,21 +230,23 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv_append_int4_kernel(const AppendProblem p, int tokens, int heads_per_cta, int groups) {
     extern __shared__ __align__(16) float2 table[];  // [token][pair] (cos, sin)
     __shared__ uint64_t turns[64];
+    __shared__ int32_t starts_here[kStartsHere + 1];
     const bool is_v = (int)blockIdx.y >= groups;
     const int h_first = ((int)blockIdx.y - (is_v ? groups : 0)) * heads_per_cta;
     const int h_last = min(h_first + heads_per_cta, p.cache.H);
     const int64_t token0 = (int64_t)blockIdx.x * tokens;
     if (is_v)
-        append_rows<T, D, true>(p, token0, tokens, h_first, h_last, table, turns);
+        append_rows<T, D, true>(p, token0, tokens, h_first, h_last, table, turns, starts_here);
     else
-        append_rows<T, D, false>(p, token0, tokens, h_first, h_last, table, turns);
+        append_rows<T, D, false>(p, token0, tokens, h_first, h_last, table, turns, starts_here);
 }
 
 template <typename T, int D>
 cudaError_t launch(const AppendProblem &p, cudaStream_t stream) {
     const int64_t all = p.starts ? p.S : (int64_t)p.B * p.S;
-    // a CTA takes a power of two of tokens and walks the heads with their sines and cosines
-    int tokens = kThreads / (D / 32);
+    // a CTA takes a power of two of tokens and walks the heads, two or four at a time,
+    // with their sines and cosines (one at a time: 16 us for 15 at 8 heads of 9000 tokens)
+    int tokens = kThreads / (D / 32) / 2;
     while (tokens > 1 && (all + tokens - 1) / tokens * 2 < 2 * 152) tokens /= 2;
     int heads = p.cache.H;
     const int64_t tiles = (all + tokens - 1) / tokens;

@@ -384,11 +384,12 @@ int64_t main_ctas(const CacheAttnProblem &p, int tokens, int per_sm = 2) {
 }
 
 template <int D, int ROWS, int TOKENS>
-cudaError_t launch_join(const CacheAttnProblem &p, int row_tiles, int64_t pairs, cudaStream_t stream, int per_sm = 2) {
+cudaError_t launch_join(const CacheAttnProblem &p, int row_tiles, int64_t pairs, cudaStream_t stream, int per_sm = 2,
+                        int join_many = kJoinMany) {
     // the join is launched while the main kernel runs and waits for its end on
     // the device, which hides its launch
     cudaLaunchConfig_t cfg = {};
-    const bool many = main_ctas(p, TOKENS, per_sm) * kWarps >= pairs * kJoinMany;
+    const bool many = main_ctas(p, TOKENS, per_sm) * kWarps >= pairs * join_many;
     const int live = (int)((int64_t)p.Q * p.G < ROWS ? (int64_t)p.Q * p.G : ROWS);
     cfg.gridDim = dim3((unsigned)pairs, many ? live : 1, many ? D / 32 : 1);
     cfg.blockDim = dim3(many ? kJoinThreads : 32 * ROWS);

@@ -34,6 +34,7 @@ namespace flex {
 namespace {
 
 constexpr float kLeastRef = 0x1p-60f;
+constexpr int kJoinMany4 = 32;  // warps of the main launch per pair, from which CTAs join a row
 
 // The codes at nibble N of both halves of a word as fp16x2: their bits alone are
 // subnormal numbers.  The tensor core cuts products off some 2^-24 below what a
@@ -69,10 +70,11 @@ template <int D, int NT>
 struct Cfg4 {
     static constexpr int kRowBytes = D / 2;             // of codes; TMA swizzle span
     static constexpr int kGroups = D / 32;
-    static constexpr int kTokens = 32;                  // of a step
+    static constexpr int kTokens = 64;                  // of a step
     static constexpr int kSub = kTokens / 16;
-    static_assert(kSub == 2, "a step's info has bits for two groups, and its first token leaves five free");
-    static constexpr int kStages = 3;
+    static constexpr int kWhole = 1 << kSub;            // in a step's info, above a bit for each of its groups
+    static_assert(2 * kWhole <= kTokens, "the first token of a step leaves their bits free");
+    static constexpr int kStages = 2;
     static constexpr int kPerSm = NT == 1 ? 3 : 2;      // CTAs
     static constexpr int kSteps = D / 16;               // k16 steps of S, m16 tiles of O
     static constexpr int kRows = 8 * NT;
@@ -120,8 +122,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
     // ---- steps ahead of the computation.  Lane i looks up the warp's step
     // 32 k + i and asks for its copies when its turn comes: of its 16-token groups
     // page * heads + head, or -1 where there is nothing that a row keeps (the groups of
-    // one box share a page).  The others get its first token, a multiple of 32, and
-    // in the low bits which groups are there (1, 2), and whether every row keeps all of it (4).
+    // one box share a page).  The others get its first token and, in the bits that
+    // this leaves free, which groups are there and whether every row keeps all of it.
     int look_b = b;
     int64_t look_off = off;
     int looked = 0;
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
             whole = whole && ph_lane[j] >= 0;
             info_lane |= ph_lane[j] >= 0 ? 1 << j : 0;
         }
-        info_lane |= whole ? 4 : 0;
+        info_lane |= whole ? C::kWhole : 0;
         // the next batch begins where lane 31's successor would be
         look_b = __shfl_sync(0xffffffffu, lb, 31);
         look_off = __shfl_sync(0xffffffffu, lo_, 31) + 1;
@@ -170,10 +172,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
             uint8_t *dst = ring + slot * C::kSlot + after;
             uint64_t *bar = &ms.full[warp][slot];
             constexpr uint32_t kGroup = 16u * (2 * C::kRowBytes + 2 * J + 2);
-            mbar_arrive_expect_tx(bar, kGroup * (uint32_t)__popc(info_lane & 3));
+            mbar_arrive_expect_tx(bar, kGroup * (uint32_t)__popc(info_lane & (C::kWhole - 1)));
 #pragma unroll
             for (int j = 0; j < SUB; ++j)
-                if (ph_lane[j] >= 0 && (j == 0 || box_rows == 16)) {
+                if (ph_lane[j] >= 0 && ((16 * j) & (box_rows - 1)) == 0) {
                     const int at = ((info_lane & ~(C::kTokens - 1)) + 16 * j) & (page - 1);
                     const int64_t row = (int64_t)ph_lane[j] * page + at;
                     tma_load_3d(dst + 16 * j * C::kRowBytes, &map_k, bar, 0, at, ph_lane[j]);
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
             }
         }
         const int base = info[0] & ~(C::kTokens - 1);
-        const bool whole = info[0] & 4;
+        const bool whole = info[0] & C::kWhole;
         const uint32_t k_at = ring_at + slot * C::kSlot, v_at = k_at + C::kCodes, ks_at = k_at + 2 * C::kCodes,
                        vs_at = ks_at + C::kKeyScales;
         if (!__all_sync(0xffffffffu, mbar_wait(&ms.full[warp][slot], phase, &ms.abort))) {
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
                 most_y = fmax3(fmax3(most_y, y[nt][0], y[nt][1]), y[nt][2], y[nt][3]);
                 most_w = fmax3(fmax3(most_w, w[nt][0], w[nt][1]), w[nt][2], w[nt][3]);
             }
-            if (__any_sync(0xffffffffu, most_y > 0x1p15f || most_w > 0x1p15f / kLeastRef)) {
+            if (__builtin_expect(__any_sync(0xffffffffu, most_y > 0x1p15f || most_w > 0x1p15f / kLeastRef), 0)) {
                 const float lr[2] = {log2f(fmaxf(vs[0], kLeastRef)), log2f(fmaxf(vs[1], kLeastRef))};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -552,7 +554,7 @@ cudaError_t launch_cache4(const CacheAttnProblem &p, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     kernel<<<(unsigned)main_ctas(p, C::kTokens, C::kPerSm), kThreads, C::kSmem, stream>>>(map_k, map_v, p, row_tiles, box_rows);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_join<D, C::kRows, C::kTokens>(p, row_tiles, pairs, stream, C::kPerSm);
+    return launch_join<D, C::kRows, C::kTokens>(p, row_tiles, pairs, stream, C::kPerSm, kJoinMany4);
 }
 
 template <int D>

@@ -48,6 +48,7 @@ struct ReadProblem {
     const int32_t *starts;           // [B + 1]
     void *out[2];                    // keys, values
     int64_t out_stride[2][2];        // h, token (elements)
+    int wide;                        // the outputs' rows are 32-byte aligned
 };
 
 struct CacheAttnProblem {

@@ -22,18 +22,31 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     return r;
 }
 
-// N floats (a multiple of 8) to bf16 or float32, in stores of 32 bytes where the address allows.
+// N floats (a multiple of 8) to bf16 or float32, in stores of 32 bytes (whole
+// sectors: two of 16 cost 20% more time) where the output's rows allow it.
 template <int N>
-__device__ __forceinline__ void store_values(uint16_t *dst, const float (&x)[N]) {
+__device__ __forceinline__ void store_values(uint16_t *dst, const float (&x)[N], bool wide) {
+    uint32_t w[N / 2];
 #pragma unroll
-    for (int i = 0; i < N; i += 8)
-        *reinterpret_cast<uint4 *>(dst + i) = make_uint4(pack_bf16x2(x[i], x[i + 1]), pack_bf16x2(x[i + 2], x[i + 3]),
-                                                         pack_bf16x2(x[i + 4], x[i + 5]), pack_bf16x2(x[i + 6], x[i + 7]));
+    for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    if (N >= 16 && wide) {
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 8) st_global_32B(dst + 2 * i, w + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 4)
+            *reinterpret_cast<uint4 *>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
 }
 template <int N>
-__device__ __forceinline__ void store_values(float *dst, const float (&x)[N]) {
+__device__ __forceinline__ void store_values(float *dst, const float (&x)[N], bool wide) {
+    if (wide) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        for (int i = 0; i < N; i += 8) st_global_32B(dst + i, reinterpret_cast<const uint32_t *>(x) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    }
 }
 
 // What a thread reads of a row, and the values that it stands for: N of them,
@@ -123,12 +136,15 @@ template <int KIND, typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadProblem p) {
     using C = Piece<KIND, D>;
     __shared__ int64_t row_of[kTokens];   // of head 0: page * H * page size + slot; -1: no page; -2: no token
+    __shared__ int32_t starts_here[kStartsHere + 1];
     const int token0 = (int)blockIdx.x * kTokens;
+    const int32_t *starts = stage_starts(p.starts, p.B, starts_here);
+    __syncthreads();
     if (threadIdx.x < kTokens) {
-        const int token = token0 + (int)threadIdx.x, b = token < p.T ? sequence_of(p.starts, p.B, token) : -1;
+        const int token = token0 + (int)threadIdx.x, b = token < p.T ? sequence_of(starts, p.B, token) : -1;
         int64_t row = -2;
         if (b >= 0) {
-            const int position = token - __ldg(p.starts + b), entry = position >> p.cache.page_shift;
+            const int position = token - starts[b], entry = position >> p.cache.page_shift;
             const int id = entry < p.max_pages ? __ldg(p.page_table + (int64_t)b * p.max_pages + entry) : -1;
             row = id >= 0 && id < p.cache.num_pages
                       ? (int64_t)id * p.cache.H * p.cache.page + (position & (p.cache.page - 1))
@@ -159,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadProblem p) 
         }
         store_values(static_cast<T *>(p.out[is_v]) + h * p.out_stride[is_v][0] + (int64_t)(token0 + tok) * p.out_stride[is_v][1] +
                          part * C::N,
-                     x);
+                     x, p.wide);
     }
 }
 

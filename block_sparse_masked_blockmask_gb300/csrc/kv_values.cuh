@@ -42,16 +42,25 @@ struct Raw8<float> {
 // the last).  Entries that do not ascend give some sequence that begins at or
 // before the token.
 __device__ __forceinline__ int sequence_of(const int32_t *starts, int n, int token) {
-    if (n <= 0 || token < __ldg(starts)) return -1;
+    if (n <= 0 || token < starts[0]) return -1;
     int lo = 0, hi = n;  // starts[lo] <= token
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (__ldg(starts + mid) <= token)
+        if (starts[mid] <= token)
             lo = mid;
         else
             hi = mid;
     }
-    return token < __ldg(starts + lo + 1) ? lo : -1;
+    return token < starts[lo + 1] ? lo : -1;
+}
+// The starts for a CTA to search in: of up to kStartsHere sequences a copy in its
+// shared memory, which takes one latency of device memory in place of one for each
+// halving.  All threads call it, and synchronise before they search.
+constexpr int kStartsHere = 127;
+__device__ __forceinline__ const int32_t *stage_starts(const int32_t *starts, int n, int32_t (&here)[kStartsHere + 1]) {
+    if (n > kStartsHere) return starts;
+    if ((int)threadIdx.x <= n) here[threadIdx.x] = __ldg(starts + threadIdx.x);
+    return here;
 }
 
 }  // namespace flex
