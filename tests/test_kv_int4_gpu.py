@@ -203,6 +203,45 @@ def test_append_drops(kind):
 
 
 @KINDS
+def test_starts_far_below_zero(kind):
+    """Starts whose distance from a token passes 32 bits: positions that no table has."""
+    H, D, page, low = 2, 64, 16, -2**31
+    k = torch.ones((1, H, 120, D), device="cuda").bfloat16()
+    table, lens = ints([[0, 1], [2, 3]]), ints([0, 31])
+    cache = new_cache(4, H, page, D, kind)
+    before = held_bytes(cache)
+    for starts in ([low, 120, 120], [low, low + 5, 120]):
+        fa.flex_kv_cache_append_packed(cache, k, k, ints(starts), table, lens)
+        for x in fa.flex_kv_cache_read(cache, table, ints(starts), 120):
+            assert (x == 0).all()
+    assert all(torch.equal(x, y) for x, y in zip(held_bytes(cache), before))
+
+
+@KINDS
+@pytest.mark.parametrize("B", [127, 128, 300])
+def test_many_sequences(B, kind):
+    """As many as a CTA keeps the starts of, and more: packed against padded appends, and what is read back."""
+    gen = torch.Generator().manual_seed(B)
+    H, D, page = 2, 64, 16
+    lens = torch.randint(0, 4, (B,), generator=gen).tolist()
+    table, pages = table_of(gen, [1] * B, 1)
+    starts, zero = starts_of(lens), ints([0] * B)
+    k, v = (torch.randn((1, H, sum(lens), D), generator=gen).to(BF16).cuda() for _ in range(2))
+    one, other = (new_cache(pages, H, page, D, kind) for _ in range(2))
+    fa.flex_kv_cache_append_packed(one, k, v, starts, table, zero)
+    padded = [torch.zeros((B, H, 3, D), dtype=BF16, device="cuda") for _ in range(2)]
+    for x, y in zip(padded, (k, v)):
+        for b, n in enumerate(lens):
+            x[b, :, :n] = y[0, :, int(starts[b]):int(starts[b]) + n]
+    fa.flex_kv_cache_append(other, *padded, table, zero, ints(lens))
+    assert all(torch.equal(x, y) for x, y in zip(held_bytes(one), held_bytes(other)))
+    for w, x in zip("kv", fa.flex_kv_cache_read(one, table, starts, sum(lens), dtype=torch.float32)):
+        held = values(one, w)
+        for b, n in enumerate(lens):
+            assert torch.equal(x[0, :, int(starts[b]):int(starts[b]) + n], held[int(table[b, 0]), :, :n].float())
+
+
+@KINDS
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["to_bf16", "to_fp32"])
 @pytest.mark.parametrize("D,page,H", [(64, 16, 1), (128, 64, 8), (128, 256, 3), (64, 32, 17)])
 def test_read(D, page, H, out, kind):
