@@ -4,20 +4,32 @@
 //
 // Bound by memory: D + D / 16 + 2 bytes of a visible token and head are read once
 // for 4 G Q D flops.  At the copy rate an SM receives 45 codes a clock, so what
-// binds beside the memory is the work on them: a code costs a quarter to a third
-// of an instruction of a warp's lane to become a 16-bit number, the same again
-// for its part of scales, pairing and products.
+// binds beside the memory is the work on them: a code costs a quarter of an
+// instruction of a warp's lane to become an operand, the same again for its part
+// of scales, pairing and products.  Measured, with the joining launch: two
+// sequences of 131071 tokens, 8 heads of 128, eight query heads each: 69 us, 62% of
+// the copy rate over the bytes above; 64 sequences of 1 to 8192: 77 us.  Of these 11
+// us go by before the first bytes arrive and after the last; the same rings without
+// the arithmetic take 57 us.
 //
 // The list of steps, the rings, the tiles of m16n8k16 products and the join are
 // those of kv_attention.cu.  What differs:
+//  * Steps are 64 tokens, computed 16 at a time by one loop body (unrolled it
+//    outgrows the instruction cache).  Of 32 tokens the first workload takes 75
+//    us, one sequence of 512 a microsecond less.  Three CTAs share an SM where rows fill
+//    one tile of 8, two where they fill two: their registers allow no more.
 //  * The order of codes in a row gives every lane what it multiplies.  Keys: lane
 //    (g, t) reads piece t of keys g and g + 8, eight values of each group of 32
 //    (all groups), and one byte permute per group puts them in one word: two
 //    k16 steps of that group.  Values: it reads piece g of its four tokens, four
 //    values of every group, and a byte permute pairs two tokens' 16-bit units.
 //    Then the code at nibble n of both halves of a word is one operand register.
-//  * Codes become fp16 exactly: or-ed into the mantissa of 1024 (code + 1024, or
-//    16 code + 1024 for the upper nibble of a byte), less its offset.
+//  * Codes become fp16 by a mask and no arithmetic: where they lie they are
+//    subnormal numbers, whose units are taken off at the end.  The 8 that each
+//    stands above zero is the accumulator's start for keys (-8 times the sum of the
+//    query's values of the group), and one more product with an operand of eights
+//    for values.  Converted by or-ing into the mantissa of 1024 and a subtraction,
+//    the first workload took 100 us for 81.
 //  * A key's products are summed in float32 group by group and then scaled, two
 //    keys a lane: 4 multiply-adds for 512 codes, where scaling the codes would
 //    take 8 and round them.
@@ -28,6 +40,9 @@
 //    values keeps its bits exactly where it matters to the row.  The sum of
 //    weights is taken relative to the same m, before vs.  Scales below 2^-60 count as
 //    2^-60 in m, so that weights without their scale stay below 2^75.
+//  * The join gives a row a CTA where the main launch has 32 warps for each pair,
+//    else a warp.  At 16 pairs of tokens behind a window 27 us, and 43 with the
+//    8-bit kernel's 8 warps; from 64 on the first workload takes 75, from 128 on 92.
 #include "kv_attention_common.cuh"
 
 namespace flex {
@@ -285,9 +300,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // rows are divided by the power of two of their largest magnitude, so
                 // that they fit fp16 (bf16 values keep all their bits down to 2^-14
-                // of it and further); by 1 where they are zero or not finite
-                const uint32_t e = top >> 7;
-                const float qf = e == 0u || e == 255u ? 1.f : __uint_as_float(e << 23);
+                // of it and further), 2^-113 at least, whose reciprocal is finite times
+                // 2^14; by 1 where they are not finite
+                const uint32_t e = max(top >> 7, 14u);
+                const float qf = e == 255u ? 1.f : __uint_as_float(e << 23);
                 const float f = 1.f / qf * (float)(1 << kQueryUp);
                 float sum[J];
 #pragma unroll

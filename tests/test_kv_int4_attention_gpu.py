@@ -202,6 +202,18 @@ def test_attention_large_and_small_queries():
     compare(q.to(BF16).cuda(), cache, table, lens)
 
 
+@pytest.mark.parametrize("power", [-112, -114, -120, -126, -133, 100])
+def test_attention_queries_at_the_ends_of_the_type(power):
+    """Rows of 2^power times small whole numbers (exact down to bf16's smallest step), with scales that bring scores back."""
+    gen = torch.Generator().manual_seed(300 + power)
+    cache, table = filled(gen, [70, 33], 1, 32, 64)
+    q = (torch.randint(-7, 8, (2, 4, 1, 64), generator=gen).double() * 2.0**power).to(BF16).cuda()
+    q[1, 3] = 0
+    assert (q[0] != 0).any()
+    for scale in (0.125, 2.0**min(-power - 6, 100)):
+        compare(q, cache, table, [70, 33], scale=scale)
+
+
 @pytest.mark.parametrize("D,G", [(64, 4), (128, 12)])
 @pytest.mark.parametrize("spread", [40, 100])
 def test_attention_scales_far_apart(D, G, spread):
