@@ -14,6 +14,9 @@
 namespace flex {
 namespace {
 
+// Keys of a sequence or window, on average, up to which the kernels for items of few
+// kv tiles are taken: 64 causal sequences up to 96 tokens, 32 query heads over 8: 27.0
+// us with them and 32.9 without; twelve up to 4096: 766 us with and 537 without.
 constexpr int64_t kFewKeys = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kLengths = 1024;  // lengths told apart, in kv tiles (longer ones count as the longest)
@@ -100,7 +103,6 @@ cudaError_t launch_attn_packed(const PackedProblem &p, cudaStream_t stream) {
     kp.lse = p.lse;
     kp.status = p.status;
     kp.wide_out = (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.out_stride[0] * 2 | (uintptr_t)p.out_stride[1] * 2) % 32 == 0;
-    // few kv tiles: at most so many keys a sequence on average, or in a window
     int64_t keys = p.total_k / p.sequences;
     if (p.mask.window != INT_MAX) keys = std::min<int64_t>(keys, (int64_t)p.mask.window + p.mask.sinks);
     kp.few_tiles = keys <= kFewKeys;

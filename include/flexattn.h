@@ -591,10 +591,17 @@ FLEX_API int flex_kv_cache_read(const flex_kv_cache *cache, const int32_t *page_
  * as masked.  What lies in slots that a row does not keep has no effect on
  * it, NaN included.  Scales are taken as positive numbers of any value, those
  * of V up to 2^80 apart within a sequence, and values of V up to 2^80 (weights
- * and sums are float32); the append writes powers of two.  Made for few query
- * tokens (a decoding step, a handful of tokens to check); any Q is computed, at
- * up to 197 TFLOP/s (a first prompt with as many key heads as query heads is
- * faster in flex_attention_fwd).  Errors: as flex_kv_cache_append, and
+ * and sums are float32); the append writes powers of two.
+ * INT4: scales are zero or positive; a V scale up to 2^100, and those of a row's
+ * tokens any distance apart (weights count down to 2^-31 of the row's largest
+ * weight times scale, in which scales below 2^-60 count as 2^-60).  scale and
+ * scale times a row's largest |q| below 2^110.  Codes are multiplied as fp16 with
+ * float32 sums, whose last places are cut off: out is off by up to 2^-16 of 24
+ * times the sum of weights times scales, beside its rounding.
+ * Made for few query tokens (a decoding step, a handful of tokens to check); any Q
+ * is computed, at up to 197 TFLOP/s (prompts are faster in
+ * flex_attention_packed_fwd, over keys that flex_kv_cache_read brings back where
+ * earlier tokens lie before them).  Errors: as flex_kv_cache_append, and
  * FLEX_ERR_UNSUPPORTED for fp32 q and for the prefix and document masks.
  *   workspace : device, 16-byte aligned, at least as many bytes as
  *               flex_kv_cache_attention_workspace gives (else FLEX_ERR_SHAPE);
