@@ -242,6 +242,16 @@ def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _empty_by_token(B: int, H: int, T: int, D: int, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """_empty for a [B, H, T, D] tensor with a token's heads next to each other (in one call of torch's: transposing
+    one that is empty takes 4 us more)."""
+    strides = (T * H * D, D, H * D, 1)
+    if stream is None:
+        return torch.empty_strided((B, H, T, D), strides, dtype=dtype, device=device)
+    with _on_stream(stream, device):
+        return torch.empty_strided((B, H, T, D), strides, dtype=dtype, device=device)
+
+
 def _device_guard(device):
     """A context in which `device` is the current CUDA device (nothing to enter when it already is)."""
     return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
@@ -789,7 +799,7 @@ def flex_kv_cache_read(cache: KVCache, page_table: torch.Tensor, starts: torch.T
         if x is None:
             if total is None:
                 raise ValueError("total is needed where k_out and v_out are not both given")
-            x = _empty((1, total, cache.shape[1], cache.shape[3]), dtype, device, stream).transpose(1, 2)
+            x = _empty_by_token(1, cache.shape[1], total, cache.shape[3], dtype, device, stream)
         elif x.device != device:
             raise ValueError("the outputs must be on the cache's device")
         outs.append(x)
@@ -931,7 +941,7 @@ def flex_attention_packed_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             raise ValueError("q, k and v must be on the plan's device")
     tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
     if out is None:
-        out = _empty((shape[0], shape[2], shape[1], shape[3]), q.dtype, device, stream).transpose(1, 2)
+        out = _empty_by_token(*shape, q.dtype, device, stream)
     elif out.device != device:
         raise ValueError("out must be on the plan's device")
     if lse is None:
