@@ -92,6 +92,17 @@ __device__ __forceinline__ uint32_t load_u16(uint32_t addr) {
 // was read.  The bit test cannot be folded away, and lane 0 alone uses it.
 __device__ __forceinline__ uint32_t zero_after(uint32_t a, uint32_t zero) { return a & zero; }
 
+// a / by and what is left, of numbers >= 0 (in 32 bits where that is enough: a 64-bit
+// division is some hundred instructions one after another).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t by) {
+    return (uint64_t)(a | by) >> 32 ? a / by : (int64_t)((uint32_t)a / (uint32_t)by);
+}
+__device__ __forceinline__ int divide(int64_t a, int by, int &left) {
+    const int64_t q = quotient(a, by);
+    left = (int)(a - q * by);
+    return (int)q;
+}
+
 // Steps of a sequence: tokens that any of its query rows keeps, [0, send) and
 // [lo_min, hi), in whole steps.
 struct Steps {
@@ -237,17 +248,17 @@ __device__ __forceinline__ bool take_share(const CacheAttnProblem &p, int pairs_
 // warps' share (512 pairs: 98 us in all, 137 with the kernel below).
 template <int D, int ROWS, int TOKENS>
 __global__ void __launch_bounds__(32 * ROWS) cache_attention_join_few_kernel(const CacheAttnProblem p, int row_tiles) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int V = D / 32;  // values per lane
     const int pairs_per_seq = p.cache.H * row_tiles;
     const int b = (int)(blockIdx.x / pairs_per_seq), pair = (int)(blockIdx.x % pairs_per_seq);
     const int r = threadIdx.x / 32, d = threadIdx.x % 32 * V, r0 = pair % row_tiles * ROWS;
     if (r0 + r >= p.Q * p.G) return;
+    const int count = steps_of<TOKENS>(p, __ldg(p.kv_lens + b)).count;  // an input: there before the main launch
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t *head = reinterpret_cast<const int64_t *>(p.workspace);
     const int64_t share = head[0];
-    const int count = steps_of<TOKENS>(p, __ldg(p.kv_lens + b)).count;
     const int64_t begin = head[1 + b] + (int64_t)pair * (count + kEnterCost) + kEnterCost;  // of its first step
-    const int c0 = (int)(begin / share), c1 = (int)((begin + count - 1) / share);
+    const int c0 = (int)quotient(begin, share), c1 = (int)quotient(begin + count - 1, share);
     if (c0 == c1) return;
     const float *parts =
         reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(p.workspace) + workspace_partials(p.B));
@@ -303,14 +314,14 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(cons
     constexpr int kColumns = 16, kGroups = kJoinThreads / kColumns, kJoinWarps = kJoinThreads / 32;
     __shared__ float top_s[kJoinWarps], sum_s[kJoinWarps], factor[kSms * kMostPerSm * kWarps];
     __shared__ float2 value_s[kJoinWarps][kColumns];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int pairs_per_seq = p.cache.H * row_tiles, warp = threadIdx.x / 32;
     const int b = (int)(blockIdx.x / pairs_per_seq), pair = (int)(blockIdx.x % pairs_per_seq), r = (int)blockIdx.y;
+    const int count = steps_of<TOKENS>(p, __ldg(p.kv_lens + b)).count;  // an input: there before the main launch
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t *head = reinterpret_cast<const int64_t *>(p.workspace);
     const int64_t share = head[0];
-    const int count = steps_of<TOKENS>(p, __ldg(p.kv_lens + b)).count;
     const int64_t begin = head[1 + b] + (int64_t)pair * (count + kEnterCost) + kEnterCost;  // of its first step
-    const int c0 = (int)(begin / share), c1 = (int)((begin + count - 1) / share);
+    const int c0 = (int)quotient(begin, share), c1 = (int)quotient(begin + count - 1, share);
     const int r0 = pair % row_tiles * ROWS;
     if (c0 == c1 || r0 + r >= p.Q * p.G) return;
     const float *parts =

@@ -7,17 +7,20 @@
 // binds beside the memory is the work on them: a code costs a quarter of an
 // instruction of a warp's lane to become an operand, the same again for its part
 // of scales, pairing and products.  Measured, with the joining launch: two
-// sequences of 131071 tokens, 8 heads of 128, eight query heads each: 69 us, 62% of
-// the copy rate over the bytes above; 64 sequences of 1 to 8192: 77 us.  Of these 11
-// us go by before the first bytes arrive and after the last; the same rings without
-// the arithmetic take 57 us.
+// sequences of 131071 tokens, 8 heads of 128, eight query heads each: 68 us, 63% of
+// the copy rate over the bytes above; 64 sequences of 1 to 8192: 74 us.  The steps
+// themselves run at 97% of the copy rate; of the 68 us 6 go by before the first bytes
+// are there (launch, the list, page table), and as many behind the last (warps end
+// some us apart, and the join).
 //
 // The list of steps, the rings, the tiles of m16n8k16 products and the join are
 // those of kv_attention.cu.  What differs:
 //  * Steps are 64 tokens, computed 16 at a time by one loop body (unrolled it
 //    outgrows the instruction cache).  Of 32 tokens the first workload takes 75
-//    us, one sequence of 512 a microsecond less.  Three CTAs share an SM where rows fill
-//    one tile of 8, two where they fill two: their registers allow no more.
+//    us, one sequence of 512 a microsecond less.  Three CTAs share an SM, and two where
+//    rows of 128 fill two tiles of 8: their registers allow no more.  (Rows of 64 that
+//    fill two: 16 sequences up to 16384, 15 rows, 48.8 us, and 53.6 with two CTAs; behind
+//    a window of 2048, 26.9 and 26.1.)
 //  * The order of codes in a row gives every lane what it multiplies.  Keys: lane
 //    (g, t) reads piece t of keys g and g + 8, eight values of each group of 32
 //    (all groups), and one byte permute per group puts them in one word: two
@@ -90,7 +93,7 @@ struct Cfg4 {
     static constexpr int kWhole = 1 << kSub;            // in a step's info, above a bit for each of its groups
     static_assert(2 * kWhole <= kTokens, "the first token of a step leaves their bits free");
     static constexpr int kStages = 2;
-    static constexpr int kPerSm = NT == 1 ? 3 : 2;      // CTAs
+    static constexpr int kPerSm = NT == 1 || D == 64 ? 3 : 2;  // CTAs
     static constexpr int kSteps = D / 16;               // k16 steps of S, m16 tiles of O
     static constexpr int kRows = 8 * NT;
     static constexpr int kCodes = kTokens * kRowBytes;  // bytes of a step's keys, or values
@@ -152,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
             sq = steps_of<C::kTokens>(p, __ldg(p.kv_lens + ++lb));
         }
         const bool live = looked + lane < steps;
-        const int pair = (int)(lo_ / sq.count), hk = pair / row_tiles, r0 = pair % row_tiles * C::kRows;
+        int at_step;
+        const int pair = divide(lo_, sq.count, at_step), hk = pair / row_tiles, r0 = pair % row_tiles * C::kRows;
         const int tmin = r0 / p.G, tmax = (min(r0 + C::kRows, p.Q * p.G) - 1) / p.G;
         // what any row of the tile keeps, [0, send) and [lo_min, hi), and what every row does
         const int hi = p.causal ? max(sq.n - p.Q + tmax + 1, 0) : sq.n;
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
         const int send = min(p.sinks, hi);
         const int all_hi = p.causal ? sq.n - p.Q + tmin + 1 : (sq.n - p.Q + tmin >= 0 ? sq.n : 0);
         const int64_t all_lo = p.causal ? max((int64_t)sq.n - p.Q + tmax - p.window + 1, (int64_t)0) : 0;
-        const int base = sq.base((int)(lo_ % sq.count), C::kTokens);
+        const int base = sq.base(at_step, C::kTokens);
         const int *table = p.page_table + (int64_t)lb * p.max_pages;
         bool whole = base + C::kTokens <= all_hi && (base >= all_lo || base + C::kTokens <= p.sinks);
         info_lane = base;
@@ -202,13 +206,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
                 }
         }
     };
-    int info[ST];  // of the current step and the ST - 1 behind it
-    lookup();
-#pragma unroll
-    for (int s = 0; s < ST; ++s) {
-        info[s] = __shfl_sync(0xffffffffu, info_lane, s);
-        if (s < steps) fetch(s, s, 0u);
-    }
+    int info[ST] = {};  // of the current step and the ST - 1 behind it
 
     const uint32_t nothing = (uint32_t)p.cache.page & 1u;  // 0, which the compiler does not know
     // byte offsets of this lane's pieces within a staged tile (TMA swizzle of the row's span)
@@ -224,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
 
     // ---- the pair being computed
     Steps sq = steps_of<C::kTokens>(p, __ldg(p.kv_lens + b));
-    int pair = (int)(off / sq.count), at_step = (int)(off % sq.count);
+    int at_step, pair = divide(off, sq.count, at_step);
     bool entering = true, whole_start = false;
     int hk = 0, r0 = 0, r1 = 0, n = 0;
     float slope[NT][2], qscale[NT][2];  // of this thread's rows, columns 2t and 2t + 1 of each row tile (base-2 units)
@@ -280,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
             r0 = pair % row_tiles * C::kRows;
             r1 = min(r0 + C::kRows, p.Q * p.G) - 1;
             // Q operand: lane (g, t) takes row g at the head dims of its key pieces
+            uint4 rows[NT][J];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int row = r0 + nt * 8 + g;
@@ -287,11 +286,26 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, NT>::kPerSm)
                 const uint16_t *src = p.q + b * p.q_stride[0] +
                                       (int64_t)(hk * p.G + (live ? row % p.G : 0)) * p.q_stride[1] +
                                       (int64_t)(live ? row / p.G : 0) * p.q_stride[2];
-                uint4 w[J];
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    rows[nt][j] = live ? *reinterpret_cast<const uint4 *>(src + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
+            }
+            // the first copies are asked for with those loads on their way (behind all SMs'
+            // first copies they take four times as long)
+            if (it == 0) {
+                lookup();
+#pragma unroll
+                for (int s = 0; s < ST; ++s) {
+                    info[s] = __shfl_sync(0xffffffffu, info_lane, s);
+                    if (s < steps) fetch(s, s, 0u);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint4 (&w)[J] = rows[nt];
                 uint32_t top = 0u;
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    w[j] = live ? *reinterpret_cast<const uint4 *>(src + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
                     const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
@@ -583,8 +597,10 @@ cudaError_t launch_cache4_rows(const CacheAttnProblem &p, cudaStream_t stream) {
 }  // namespace
 
 int64_t cache_attention_int4_workspace(const CacheAttnProblem &p) {
-    const bool one = tile_rows(p) == 8;
-    const int64_t ctas = main_ctas(p, Cfg4<128, 1>::kTokens, one ? Cfg4<128, 1>::kPerSm : Cfg4<128, 2>::kPerSm);
+    const bool one = tile_rows(p) == 8, wide = p.cache.D == 128;
+    const int per_sm = one ? Cfg4<128, 1>::kPerSm : wide ? Cfg4<128, 2>::kPerSm : Cfg4<64, 2>::kPerSm;
+    static_assert(Cfg4<64, 1>::kPerSm == Cfg4<128, 1>::kPerSm && Cfg4<64, 1>::kTokens == Cfg4<128, 1>::kTokens, "");
+    const int64_t ctas = main_ctas(p, Cfg4<128, 1>::kTokens, per_sm);
     return workspace_partials(p.B) + 2 * kWarps * ctas * partial_floats(tile_rows(p), p.cache.D) * 4;
 }
 
