@@ -18,10 +18,11 @@
 // Bound by memory for long prompts (2 D values read, D + D / 16 + 2 bytes written a
 // token and head), before that by the chain of its loads (lengths, page, values, frequencies) and
 // its some 12 instructions a value.  Measured: 8 sequences of up to 2047 tokens (7356 in
-// all), 8 heads of 128, keys rotated: 15.2 us, where the copy rate would take 6.9.
+// all), 8 heads of 128, keys rotated: 11.7 us, where the copy rate would take 5.6.
 // The loads of a head's values are under way while the one before is coded, and the
-// first while the token's place is looked up (18 us without both).  More CTAs an
-// SM by launch bounds spill (6 of them 15.6 us, 8 19.1).
+// first while the token's place is looked up.  Five CTAs an SM where the source is
+// bf16 (left to itself the compiler takes registers for four: 12.7 us); six spill
+// (12.5), as do more than three from float32.
 #include "kv_internal.h"
 #include "kv_values.cuh"
 
@@ -53,6 +54,13 @@ __device__ __forceinline__ float scale_of(uint32_t most) {
 __device__ __forceinline__ float reciprocal_up(float scale) {
     return scale > 0.f ? __uint_as_float(__float_as_uint(__frcp_rn(scale)) + 1u) : 0.f;
 }
+
+// Where a token's table holds (cos, sin) of a pair: two pairs in 16 bytes, those that the
+// threads of a slot read together next to each other, and a token's row 64 bytes
+// longer, so that two tokens' lie in different banks (in the order of pairs the
+// reads met 16 to a bank, 15.1 us for 12.7 at the size above).
+__host__ __device__ constexpr int table_row(int pairs) { return pairs + 8; }
+__device__ __forceinline__ int table_entry(int pair, int pairs) { return (pair % 8 / 2 * (pairs / 8) + pair / 8) * 2 + pair % 2; }
 
 // T: source type; IS_V: values (else keys).  Threads of a CTA: tokens x heads
 // at a time x D / 32.
@@ -118,12 +126,14 @@ __device__ __forceinline__ void append_rows(const AppendProblem &p, int64_t toke
                 sincos_at(turns[i], (int32_t)position, &cs.y, &cs.x);
                 cs.x *= p.attention_scale;
                 cs.y *= p.attention_scale;
-                table[tok * pairs + i] = cs;
+                table[tok * table_row(pairs) + table_entry(i, pairs)] = cs;
             }
         }
         __syncthreads();
     }
-    const float2 *cs = table + tok * pairs;
+    auto turns_of = [&](int pair) {  // of it and the next one
+        return *reinterpret_cast<const float4 *>(table + tok * table_row(pairs) + table_entry(pair, pairs));
+    };
     for (int h = h0; h - slot / tokens < h_last; h += heads) {
         const bool mine = live && h < h_last;
         float x[RUNS][8];
@@ -138,11 +148,13 @@ __device__ __forceinline__ void append_rows(const AppendProblem &p, int64_t toke
                     for (int k = 0; k < 2; ++k) {
                         const int d = 32 * (k * J / RUNS) + R * part + 8 * (k % (RUNS / J));
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 w = cs[d + e];
-                            const float a = x[k][e], z = x[k + 2][e];
+                        for (int e = 0; e < 8; e += 2) {
+                            const float4 w = turns_of(d + e);
+                            const float a = x[k][e], z = x[k + 2][e], b = x[k][e + 1], y = x[k + 2][e + 1];
                             x[k][e] = a * w.x - z * w.y;
                             x[k + 2][e] = z * w.x + a * w.y;
+                            x[k][e + 1] = b * w.z - y * w.w;
+                            x[k + 2][e + 1] = y * w.z + b * w.w;
                         }
                     }
                 } else {
@@ -156,9 +168,10 @@ __device__ __forceinline__ void append_rows(const AppendProblem &p, int64_t toke
                         float z[8];
                         other.unpack(z);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 w = cs[(low ? d : d - pairs) + e];
+                        for (int e = 0; e < 8; e += 2) {
+                            const float4 w = turns_of((low ? d : d - pairs) + e);
                             x[k][e] = x[k][e] * w.x + (low ? -z[e] : z[e]) * w.y;
+                            x[k][e + 1] = x[k][e + 1] * w.z + (low ? -z[e + 1] : z[e + 1]) * w.w;
                         }
                     }
                 }
@@ -168,11 +181,13 @@ __device__ __forceinline__ void append_rows(const AppendProblem &p, int64_t toke
                     const int d = 32 * (k * J / RUNS) + R * part + 8 * (k % (RUNS / J));
                     if (d >= p.rotary) continue;
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float2 w = cs[(d + e) / 2];
-                        const float a = x[k][e], z = x[k][e + 1];
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 w = turns_of((d + e) / 2);
+                        const float a = x[k][e], z = x[k][e + 1], b = x[k][e + 2], y = x[k][e + 3];
                         x[k][e] = a * w.x - z * w.y;
                         x[k][e + 1] = z * w.x + a * w.y;
+                        x[k][e + 2] = b * w.z - y * w.w;
+                        x[k][e + 3] = y * w.z + b * w.w;
                     }
                 }
             }
@@ -235,7 +250,7 @@ __device__ __forceinline__ void append_rows(const AppendProblem &p, int64_t toke
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv_append_int4_kernel(const AppendProblem p, int tokens, int heads_per_cta, int groups) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) kv_append_int4_kernel(const AppendProblem p, int tokens, int heads_per_cta, int groups) {
     extern __shared__ __align__(16) float2 table[];  // [token][pair] (cos, sin)
     __shared__ uint64_t turns[64];
     __shared__ int32_t starts_here[kStartsHere + 1];
@@ -253,7 +268,7 @@ template <typename T, int D>
 cudaError_t launch(const AppendProblem &p, cudaStream_t stream) {
     const int64_t all = p.starts ? p.S : (int64_t)p.B * p.S;
     // a CTA takes a power of two of tokens and walks the heads, two or four at a time,
-    // with their sines and cosines (one at a time: 16 us for 15 at 7356 tokens of 8 heads)
+    // with their sines and cosines (one at a time: 12.5 us for 11.7 at the size above)
     int tokens = kThreads / (D / 32) / 2;
     while (tokens > 1 && (all + tokens - 1) / tokens * 2 < 2 * 152) tokens /= 2;
     int heads = p.cache.H;
@@ -262,7 +277,7 @@ cudaError_t launch(const AppendProblem &p, cudaStream_t stream) {
     while (heads > at_once && tiles * 2 * ((p.cache.H + heads - 1) / heads) < 6 * 152) heads = (heads + 1) / 2;
     const int groups = (p.cache.H + heads - 1) / heads;
     if (tiles > INT32_MAX || 2 * groups > 65535) return cudaErrorInvalidValue;
-    const int smem = p.inv_freq ? tokens * p.rotary * 4 : 0;
+    const int smem = p.inv_freq ? tokens * table_row(p.rotary / 2) * 8 : 0;
     kv_append_int4_kernel<T, D><<<dim3((unsigned)tiles, 2u * groups), kThreads, smem, stream>>>(p, tokens, heads, groups);
     return cudaGetLastError();
 }
