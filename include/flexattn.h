@@ -592,8 +592,8 @@ FLEX_API int flex_kv_cache_read(const flex_kv_cache *cache, const int32_t *page_
  * it, NaN included.  Scales are taken as positive numbers of any value, those
  * of V up to 2^80 apart within a sequence, and values of V up to 2^80 (weights
  * and sums are float32); the append writes powers of two.
- * INT4: scales are zero or positive; a V scale up to 2^100, and those of a row's
- * tokens any distance apart (weights count down to 2^-31 of the row's largest
+ * INT4: scales are zero or positive, up to 2^100; those of V of a row's tokens may be
+ * any distance apart (weights count down to 2^-31 of the row's largest
  * weight times scale, in which scales below 2^-60 count as 2^-60).  scale and
  * scale times a row's largest |q| below 2^110.  Codes are multiplied as fp16 with
  * float32 sums, whose last places are cut off: out is off by up to 2^-16 of 24

@@ -5,6 +5,9 @@ softcap add is off by 2^-22 of its terms; so is lse, plus 2^-19 for exponentials
 (2^-8), the row's sum is not; out is rounded once more (2^-8).
 """
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -250,6 +253,38 @@ def test_streams_graphs_and_repeats():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+FIRST_CALL = """
+import torch
+from block_sparse_masked_blockmask_gb300 import flexattn as fa
+starts = torch.tensor([0, 70, 70, 150], dtype=torch.int32, device="cuda")
+zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+table = torch.arange(30, dtype=torch.int32, device="cuda").view(3, 10)
+q, k, v = (torch.randn((1, 150, h, 64), device="cuda").bfloat16().transpose(1, 2) for h in (6, 2, 2))
+c = fa.flex_kv_cache_create(30, 2, 64, 16, torch.uint8)
+
+def step():
+    fa.flex_kv_cache_append_packed(c, k, v, starts, table, zero)
+    k2, v2 = fa.flex_kv_cache_read(c, table, starts, 150)
+    plan = fa.flex_packed_plan_create(starts, None, 150, None, 6, 2)
+    return fa.flex_attention_packed_fwd(q, k2, v2, plan)
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+want = step()
+assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and want[0].isfinite().all()
+assert fa.flex_device_status() == fa.FLEX_OK
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_tokens_past_32_bits():
