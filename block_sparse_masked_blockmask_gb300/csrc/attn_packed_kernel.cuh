@@ -177,16 +177,6 @@ struct PackedScore {
     }
 };
 
-// TMEM read of 64 columns of this thread's lane, completed before returning.
-__device__ __forceinline__ void tmem_ld64_sync(uint32_t taddr, uint32_t (&r)[64]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(taddr)
-        : "memory");
-}
-
 // The largest magnitude's bits of the two bf16 of each word, and whether one is
 // an infinity or NaN.
 __device__ __forceinline__ uint32_t most_bf16x2(uint32_t most, uint32_t w) { return __vmaxu2(most, w & 0x7FFF7FFFu); }
@@ -657,7 +647,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // ----------------------------------------------------------- softmax
         regs_increase<kRegsSoftmax>();
         const int i = warp / 4;
-        const int t = threadIdx.x % 128;
         const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + C::s_col(i);
         const uint32_t p_addr = tmem + lane_base + C::p_col(i);
@@ -904,38 +893,59 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!ok) record_failure(ms, p.status);
             if (ok) {
                 tc_fence_after_sync();
-                const bool odd = sl.odd != 0;
+                const bool odd = __any_sync(0xffffffffu, sl.odd != 0);
                 const Row row = row_of(sl);
                 const int64_t token = sl.q_row + row.token;
                 uint16_t *dst = p.out + row.h * p.out_stride[0] + token * p.out_stride[1];
                 const bool kept = have && l_run != 0.f;  // NaN stays
                 const float inv = kept ? 1.f / l_run : 0.f;
+                // 32 columns at a time: code that runs once an item is fetched anew each time
+                // (twelve prompts up to 4096: 530 us for 536 with 64).  Whole 32-byte sectors
+                // per store, two lanes next to each other in a row: lanes swap every other
+                // sector with their neighbour (32 rows in one store are as many lines, one
+                // after another; 524 us).
+                const bool second = lane & 1;
+                const unsigned long long mine = reinterpret_cast<unsigned long long>(dst),
+                                         other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                uint16_t *even = reinterpret_cast<uint16_t *>(second ? other : mine) + 16 * second,
+                         *uneven = reinterpret_cast<uint16_t *>(second ? mine : other) + 16 * second;
+                const unsigned lives = __ballot_sync(0xffffffffu, row.live);
+                const bool even_live = lives >> (lane & 30) & 1u, uneven_live = lives >> (lane | 1) & 1u;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 64) {
-                    uint32_t o[64];
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
                     if (have) {
-                        tmem_ld64_sync(o_addr + c0, o);
+                        tmem_ld32_sync(o_addr + c0, o);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) o[j] = 0u;
+                        for (int j = 0; j < 32; ++j) o[j] = 0u;
                     }
+                    uint32_t pk[2][8];
 #pragma unroll
-                    for (int c = 0; c < 64; c += 16) {
-                        uint32_t pk[8];
+                    for (int j = 0; j < 16; ++j) {
+                        pk[j / 8][j % 8] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        if (!kept) pk[j / 8][j % 8] = 0u;
+                    }
+                    if (p.wide_out) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            pk[j] = pack_bf16x2(__uint_as_float(o[c + 2 * j]) * inv, __uint_as_float(o[c + 2 * j + 1]) * inv);
-                            if (!kept) pk[j] = 0u;
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? pk[0][j] : pk[1][j], 1);
+                            if (second)
+                                pk[0][j] = got;
+                            else
+                                pk[1][j] = got;
                         }
-                        if (!row.live) continue;
-                        if (p.wide_out) {  // whole 32-byte sectors per store
-                            st_global_32B(dst + c0 + c, pk);
-                        } else {
-                            *reinterpret_cast<uint4 *>(dst + c0 + c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                            *reinterpret_cast<uint4 *>(dst + c0 + c + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-                        }
+                        if (even_live) st_global_32B(even + c0, pk[0]);
+                        if (uneven_live) st_global_32B(uneven + c0, pk[1]);
+                    } else if (row.live) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4 *>(dst + c0 + 8 * j) =
+                                make_uint4(pk[j / 2][j % 2 * 4], pk[j / 2][j % 2 * 4 + 1], pk[j / 2][j % 2 * 4 + 2],
+                                           pk[j / 2][j % 2 * 4 + 3]);
                     }
                 }
+                if (odd) __syncwarp();  // the row may be its neighbour's stores
                 if (row.live) p.lse[(int64_t)row.h * p.total_q + token] = kept ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
                 if (odd && row.live) {
                     // the values that were zeroed, of the columns that this row keeps, on top of what was stored
