@@ -653,18 +653,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t o_addr = tmem + lane_base + C::o_col(i);
         // This thread's row of an item.  Worked out from the thread's index where it is
         // needed (volatile, so that no register keeps it): the loop over full tiles
-        // has none to spare.
+        // has none to spare, the one of few columns has.
+        const int row_in = SHORT ? (int)(threadIdx.x % 128) / p.G : 0, row_head = SHORT ? (int)(threadIdx.x % 128) % p.G : 0;
         struct Row {
             int token, h, pos;
             bool live;
         };
         auto row_of = [&](const PackedItem &sl) {
-            uint32_t tid;
-            asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
-            const int r = (int)(tid % 128u), in = r / p.G;
+            int in = row_in, head = row_head;
+            if constexpr (!SHORT) {
+                uint32_t tid;
+                asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+                const int r = (int)(tid % 128u);
+                in = r / p.G;
+                head = r % p.G;
+            }
             Row row;
             row.token = i * p.tokens + in;
-            row.h = sl.hk * p.G + r % p.G;
+            row.h = sl.hk * p.G + head;
             row.pos = sl.pos + row.token;
             row.live = in < p.tokens && row.token < sl.q_tokens;
             return row;
