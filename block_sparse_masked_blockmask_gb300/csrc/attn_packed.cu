@@ -15,9 +15,11 @@ namespace flex {
 namespace {
 
 // Keys of a sequence or window, on average, up to which the kernels for items of few
-// kv tiles are taken: 64 causal sequences up to 96 tokens, 32 query heads over 8: 27.0
-// us with them and 32.9 without; twelve up to 4096: 766 us with and 537 without.
-constexpr int64_t kFewKeys = 256;
+// kv tiles are taken.  Causal, 32 query heads over 8, D 128, with them and without: 64
+// sequences up to 96 tokens 24.7 and 31.7 us, 32 of 256 46.9 and 53.2, 16 of 384 45.8
+// and 50.0, 16 of 512 66.8 and 66.1 (D 64, 32 of 512: 106 and 92), twelve up to
+// 4096 733 and 526.
+constexpr int64_t kFewKeys = 384;
 constexpr int kPlanThreads = 1024;
 constexpr int kLengths = 1024;  // lengths told apart, in kv tiles (longer ones count as the longest)
 

@@ -26,14 +26,14 @@
 //  * Items of few kv tiles have kernels of their own (SHORT): such an item is mostly
 //    masked steps, and their softmax takes 32 columns at a time, those that a warp's
 //    rows keep nothing of left out, where the loop for whole tiles has a thread's
-//    128 scores in registers.  (In one kernel the registers that the short form
-//    takes cost the long one 30%.)  Which one: attn_packed.cu.
+//    128 scores in registers.  (In one kernel the loop for whole tiles lost
+//    registers to the other and was slower.)  Which one: attn_packed.cu.
 //  * lse to float32's accuracy: the row sum takes the weights before their
 //    rounding to bf16, softcap is not the hardware's tanh, and ALiBi's distances
 //    are whole numbers until they meet the slope.
-// Measured, causal, D 128: a sequence of 16384 tokens, 32 query heads over 8, 1602 us or
-// 1373 TFLOP/s of kept pairs (the kernel of as many key heads as query heads: 1434);
-// twelve of all lengths up to 4096, 537 us, 59% of the tensor peak: short sequences pay for
+// Measured, causal, D 128: a sequence of 16384 tokens, 32 query heads over 8, 1595 us or
+// 1379 TFLOP/s of kept pairs (the kernel of as many key heads as query heads: 1434);
+// twelve of all lengths up to 4096, 522 us, 61% of the tensor peak: short sequences pay for
 // their masked tiles and for an item's first and last step.
 #pragma once
 
